@@ -76,8 +76,14 @@ enum {
   DG_OP_MASKED = 2,
   DG_OP_BF16_GEMM_NT = 3,
   DG_OP_GEMM_NT_UE8M0 = 4,
-  DG_OP_K_GROUPED = 5 /* dg_k_grouped_fp8_gemm_nt_contiguous (plan description only) */
+  DG_OP_K_GROUPED = 5, /* dg_k_grouped_fp8_gemm_nt_contiguous (plan description only) */
+  DG_OP_MXFP4_GEMM_NT = 6,
+  DG_OP_MOE_GATE = 7,  /* workspace only: rows = T, N = E */
+  DG_OP_MOE_LAYOUT = 8 /* workspace only: rows = T, K = k */
 };
+
+/* Element types of the operators that take more than one. */
+enum { DG_F32 = 0, DG_BF16 = 1 };
 
 /*
  * Dense GEMM.  Lesson 13, Fig. 13-1; DeepGEMM's "normal" GEMM (the Feb-2025
@@ -293,6 +299,135 @@ int dg_m_grouped_fp8_gemm_nt_masked_ue8m0(const uint8_t* A, const int32_t* sfa, 
                                           const int32_t* sfb, uint16_t* D, const int32_t* masked_m,
                                           int64_t G, int64_t max_m, int64_t N, int64_t K, int64_t expected_m,
                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Microscaled 4-bit floating point: e2m1 elements (magnitudes 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6; sign in bit 3), two to a byte along K (the even element in the
+ * lower nibble), with one power-of-two scale per 32 elements of a row, code c
+ * meaning 2^(c - 127) and 255 meaning NaN.  The codes of the four blocks of 128
+ * elements share one int32 (block 4 w + j in byte j), words MN-major:
+ * [K/128][rows].  K is a positive multiple of 128.
+ *
+ * dg_quant_mxfp4: rows of x (dtype DG_F32 or DG_BF16) to codes and scales.
+ *   x  [G,R,K] (row_token null), or [T,K] gathered by token: row r of group g
+ *      takes row row_token[g][r] of x; rows whose entry is outside [0, T) are
+ *      not written
+ *   q  [G,R,K/2] (written)      sf [G][K/128][R] int32 (written)
+ * c is the least code with 6 * 2^(c - 127) >= amax of the block, clamped to
+ * [0, 253]; a block of zeros gets 127; a block that holds a NaN or an infinity
+ * gets 255 and zero elements.  Elements are x * 2^(127 - c), an exact scaling,
+ * rounded to nearest, ties to the even mantissa, the sign of zero kept.
+ * Bit-exact and deterministic.  T is ignored when row_token is null.
+ * Limits: G <= 65535, R < 2^31, ceil(R / 16) * (K / 128) < 2^31; x, q 16-byte
+ * aligned, sf and row_token 4-byte aligned.
+ *
+ * dg_dequant_mxfp4: the values back, y [G,R,K] of `dtype` (exact in both, past
+ * their range infinite; a block of code 255 gives NaN).
+ */
+int dg_quant_mxfp4(const void* x, int dtype, uint8_t* q, int32_t* sf, const int32_t* row_token, int64_t G,
+                   int64_t T, int64_t R, int64_t K, void* stream);
+int dg_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, int dtype, int64_t G, int64_t R, int64_t K,
+                     void* stream);
+
+/*
+ * Products of microscaled 4-bit operands, D = A . B^T in bf16: dense,
+ * M-grouped contiguous and M-grouped masked, with the operands, index arrays,
+ * undefined rows and rules of the FP8 forms of the same names, except
+ *   A [rows,K/2], B [(G,)N,K/2] packed e2m1
+ *   sfa [K/128][rows] int32, sfb [(G)][K/128][N] int32 (masked sfa
+ *   [G][K/128][max_m]): both operands scaled per row and 32 elements
+ * The matrix cores apply the scales; sums are fp32, rounded once to bf16.
+ * A row or column with a NaN code (255) gives NaN.  K is a positive multiple
+ * of 128 up to 2^24, N of 16; no other limit on sizes (operands past 4 GiB are
+ * addressed in 64 bits).  Deterministic.
+ * workspace (dense only): as for dg_fp8_gemm_nt: optional, zero-filled before
+ * its first use and left reusable, full size
+ * dg_get_workspace_size(DG_OP_MXFP4_GEMM_NT, M, N, K, 1).
+ */
+int dg_mxfp4_gemm_nt(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb, uint16_t* D,
+                     int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+int dg_m_grouped_mxfp4_gemm_nt_contiguous(const uint8_t* A, const int32_t* sfa, const uint8_t* B,
+                                          const int32_t* sfb, uint16_t* D, const int32_t* m_indices,
+                                          int64_t M_total, int64_t N, int64_t K, int64_t G, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb,
+                                      uint16_t* D, const int32_t* masked_m, int64_t G, int64_t max_m, int64_t N,
+                                      int64_t K, int64_t expected_m, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Router: the k experts of each token, their weights, the experts' loads and
+ * the balance loss.
+ *   logits   [T,E] of `dtype` (DG_F32 or DG_BF16), E in [1, 1024], k in [1, min(E, 16)]
+ *   valid    [T] bytes or NULL: tokens with 0 (padding) are not read
+ *   topk_idx [T,k] int32 (written): experts of the k largest logits, largest
+ *            first, of equal ones the lower expert first; -inf and NaN are
+ *            never chosen; -1 where nothing is left to choose
+ *   topk_w   [T,k] fp32 (written): with p = softmax(logits of the row),
+ *            w_scale * p_j / (sum of the chosen p) if renorm, else w_scale * p_j;
+ *            0 where topk_idx is -1
+ *   counts   [E+1] int32 (written): choices c_e of each expert, then the number n
+ *            of tokens with a choice
+ *   prob_sum [E] fp32 (written): P_e = sum of p_te over the tokens
+ *   loss     [1] fp32 (written): loss_coef * E / (C n) * sum_e c_e P_e, C = sum_e c_e
+ *            (0 when nothing is routed)
+ * A masked token, or one whose logits are all -inf, has no expert and enters
+ * no sum.  A row with a NaN or +inf has NaN probabilities: its weights, prob_sum
+ * and the loss are NaN, its experts are still distinct and in range.
+ * workspace: required, dg_get_workspace_size(DG_OP_MOE_GATE, T, E, k, 1) bytes,
+ * zero-filled before its first use and left reusable.  Deterministic.
+ *
+ * dg_moe_gate_bwd: dlogits [T,E] (of `dtype`, written) = gradient of
+ * sum(dw * topk_w) + dloss * loss, the counts being constants.  topk_idx,
+ * topk_w, counts are dg_moe_gate's; dw [T,k] fp32 or NULL (zeros); dloss [1]
+ * fp32 on the device or NULL (zero).  Rows without an expert get zeros.
+ */
+int dg_moe_gate(const void* logits, int dtype, const uint8_t* valid, int32_t* topk_idx, float* topk_w,
+                int32_t* counts, float* prob_sum, float* loss, int64_t T, int64_t E, int64_t k, int renorm,
+                float w_scale, float loss_coef, void* workspace, size_t workspace_bytes, void* stream);
+int dg_moe_gate_bwd(const void* logits, int dtype, const int32_t* topk_idx, const float* topk_w,
+                    const int32_t* counts, const float* dw, const float* dloss, void* dlogits, int64_t T,
+                    int64_t E, int64_t k, int renorm, float w_scale, float loss_coef, void* stream);
+
+/*
+ * Row order of the grouped products from the chosen experts.  topk_idx [T,k]
+ * holds experts; expert first_expert + g is group g of [0, G) here, other
+ * entries (another GPU's experts, -1) are skipped.  A group's choices take its
+ * rows in (token, choice) order.
+ *   contiguous: group g's rows start at a multiple of 128, groups in order.
+ *     counts    [G] int32 (written)
+ *     m_indices [M_total] int32 (written): group of each row, -1 on padding
+ *     row_token [M_total] int32 (written): token of each row, -1 on padding
+ *     row_of    [T,k] int32 (written): row of each choice, -1 if it has none
+ *     M_total = T k + 127 G rounded up to 128 always suffices; choices past
+ *     M_total get no row.
+ *   masked: group g's rows are [g max_m, g max_m + masked_m[g]); choices past
+ *     max_m get no row.
+ *     masked_m [G] int32 (written), row_token [G,max_m], row_of [T,k] as above.
+ * k in [1, 16], G in [1, 1024], T k + 128 G < 2^31.  workspace: required,
+ * dg_get_workspace_size(DG_OP_MOE_LAYOUT, T, 0, k, G) bytes, zero-filled before
+ * its first use and left reusable.  Deterministic.
+ */
+int dg_moe_layout_contiguous(const int32_t* topk_idx, int32_t* counts, int32_t* m_indices, int32_t* row_token,
+                             int32_t* row_of, int64_t T, int64_t k, int64_t first_expert, int64_t G,
+                             int64_t M_total, void* workspace, size_t workspace_bytes, void* stream);
+int dg_moe_layout_masked(const int32_t* topk_idx, int32_t* masked_m, int32_t* row_token, int32_t* row_of,
+                         int64_t T, int64_t k, int64_t first_expert, int64_t G, int64_t max_m, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Expert rows back to tokens: y[t] = sum_j w[t,j] rows[row_of[t,j]] over the
+ * choices with a row in [0, R), summed in fp32 in the order of the choices.
+ *   rows [R,N] bf16   row_of [T,k] int32   w [T,k] fp32   y [T,N] of `dtype` (written)
+ * dg_moe_combine_bwd: drows [R,N] bf16: drows[row_of[t,j]] = w[t,j] dy[t] (rows
+ * of no choice are not written; a row belongs to one choice at most), and
+ * dw [T,k] fp32 (written): the dot product of rows[row_of[t,j]] and dy[t], 0
+ * without a row.  dy [T,N] of `dtype`.  N is a multiple of 16.  Deterministic.
+ */
+int dg_moe_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, int dtype, int64_t T,
+                   int64_t k, int64_t N, int64_t R, void* stream);
+int dg_moe_combine_bwd(const void* dy, int dtype, const uint16_t* rows, const int32_t* row_of, const float* w,
+                       uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R, void* stream);
 
 /* Workspace bytes that let `op` use its full K split for this shape with the
  * current CU cap (0 = none used); a call split into row chunks reuses it for

@@ -21,7 +21,8 @@ LIB_NAME = "libdg_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "api.cpp"]
+SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip",
+           "moe_gate.hip", "moe_layout.hip", "moe_combine.hip", "api.cpp", "api_moe.cpp"]
 # per-source flags: the persistent kernels need the iterative ILP scheduler to
 # stay within 256 VGPRs (two waves per SIMD) without spilling
 SOURCE_FLAGS = {"gemm_persist.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
@@ -59,7 +60,7 @@ def build(verbose=False, out_path=None, extra_flags=()):
     lib_path = out_path or LIB_PATH
     build_dir = BUILD if out_path is None else os.path.join(os.path.dirname(out_path), "_build")
     os.makedirs(build_dir, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         results = list(ex.map(lambda s: _compile(s, build_dir, list(extra_flags)), SOURCES))
     report = []
     for (obj, log), src in zip(results, SOURCES):

@@ -38,6 +38,7 @@
 
 #include "dg.h"
 #include "dg_internal.hpp"
+#include "host.hpp"
 
 namespace {
 
@@ -49,12 +50,11 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_dev_kind[kMaxDevices];
 std::atomic<int> g_dev_cus[kMaxDevices];
 
-// Byte offsets a kernel may use inside one buffer range: below the
-// out-of-range marker (0xFFFFFF00) the kernels give lanes outside a tile.
-constexpr int64_t kOffLim = (int64_t)0xFFFFFF00 - 4096;
-constexpr int64_t kMaxGroups = 1024;
+}  // namespace
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+// host helpers declared in host.hpp
+namespace dg {
+
 int fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -69,8 +69,6 @@ int ok() {
   g_last_error.clear();
   return DG_OK;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Checks that a HIP device is current and is gfx950; returns its CU count (>0) or fails.
 int check_device(int* cus) {
@@ -119,7 +117,13 @@ int effective_cus(int device_cus) {
   return (cap > 0 && cap < device_cus) ? cap : device_cus;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool print_configs() { return std::getenv("DG_PRINT_CONFIGS") != nullptr; }
+
+}  // namespace dg
+
+namespace {
+
+using namespace dg;
 
 // ---- DG_FORCE_CONFIG
 enum ForceKernel { kForceNone = 0, kForceWide = 1, kForcePersistent = 2 };
@@ -155,8 +159,6 @@ Force forced() {
   }
   return f;
 }
-bool print_configs() { return std::getenv("DG_PRINT_CONFIGS") != nullptr; }
-
 // Rows per launch (a multiple of 256): A rows of row_bytes each (plus one
 // tile of overhang) and output rows of out_bytes each stay inside 32-bit
 // offsets; 0 when not even 256 rows fit.
@@ -988,7 +990,7 @@ int dg_quant_128x128_ue8m0(const float* x, uint8_t* q, int32_t* sfb, int64_t G, 
 }
 
 size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t G) {
-  (void)G;
+  if (op >= DG_OP_MXFP4_GEMM_NT) return moe_workspace_size(op, rows, N, K, G, effective_cus(query_cus()));
   if (op != DG_OP_GEMM_NT && op != DG_OP_BF16_GEMM_NT && op != DG_OP_GEMM_NT_UE8M0) return 0;
   if (rows <= 0 || N <= 0 || K <= 0 || K % (op == DG_OP_BF16_GEMM_NT ? 64 : 128)) return 0;
   const int ecus = effective_cus(query_cus());
@@ -1015,6 +1017,11 @@ size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t
 const char* dg_describe_plan(int op, int64_t rows, int64_t N, int64_t K, int64_t G) {
   thread_local std::string text;
   text.clear();
+  if (op >= DG_OP_MXFP4_GEMM_NT) {
+    char plan[320];
+    if (moe_describe_plan(op, rows, N, K, G, effective_cus(query_cus()), plan, sizeof(plan))) text = plan;
+    return text.c_str();
+  }
   if ((op != DG_OP_GEMM_NT && op != DG_OP_CONTIGUOUS && op != DG_OP_GEMM_NT_UE8M0 && op != DG_OP_BF16_GEMM_NT &&
        op != DG_OP_K_GROUPED && op != DG_OP_MASKED) ||
       rows <= 0 || N <= 0 || K <= 0 || K % (op == DG_OP_BF16_GEMM_NT ? 64 : 128) || N % 16)

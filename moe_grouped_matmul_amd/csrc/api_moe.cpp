@@ -1,0 +1,366 @@
+// C ABI of the mixture-of-experts operators and the microscaled 4-bit
+// products: argument validation, plans and launches on the caller's stream.
+// As in api.cpp, no call allocates, synchronises or reads device data on the
+// host, and no call throws.
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+
+#include "dg.h"
+#include "host.hpp"
+#include "moe_internal.hpp"
+
+namespace {
+
+using namespace dg;
+
+constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxExperts = 1024;
+constexpr int64_t kMaxTopK = 16;
+
+hipStream_t hs(void* stream) { return static_cast<hipStream_t>(stream); }
+
+int launched(hipError_t e) {
+  return e == hipSuccess ? ok() : fail(DG_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
+}
+
+int check_dtype(int dtype) {
+  if (dtype != DG_F32 && dtype != DG_BF16) return fail(DG_ERR_INVALID_ARG, "dtype must be DG_F32 or DG_BF16 (got %d)", dtype);
+  return DG_OK;
+}
+
+// ---- microscaled 4-bit products
+
+struct MxPlan {
+  int tile = kMx64x64;
+  int m_tiles = 0;
+  int n_tiles = 0;
+  int splits = 1;
+  int steps_per_split = 0;
+};
+
+// Dense: 256 x 256 tiles where they fill most of the CUs, else 128 x 256 ones, else 64 x 64 tiles with K
+// split until two workgroups per CU have work.
+MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) {
+  MxPlan pl;
+  const int64_t steps = ceil_div(K, 256);
+  const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256);
+  const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 256);
+  if (M > 128 && t256 * 10 >= (int64_t)cus * 6) pl.tile = kMx256x256;
+  else if (M > 64 && t128 * 10 >= (int64_t)cus * 6) pl.tile = kMx128x256;
+  else pl.tile = kMx64x64;
+  pl.m_tiles = (int)ceil_div(M, mx_bm(pl.tile));
+  pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
+  int64_t s = 1;
+  if (pl.tile == kMx64x64) {
+    const int64_t tiles = (int64_t)pl.m_tiles * pl.n_tiles;
+    s = std::min({2 * cus / std::max<int64_t>(tiles, 1), steps / 4, (int64_t)16});
+    if (s < 1 || tiles > kMxMaxCounters) s = 1;
+    while (s > 1 && mx_workspace_bytes(pl.tile, pl.m_tiles, pl.n_tiles, (int)s) > ws_bytes) --s;
+  }
+  pl.steps_per_split = (int)ceil_div(steps, s);
+  pl.splits = (int)ceil_div(steps, pl.steps_per_split);  // every split non-empty
+  return pl;
+}
+
+int check_mx_shape(int64_t N, int64_t K) {
+  if (K <= 0 || K % 128 != 0) return fail(DG_ERR_SHAPE, "K must be a positive multiple of 128 (got %lld)", (long long)K);
+  if (N <= 0 || N % 16 != 0) return fail(DG_ERR_SHAPE, "N must be a positive multiple of 16 (got %lld)", (long long)N);
+  // a tile's rows (256 of K / 2 bytes) are addressed with 32-bit offsets
+  if (K > (int64_t)1 << 24 || N > (int64_t)1 << 30) return fail(DG_ERR_SHAPE, "N or K too large");
+  return DG_OK;
+}
+
+int check_mx_operands(const void* A, const void* sfa, const void* B, const void* sfb, const void* D) {
+  if (!A || !sfa || !B || !sfb || !D) return fail(DG_ERR_INVALID_ARG, "null operand pointer");
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, 16))
+    return fail(DG_ERR_ALIGN, "A, B and D must be 16-byte aligned");
+  if (!aligned(sfa, 4) || !aligned(sfb, 4)) return fail(DG_ERR_ALIGN, "scale arrays must be 4-byte aligned");
+  return DG_OK;
+}
+
+int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb, uint16_t* D,
+           const int32_t* index, int64_t rows, int64_t N, int64_t K, int64_t G, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_mx_shape(N, K);
+  if (rc) return rc;
+  if (G < 1 || G > kMaxGroups) return fail(DG_ERR_SHAPE, "G must be in [1, 1024] (got %lld)", (long long)G);
+  if (rows < 0) return fail(DG_ERR_SHAPE, "row counts must be >= 0");
+  if (rows > kIntMax) return fail(DG_ERR_SHAPE, "too many rows (%lld)", (long long)rows);
+  if (rows == 0) return ok();
+  if ((rc = check_mx_operands(A, sfa, B, sfb, D))) return rc;
+  if (form != kMxDense && !index) return fail(DG_ERR_INVALID_ARG, form == kMxMasked ? "null masked_m" : "null m_indices");
+  if (form != kMxDense && !aligned(index, 4)) return fail(DG_ERR_ALIGN, "index arrays must be 4-byte aligned");
+  if (ws && (!aligned(ws, 16) || ws_bytes % 4))
+    return fail(DG_ERR_WORKSPACE, "workspace must be 16-byte aligned with a size that is a multiple of 4");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  cus = effective_cus(cus);
+  MxPlan pl;
+  if (form == kMxDense) {
+    pl = plan_mx_dense(rows, N, K, cus, ws ? ws_bytes : 0);
+  } else {
+    pl.tile = form == kMxMasked && rows <= 256 ? kMx64x64 : kMx128x256;
+    pl.m_tiles = (int)ceil_div(rows, mx_bm(pl.tile));
+    pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
+    pl.steps_per_split = (int)ceil_div(K, 256);
+  }
+  const int64_t units = (int64_t)pl.n_tiles * (form == kMxMasked ? G : pl.splits);
+  if ((ceil_div(units, 8) * 8) * pl.m_tiles > kIntMax) return fail(DG_ERR_SHAPE, "too many tiles");
+  MxGemmParams p{};
+  p.A = A;
+  p.sfa = sfa;
+  p.B = B;
+  p.sfb = sfb;
+  p.D = D;
+  p.ws = ws;
+  p.index = index;
+  p.rows = rows;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.G = (int)G;
+  p.m_tiles = pl.m_tiles;
+  p.n_tiles = pl.n_tiles;
+  p.splits = pl.splits;
+  p.steps_per_split = pl.steps_per_split;
+  if (print_configs())
+    std::fprintf(stderr, "[dg] mxfp4%s rows=%lld N=%lld K=%lld G=%lld tile=%dx%d tiles=%lld splits=%d\n",
+                 form == kMxDense ? "" : form == kMxMasked ? "_masked" : "_contiguous", (long long)rows, (long long)N,
+                 (long long)K, (long long)G, mx_bm(pl.tile), mx_bn(pl.tile), (long long)pl.m_tiles * pl.n_tiles, pl.splits);
+  return launched(launch_mxfp4_gemm(form, pl.tile, p, hs(stream)));
+}
+
+int check_quant(int dtype, int64_t G, int64_t R, int64_t K) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (K <= 0 || K % 128) return fail(DG_ERR_SHAPE, "K must be a positive multiple of 128 (got %lld)", (long long)K);
+  if (G < 0 || R < 0) return fail(DG_ERR_SHAPE, "G and row counts must be >= 0");
+  if (K > kIntMax || R > kIntMax || G > 65535 || ceil_div(R, 16) * (K / 128) > kIntMax)
+    return fail(DG_ERR_SHAPE, "problem too large");
+  return DG_OK;
+}
+
+int check_topk(int64_t T, int64_t k) {
+  if (T < 0) return fail(DG_ERR_SHAPE, "T must be >= 0");
+  if (k < 1 || k > kMaxTopK) return fail(DG_ERR_SHAPE, "k must be in [1, 16] (got %lld)", (long long)k);
+  if (T * k > kIntMax) return fail(DG_ERR_SHAPE, "T * k too large");
+  return DG_OK;
+}
+
+int check_gate(int dtype, int64_t T, int64_t E, int64_t k, float w_scale) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (T > kIntMax) return fail(DG_ERR_SHAPE, "T too large");
+  if ((rc = check_topk(T, k))) return rc;
+  if (E < 1 || E > kMaxExperts) return fail(DG_ERR_SHAPE, "E must be in [1, 1024] (got %lld)", (long long)E);
+  if (k > E) return fail(DG_ERR_SHAPE, "k must be at most E (got %lld of %lld)", (long long)k, (long long)E);
+  if (!(std::fabs(w_scale) > 0.f) || std::isinf(w_scale)) return fail(DG_ERR_INVALID_ARG, "w_scale must be finite and not 0");
+  return DG_OK;
+}
+
+int run_layout(const int32_t* topk_idx, int32_t* counts, int32_t* m_indices, int32_t* row_token, int32_t* row_of, int64_t T,
+               int64_t k, int64_t first_expert, int64_t G, int64_t max_m, int64_t rows, void* ws, size_t ws_bytes,
+               void* stream) {
+  if (T > kIntMax) return fail(DG_ERR_SHAPE, "T too large");
+  int rc = check_topk(T, k);
+  if (rc) return rc;
+  if (G < 1 || G > kMaxGroups) return fail(DG_ERR_SHAPE, "G must be in [1, 1024] (got %lld)", (long long)G);
+  if (first_expert < 0 || first_expert > kIntMax - G) return fail(DG_ERR_SHAPE, "first_expert out of range");
+  if (rows < 0 || rows > kIntMax || T * k + 128 * G > kIntMax) return fail(DG_ERR_SHAPE, "row numbers must fit 32 bits");
+  const bool masked = max_m > 0;
+  if (!counts || (rows > 0 && (!row_token || (!masked && !m_indices))) || (T > 0 && (!topk_idx || !row_of)))
+    return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(topk_idx, 4) || !aligned(counts, 4) || !aligned(row_token, 4) || !aligned(row_of, 4) || !aligned(m_indices, 4))
+    return fail(DG_ERR_ALIGN, "index arrays must be 4-byte aligned");
+  const size_t need = layout_workspace_bytes(T * k, G);
+  if (!ws || !aligned(ws, 16) || ws_bytes < need)
+    return fail(DG_ERR_WORKSPACE, "a 16-byte aligned workspace of at least %zu bytes is needed", need);
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  LayoutParams p{};
+  p.idx = topk_idx;
+  p.counts = counts;
+  p.m_indices = masked ? nullptr : m_indices;
+  p.row_token = row_token;
+  p.row_of = row_of;
+  p.ws = ws;
+  p.n = T * k;
+  p.k = (int)k;
+  p.first = (int)first_expert;
+  p.G = (int)G;
+  p.max_m = max_m;
+  p.rows = rows;
+  return launched(launch_layout(p, hs(stream)));
+}
+
+int check_combine(int dtype, int64_t T, int64_t k, int64_t N, int64_t R) {
+  int rc = check_dtype(dtype);
+  if (rc) return rc;
+  if (T > kIntMax) return fail(DG_ERR_SHAPE, "T too large");
+  if ((rc = check_topk(T, k))) return rc;
+  if (N <= 0 || N % 16) return fail(DG_ERR_SHAPE, "N must be a positive multiple of 16 (got %lld)", (long long)N);
+  if (N > (int64_t)1 << 30 || R < 0 || R > kIntMax) return fail(DG_ERR_SHAPE, "N or row count out of range");
+  return DG_OK;
+}
+
+}  // namespace
+
+namespace dg {
+
+size_t moe_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
+  size_t need = 0;
+  if (op == DG_OP_MXFP4_GEMM_NT) {
+    if (rows <= 0 || rows > kIntMax || N <= 0 || N > (int64_t)1 << 30 || K <= 0 || K % 128) return 0;
+    const MxPlan pl = plan_mx_dense(rows, N, K, cus, (size_t)-1);
+    need = mx_workspace_bytes(pl.tile, pl.m_tiles, pl.n_tiles, pl.splits);
+  } else if (op == DG_OP_MOE_GATE) {
+    if (rows < 0 || rows > kIntMax || N < 1 || N > kMaxExperts) return 0;
+    need = gate_workspace_bytes(rows, N);
+  } else if (op == DG_OP_MOE_LAYOUT) {
+    if (rows < 0 || rows > kIntMax || K < 1 || K > kMaxTopK || G < 1 || G > kMaxGroups) return 0;
+    need = layout_workspace_bytes(rows * K, G);
+  }
+  return (need + 15) / 16 * 16;
+}
+
+int moe_describe_plan(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus, char* buf, size_t n) {
+  if (op != DG_OP_MXFP4_GEMM_NT || rows <= 0 || rows > kIntMax || N <= 0 || N % 16 || N > (int64_t)1 << 30 || K <= 0 || K % 128 ||
+      K > (int64_t)1 << 24)
+    return 0;
+  (void)G;
+  const MxPlan pl = plan_mx_dense(rows, N, K, cus, (size_t)-1);
+  std::snprintf(buf, n, "kernel=mxfp4 tile=%dx%d tiles=%lld splits=%d", mx_bm(pl.tile), mx_bn(pl.tile),
+                (long long)pl.m_tiles * pl.n_tiles, pl.splits);
+  return 1;
+}
+
+}  // namespace dg
+
+extern "C" {
+
+int dg_quant_mxfp4(const void* x, int dtype, uint8_t* q, int32_t* sf, const int32_t* row_token, int64_t G, int64_t T,
+                   int64_t R, int64_t K, void* stream) {
+  int rc = check_quant(dtype, G, R, K);
+  if (rc) return rc;
+  if (T < 0 || T > kIntMax) return fail(DG_ERR_SHAPE, "T out of range");
+  if (G == 0 || R == 0) return ok();
+  if (!q || !sf || (!x && (T > 0 || !row_token))) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(q, 16)) return fail(DG_ERR_ALIGN, "x and q must be 16-byte aligned");
+  if (!aligned(sf, 4) || !aligned(row_token, 4)) return fail(DG_ERR_ALIGN, "sf and row_token must be 4-byte aligned");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  return launched(launch_quant_mxfp4(x, dtype == DG_BF16, q, sf, row_token, G, T, R, K, hs(stream)));
+}
+
+int dg_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, int dtype, int64_t G, int64_t R, int64_t K, void* stream) {
+  int rc = check_quant(dtype, G, R, K);
+  if (rc) return rc;
+  if (G == 0 || R == 0) return ok();
+  if (!q || !sf || !y) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(y, 16) || !aligned(q, 16)) return fail(DG_ERR_ALIGN, "q and y must be 16-byte aligned");
+  if (!aligned(sf, 4)) return fail(DG_ERR_ALIGN, "sf must be 4-byte aligned");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  return launched(launch_dequant_mxfp4(q, sf, y, dtype == DG_BF16, G, R, K, hs(stream)));
+}
+
+int dg_mxfp4_gemm_nt(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb, uint16_t* D, int64_t M,
+                     int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_mx(kMxDense, A, sfa, B, sfb, D, nullptr, M, N, K, 1, workspace, workspace_bytes, stream);
+}
+
+int dg_m_grouped_mxfp4_gemm_nt_contiguous(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb,
+                                          uint16_t* D, const int32_t* m_indices, int64_t M_total, int64_t N, int64_t K,
+                                          int64_t G, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return run_mx(kMxContiguous, A, sfa, B, sfb, D, m_indices, M_total, N, K, G, nullptr, 0, stream);
+}
+
+int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb, uint16_t* D,
+                                      const int32_t* masked_m, int64_t G, int64_t max_m, int64_t N, int64_t K,
+                                      int64_t expected_m, void* workspace, size_t workspace_bytes, void* stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  (void)expected_m;
+  return run_mx(kMxMasked, A, sfa, B, sfb, D, masked_m, max_m, N, K, G, nullptr, 0, stream);
+}
+
+int dg_moe_gate(const void* logits, int dtype, const uint8_t* valid, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                float* prob_sum, float* loss, int64_t T, int64_t E, int64_t k, int renorm, float w_scale, float loss_coef,
+                void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_gate(dtype, T, E, k, w_scale);
+  if (rc) return rc;
+  if (!counts || !prob_sum || !loss || (T > 0 && (!logits || !topk_idx || !topk_w)))
+    return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(logits, 16)) return fail(DG_ERR_ALIGN, "logits must be 16-byte aligned");
+  if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(counts, 4) || !aligned(prob_sum, 4) || !aligned(loss, 4))
+    return fail(DG_ERR_ALIGN, "outputs must be 4-byte aligned");
+  const size_t need = gate_workspace_bytes(T, E);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+    return fail(DG_ERR_WORKSPACE, "a 16-byte aligned workspace of at least %zu bytes is needed", need);
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  GateParams p{logits, valid, topk_idx, topk_w, counts, prob_sum, loss, workspace, T, (int)E, (int)k, renorm, w_scale, loss_coef};
+  return launched(launch_gate(p, dtype == DG_BF16, hs(stream)));
+}
+
+int dg_moe_gate_bwd(const void* logits, int dtype, const int32_t* topk_idx, const float* topk_w, const int32_t* counts,
+                    const float* dw, const float* dloss, void* dlogits, int64_t T, int64_t E, int64_t k, int renorm,
+                    float w_scale, float loss_coef, void* stream) {
+  int rc = check_gate(dtype, T, E, k, w_scale);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!logits || !topk_idx || !topk_w || !counts || !dlogits) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(logits, 16) || !aligned(dlogits, 16)) return fail(DG_ERR_ALIGN, "logits and dlogits must be 16-byte aligned");
+  if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(counts, 4) || !aligned(dw, 4) || !aligned(dloss, 4))
+    return fail(DG_ERR_ALIGN, "index and gradient arrays must be 4-byte aligned");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  GateBwdParams p{logits, topk_idx, topk_w, counts, dw, dloss, dlogits, T, (int)E, (int)k, renorm, w_scale, loss_coef};
+  return launched(launch_gate_bwd(p, dtype == DG_BF16, hs(stream)));
+}
+
+int dg_moe_layout_contiguous(const int32_t* topk_idx, int32_t* counts, int32_t* m_indices, int32_t* row_token, int32_t* row_of,
+                             int64_t T, int64_t k, int64_t first_expert, int64_t G, int64_t M_total, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  return run_layout(topk_idx, counts, m_indices, row_token, row_of, T, k, first_expert, G, 0, M_total, workspace,
+                    workspace_bytes, stream);
+}
+
+int dg_moe_layout_masked(const int32_t* topk_idx, int32_t* masked_m, int32_t* row_token, int32_t* row_of, int64_t T, int64_t k,
+                         int64_t first_expert, int64_t G, int64_t max_m, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  if (max_m < 1 || max_m > kIntMax || G > kMaxGroups) return fail(DG_ERR_SHAPE, "max_m must be >= 1 and G at most 1024");
+  return run_layout(topk_idx, masked_m, nullptr, row_token, row_of, T, k, first_expert, G, max_m, G * max_m, workspace,
+                    workspace_bytes, stream);
+}
+
+int dg_moe_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, int dtype, int64_t T, int64_t k,
+                   int64_t N, int64_t R, void* stream) {
+  int rc = check_combine(dtype, T, k, N, R);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if ((!rows && R > 0) || !row_of || !w || !y) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(rows, 16) || !aligned(y, 16)) return fail(DG_ERR_ALIGN, "rows and y must be 16-byte aligned");
+  if (!aligned(row_of, 4) || !aligned(w, 4)) return fail(DG_ERR_ALIGN, "row_of and w must be 4-byte aligned");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  return launched(launch_combine(rows, row_of, w, y, dtype == DG_BF16, T, k, N, R, hs(stream)));
+}
+
+int dg_moe_combine_bwd(const void* dy, int dtype, const uint16_t* rows, const int32_t* row_of, const float* w, uint16_t* drows,
+                       float* dw, int64_t T, int64_t k, int64_t N, int64_t R, void* stream) {
+  int rc = check_combine(dtype, T, k, N, R);
+  if (rc) return rc;
+  if (T == 0) return ok();
+  if (!dy || (R > 0 && (!rows || !drows)) || !row_of || !w || !dw) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(rows, 16) || !aligned(dy, 16) || !aligned(drows, 16))
+    return fail(DG_ERR_ALIGN, "dy, rows and drows must be 16-byte aligned");
+  if (!aligned(row_of, 4) || !aligned(w, 4) || !aligned(dw, 4)) return fail(DG_ERR_ALIGN, "row_of, w and dw must be 4-byte aligned");
+  int cus = 0;
+  if ((rc = check_device(&cus))) return rc;
+  return launched(launch_combine_bwd(dy, dtype == DG_BF16, rows, row_of, w, drows, dw, T, k, N, R, hs(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,115 @@
+// Expert rows back to tokens, and the gradient, for gfx950:
+//   y[t] = sum_j w[t, j] * rows[row_of[t, j]]
+//   drows[row_of[t, j]] = w[t, j] * dy[t],   dw[t, j] = <rows[row_of[t, j]], dy[t]>
+// over the choices j whose row is in [0, R).  rows and drows are bf16, sums
+// are held in fp32 and rounded once; the order of a token's sum is that of its
+// choices.  HBM-bound: every chosen row is read once (forward and, for dw,
+// backward) or written once (drows).
+
+#include "gemm_common.hpp"
+#include "moe_internal.hpp"
+
+namespace dg {
+namespace {
+
+__device__ __forceinline__ void bf16x8(uint4 w, float* v) {
+  v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
+  v[4] = __uint_as_float(w.z << 16); v[5] = __uint_as_float(w.z & 0xffff0000u);
+  v[6] = __uint_as_float(w.w << 16); v[7] = __uint_as_float(w.w & 0xffff0000u);
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// one workgroup per token, 8 columns per thread and pass
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ row_of,
+                                                      const float* __restrict__ w, void* __restrict__ y, int k, int N,
+                                                      int64_t R) {
+  const int64_t t = blockIdx.x;
+  for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < k; ++j) {
+      const int64_t r = row_of[t * k + j];
+      if (r < 0 || r >= R) continue;
+      const float wj = w[t * k + j];
+      float v[8];
+      bf16x8(*reinterpret_cast<const uint4*>(rows + r * N + c), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(wj, v[i], s[i]);
+    }
+    if constexpr (BF16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + t * N + c) = pack8(s);
+    } else {
+      float* d = static_cast<float*>(y) + t * N + c;
+      *reinterpret_cast<float4*>(d) = make_float4(s[0], s[1], s[2], s[3]);
+      *reinterpret_cast<float4*>(d + 4) = make_float4(s[4], s[5], s[6], s[7]);
+    }
+  }
+}
+
+// one workgroup per (token, choice)
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict__ dy, const uint16_t* __restrict__ rows,
+                                                          const int32_t* __restrict__ row_of, const float* __restrict__ w,
+                                                          uint16_t* __restrict__ drows, float* __restrict__ dw, int k, int N,
+                                                          int64_t R) {
+  __shared__ float part[4];
+  const int64_t i = blockIdx.x;
+  const int64_t t = i / k;
+  const int64_t r = row_of[i];
+  if (r < 0 || r >= R) {  // uniform over the workgroup
+    if (threadIdx.x == 0) dw[i] = 0.f;
+    return;
+  }
+  const float wj = w[i];
+  float dot = 0.f;
+  for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
+    float v[8], d[8], o[8];
+    bf16x8(*reinterpret_cast<const uint4*>(rows + r * N + c), v);
+    if constexpr (BF16) {
+      bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dy) + t * N + c), d);
+    } else {
+      const float* s = static_cast<const float*>(dy) + t * N + c;
+      const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+      d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w; d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      dot = __builtin_fmaf(v[e], d[e], dot);
+      o[e] = wj * d[e];
+    }
+    *reinterpret_cast<uint4*>(drows + r * N + c) = pack8(o);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+  __syncthreads();
+  if (threadIdx.x == 0) dw[i] = (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+}  // namespace
+
+hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
+                          int64_t k, int64_t N, int64_t R, hipStream_t stream) {
+  if (bf16_y)
+    hipLaunchKernelGGL(combine_kernel<true>, dim3((unsigned)T), dim3(256), 0, stream, rows, row_of, w, y, (int)k, (int)N, R);
+  else
+    hipLaunchKernelGGL(combine_kernel<false>, dim3((unsigned)T), dim3(256), 0, stream, rows, row_of, w, y, (int)k, (int)N, R);
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows, const int32_t* row_of, const float* w,
+                              uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
+                              hipStream_t stream) {
+  if (bf16_y)
+    hipLaunchKernelGGL(combine_bwd_kernel<true>, dim3((unsigned)(T * k)), dim3(256), 0, stream, dy, rows, row_of, w, drows,
+                       dw, (int)k, (int)N, R);
+  else
+    hipLaunchKernelGGL(combine_bwd_kernel<false>, dim3((unsigned)(T * k)), dim3(256), 0, stream, dy, rows, row_of, w, drows,
+                       dw, (int)k, (int)N, R);
+  return hipGetLastError();
+}
+
+}  // namespace dg

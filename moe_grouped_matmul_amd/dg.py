@@ -30,6 +30,12 @@ DG_OP_MASKED = 2
 DG_OP_BF16_GEMM_NT = 3
 DG_OP_GEMM_NT_UE8M0 = 4
 DG_OP_K_GROUPED = 5
+DG_OP_MXFP4_GEMM_NT = 6
+DG_OP_MOE_GATE = 7
+DG_OP_MOE_LAYOUT = 8
+
+DG_F32 = 0
+DG_BF16 = 1
 
 EXPORTED = (
     "dg_fp8_gemm_nt",
@@ -46,6 +52,17 @@ EXPORTED = (
     "dg_fp8_gemm_nt_ue8m0",
     "dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0",
     "dg_m_grouped_fp8_gemm_nt_masked_ue8m0",
+    "dg_quant_mxfp4",
+    "dg_dequant_mxfp4",
+    "dg_mxfp4_gemm_nt",
+    "dg_m_grouped_mxfp4_gemm_nt_contiguous",
+    "dg_m_grouped_mxfp4_gemm_nt_masked",
+    "dg_moe_gate",
+    "dg_moe_gate_bwd",
+    "dg_moe_layout_contiguous",
+    "dg_moe_layout_masked",
+    "dg_moe_combine",
+    "dg_moe_combine_bwd",
     "dg_get_workspace_size",
     "dg_describe_plan",
     "dg_get_m_alignment_for_contiguous_layout",
@@ -92,6 +109,18 @@ def load_library():
     lib.dg_quant_1x128_ue8m0.argtypes = [P, P, P, I64, I64, I64, P]
     lib.dg_quant_128x128_ue8m0.argtypes = [P, P, P, I64, I64, I64, P]
     lib.dg_fp8_gemm_nt_ue8m0.argtypes = [P, P, P, P, P, I64, I64, I64, P, SZ, P]
+    F = ctypes.c_float
+    lib.dg_quant_mxfp4.argtypes = [P, I, P, P, P, I64, I64, I64, I64, P]
+    lib.dg_dequant_mxfp4.argtypes = [P, P, P, I, I64, I64, I64, P]
+    lib.dg_mxfp4_gemm_nt.argtypes = [P, P, P, P, P, I64, I64, I64, P, SZ, P]
+    lib.dg_m_grouped_mxfp4_gemm_nt_contiguous.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, P, SZ, P]
+    lib.dg_m_grouped_mxfp4_gemm_nt_masked.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I64, P, SZ, P]
+    lib.dg_moe_gate.argtypes = [P, I, P, P, P, P, P, P, I64, I64, I64, I, F, F, P, SZ, P]
+    lib.dg_moe_gate_bwd.argtypes = [P, I, P, P, P, P, P, P, I64, I64, I64, I, F, F, P]
+    lib.dg_moe_layout_contiguous.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I64, P, SZ, P]
+    lib.dg_moe_layout_masked.argtypes = [P, P, P, P, I64, I64, I64, I64, I64, P, SZ, P]
+    lib.dg_moe_combine.argtypes = [P, P, P, P, I, I64, I64, I64, I64, P]
+    lib.dg_moe_combine_bwd.argtypes = [P, I, P, P, P, P, P, I64, I64, I64, I64, P]
     lib.dg_get_workspace_size.argtypes = [I, I64, I64, I64, I64]
     lib.dg_get_workspace_size.restype = SZ
     lib.dg_describe_plan.argtypes = [I, I64, I64, I64, I64]
@@ -104,7 +133,10 @@ def load_library():
     for name in ("dg_fp8_gemm_nt", "dg_fp8_gemm_nt_noalloc", "dg_fp8_gemm_nt_acc", "dg_bf16_gemm_nt", "dg_m_grouped_fp8_gemm_nt_contiguous", "dg_m_grouped_fp8_gemm_nt_masked",
                  "dg_k_grouped_fp8_gemm_nt_contiguous", "dg_quant_1x128", "dg_quant_1x128_ue8m0",
                  "dg_quant_128x128_ue8m0", "dg_fp8_gemm_nt_ue8m0", "dg_m_grouped_fp8_gemm_nt_contiguous_ue8m0",
-                 "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_quant_128x128", "dg_set_num_cus", "dg_get_num_cus",
+                 "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_quant_128x128", "dg_quant_mxfp4", "dg_dequant_mxfp4",
+                 "dg_mxfp4_gemm_nt", "dg_m_grouped_mxfp4_gemm_nt_contiguous", "dg_m_grouped_mxfp4_gemm_nt_masked",
+                 "dg_moe_gate", "dg_moe_gate_bwd", "dg_moe_layout_contiguous", "dg_moe_layout_masked",
+                 "dg_moe_combine", "dg_moe_combine_bwd", "dg_set_num_cus", "dg_get_num_cus",
                  "dg_get_m_alignment_for_contiguous_layout"):
         getattr(lib, name).restype = I
     _lib = lib
@@ -484,3 +516,217 @@ def dg_m_grouped_fp8_gemm_nt_masked_ue8m0(A, sfa, B, sfb, D, masked_m, expected_
     _check(load_library().dg_m_grouped_fp8_gemm_nt_masked_ue8m0(
         _ptr(A), _ptr(sfa), _ptr(B), _ptr(sfb), _ptr(D), _ptr(masked_m), G, max_m, N, K, int(expected_m),
         ctypes.c_void_p(0), 0, _stream(stream)))
+
+
+# ---- mixture-of-experts operators and microscaled 4-bit products.  Their calls
+# are short (a decode step makes several), so arguments are checked in one pass
+# without repeated device queries.
+
+_FLOATS = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
+
+
+def _arg(t, name, dtype, shape, dev):
+    """Pointer of tensor t, checked: dtype, shape, contiguity, current device."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor on the current device cuda:{dev} (it is on {t.device})")
+    if t.shape != shape:
+        raise ValueError(f"shape mismatch: {name} must be {tuple(shape)} (got {tuple(t.shape)})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _float_arg(t, name):
+    if t.dtype not in _FLOATS:
+        raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    return _FLOATS[t.dtype]
+
+
+def _dims(t, name, *allowed):
+    if t.dim() not in allowed:
+        raise ValueError(f"{name} must have {' or '.join(map(str, allowed))} dims (got shape {tuple(t.shape)})")
+    return t.shape
+
+
+def _ws_arg(ws, dev):
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def dg_quant_mxfp4(x, q, sf, row_token=None, stream=None):
+    """x fp32 or bf16 -> packed e2m1 codes q (uint8) and scale words sf (int32).
+
+    Without row_token: x [R,K] or [G,R,K], q [(G,)R,K/2], sf [(G,)K/128,R].  With row_token
+    [(G,)R] int32: x [T,K], row r takes row row_token[r] of x; rows whose entry is outside
+    [0,T) are not written."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(x, "x")
+    if row_token is None:
+        lead = tuple(_dims(x, "x", 2, 3)[:-1])
+        T = 0
+        rt = None
+    else:
+        _dims(x, "x", 2)
+        lead = tuple(_dims(row_token, "row_token", 1, 2))
+        T = x.shape[0]
+        rt = _arg(row_token, "row_token", torch.int32, lead, dev)
+    K = x.shape[-1]
+    G, R = (1, lead[0]) if len(lead) == 1 else lead
+    _check(load_library().dg_quant_mxfp4(
+        _arg(x, "x", x.dtype, x.shape, dev), dt, _arg(q, "q", torch.uint8, lead + (K // 2,), dev),
+        _arg(sf, "sf", torch.int32, lead[:-1] + (K // 128, R), dev), rt, G, T, R, K, _raw_stream(stream)))
+
+
+def dg_dequant_mxfp4(q, sf, y, stream=None):
+    """Packed e2m1 codes q [(G,)R,K/2] and scale words sf [(G,)K/128,R] -> values y [(G,)R,K] (fp32 or bf16)."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(y, "y")
+    lead, K = tuple(_dims(y, "y", 2, 3)[:-1]), y.shape[-1]
+    G, R = (1, lead[0]) if len(lead) == 1 else lead
+    _check(load_library().dg_dequant_mxfp4(
+        _arg(q, "q", torch.uint8, lead + (K // 2,), dev), _arg(sf, "sf", torch.int32, lead[:-1] + (K // 128, R), dev),
+        _arg(y, "y", y.dtype, y.shape, dev), dt, G, R, K, _raw_stream(stream)))
+
+
+def dg_mxfp4_gemm_nt(A, sfa, B, sfb, D, workspace=None, stream=None):
+    """D[M,N] (bf16, written) = A . B^T: A [M,K/2] and B [N,K/2] packed e2m1 (uint8), sfa [K/128,M] and
+    sfb [K/128,N] int32."""
+    dev = torch.cuda.current_device()
+    M, kb = _dims(A, "A", 2)
+    N = _dims(B, "B", 2)[0]
+    K = 2 * kb
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    _check(load_library().dg_mxfp4_gemm_nt(
+        _arg(A, "A", torch.uint8, (M, kb), dev), _arg(sfa, "sfa", torch.int32, (K // 128, M), dev),
+        _arg(B, "B", torch.uint8, (N, kb), dev), _arg(sfb, "sfb", torch.int32, (K // 128, N), dev),
+        _arg(D, "D", torch.bfloat16, (M, N), dev), M, N, K, ws, ws_bytes, _raw_stream(stream)))
+
+
+def dg_m_grouped_mxfp4_gemm_nt_contiguous(A, sfa, B, sfb, D, m_indices, stream=None):
+    """M-grouped contiguous: A [M_total,K/2], sfa [K/128,M_total], B [G,N,K/2], sfb [G,K/128,N], D [M_total,N]
+    bf16, m_indices [M_total] int32 (-1 = padding row, not written)."""
+    dev = torch.cuda.current_device()
+    M, kb = _dims(A, "A", 2)
+    G, N = _dims(B, "B", 3)[:2]
+    K = 2 * kb
+    _check(load_library().dg_m_grouped_mxfp4_gemm_nt_contiguous(
+        _arg(A, "A", torch.uint8, (M, kb), dev), _arg(sfa, "sfa", torch.int32, (K // 128, M), dev),
+        _arg(B, "B", torch.uint8, (G, N, kb), dev), _arg(sfb, "sfb", torch.int32, (G, K // 128, N), dev),
+        _arg(D, "D", torch.bfloat16, (M, N), dev), _arg(m_indices, "m_indices", torch.int32, (M,), dev), M, N, K, G,
+        None, 0, _raw_stream(stream)))
+
+
+def dg_m_grouped_mxfp4_gemm_nt_masked(A, sfa, B, sfb, D, masked_m, expected_m=0, stream=None):
+    """M-grouped masked: A [G,max_m,K/2], sfa [G,K/128,max_m], B [G,N,K/2], sfb [G,K/128,N], D [G,max_m,N] bf16,
+    masked_m [G] int32 on device (rows past it are not written)."""
+    dev = torch.cuda.current_device()
+    G, max_m, kb = _dims(A, "A", 3)
+    N = _dims(B, "B", 3)[1]
+    K = 2 * kb
+    _check(load_library().dg_m_grouped_mxfp4_gemm_nt_masked(
+        _arg(A, "A", torch.uint8, (G, max_m, kb), dev), _arg(sfa, "sfa", torch.int32, (G, K // 128, max_m), dev),
+        _arg(B, "B", torch.uint8, (G, N, kb), dev), _arg(sfb, "sfb", torch.int32, (G, K // 128, N), dev),
+        _arg(D, "D", torch.bfloat16, (G, max_m, N), dev), _arg(masked_m, "masked_m", torch.int32, (G,), dev), G, max_m,
+        N, K, int(expected_m), None, 0, _raw_stream(stream)))
+
+
+def dg_moe_gate(logits, topk_idx, topk_w, counts, prob_sum, loss, renorm=True, w_scale=1.0, loss_coef=0.0, valid=None,
+                workspace=None, stream=None):
+    """Router: logits [T,E] fp32 or bf16 -> topk_idx [T,k] int32, topk_w [T,k] fp32, counts [E+1] int32 (choices of
+    each expert, then tokens routed), prob_sum [E] fp32, loss [1] fp32.  valid [T] bool or uint8: tokens with 0 are
+    skipped.  workspace: dg_get_workspace_size(DG_OP_MOE_GATE, T, E, k) bytes."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(logits, "logits")
+    T, E = _dims(logits, "logits", 2)
+    k = _dims(topk_idx, "topk_idx", 2)[1]
+    vp = None
+    if valid is not None:
+        vp = _arg(valid, "valid", torch.bool if valid.dtype is torch.bool else torch.uint8, (T,), dev)
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    _check(load_library().dg_moe_gate(
+        _arg(logits, "logits", logits.dtype, (T, E), dev), dt, vp, _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+        _arg(topk_w, "topk_w", torch.float32, (T, k), dev), _arg(counts, "counts", torch.int32, (E + 1,), dev),
+        _arg(prob_sum, "prob_sum", torch.float32, (E,), dev), _arg(loss, "loss", torch.float32, (1,), dev), T, E, k,
+        int(renorm), w_scale, loss_coef, ws, ws_bytes, _raw_stream(stream)))
+
+
+def dg_moe_gate_bwd(logits, topk_idx, topk_w, counts, dw, dloss, dlogits, renorm=True, w_scale=1.0, loss_coef=0.0,
+                    stream=None):
+    """Gradient of sum(dw * topk_w) + dloss * loss: dlogits [T,E] of the logits' type.  dw [T,k] fp32 or None, dloss
+    [1] fp32 or None; the other arguments are dg_moe_gate's."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(logits, "logits")
+    T, E = _dims(logits, "logits", 2)
+    k = _dims(topk_idx, "topk_idx", 2)[1]
+    _check(load_library().dg_moe_gate_bwd(
+        _arg(logits, "logits", logits.dtype, (T, E), dev), dt, _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
+        _arg(topk_w, "topk_w", torch.float32, (T, k), dev), _arg(counts, "counts", torch.int32, (E + 1,), dev),
+        None if dw is None else _arg(dw, "dw", torch.float32, (T, k), dev),
+        None if dloss is None else _arg(dloss, "dloss", torch.float32, (1,), dev),
+        _arg(dlogits, "dlogits", logits.dtype, (T, E), dev), T, E, k, int(renorm), w_scale, loss_coef,
+        _raw_stream(stream)))
+
+
+def dg_moe_layout_contiguous(topk_idx, counts, m_indices, row_token, row_of, first_expert=0, workspace=None, stream=None):
+    """Rows of the contiguous form from topk_idx [T,k] int32: counts [G], m_indices and row_token [M_total], row_of
+    [T,k], all int32, for experts first_expert + [0, G).  workspace: dg_get_workspace_size(DG_OP_MOE_LAYOUT, T, 0, k,
+    G) bytes."""
+    dev = torch.cuda.current_device()
+    T, k = _dims(topk_idx, "topk_idx", 2)
+    (G,), (M,) = _dims(counts, "counts", 1), _dims(m_indices, "m_indices", 1)
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    i32 = torch.int32
+    _check(load_library().dg_moe_layout_contiguous(
+        _arg(topk_idx, "topk_idx", i32, (T, k), dev), _arg(counts, "counts", i32, (G,), dev),
+        _arg(m_indices, "m_indices", i32, (M,), dev), _arg(row_token, "row_token", i32, (M,), dev),
+        _arg(row_of, "row_of", i32, (T, k), dev), T, k, first_expert, G, M, ws, ws_bytes, _raw_stream(stream)))
+
+
+def dg_moe_layout_masked(topk_idx, masked_m, row_token, row_of, first_expert=0, workspace=None, stream=None):
+    """Rows of the masked form from topk_idx [T,k] int32: masked_m [G], row_token [G,max_m], row_of [T,k] (flat rows of
+    [G * max_m]), all int32, for experts first_expert + [0, G).  workspace as for dg_moe_layout_contiguous."""
+    dev = torch.cuda.current_device()
+    T, k = _dims(topk_idx, "topk_idx", 2)
+    G, max_m = _dims(row_token, "row_token", 2)
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    i32 = torch.int32
+    _check(load_library().dg_moe_layout_masked(
+        _arg(topk_idx, "topk_idx", i32, (T, k), dev), _arg(masked_m, "masked_m", i32, (G,), dev),
+        _arg(row_token, "row_token", i32, (G, max_m), dev), _arg(row_of, "row_of", i32, (T, k), dev), T, k, first_expert,
+        G, max_m, ws, ws_bytes, _raw_stream(stream)))
+
+
+def dg_moe_combine(rows, row_of, w, y, stream=None):
+    """y[t] = sum_j w[t,j] rows[row_of[t,j]]: rows [R,N] bf16, row_of [T,k] int32 (-1: none), w [T,k] fp32, y [T,N]
+    fp32 or bf16 (written)."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(y, "y")
+    R, N = _dims(rows, "rows", 2)
+    T, k = _dims(row_of, "row_of", 2)
+    _check(load_library().dg_moe_combine(
+        _arg(rows, "rows", torch.bfloat16, (R, N), dev), _arg(row_of, "row_of", torch.int32, (T, k), dev),
+        _arg(w, "w", torch.float32, (T, k), dev), _arg(y, "y", y.dtype, (T, N), dev), dt, T, k, N, R,
+        _raw_stream(stream)))
+
+
+def dg_moe_combine_bwd(dy, rows, row_of, w, drows, dw, stream=None):
+    """Gradients of dg_moe_combine: drows [R,N] bf16 (rows of no choice are not written) and dw [T,k] fp32 from dy
+    [T,N] fp32 or bf16."""
+    dev = torch.cuda.current_device()
+    dt = _float_arg(dy, "dy")
+    R, N = _dims(rows, "rows", 2)
+    T, k = _dims(row_of, "row_of", 2)
+    _check(load_library().dg_moe_combine_bwd(
+        _arg(dy, "dy", dy.dtype, (T, N), dev), dt, _arg(rows, "rows", torch.bfloat16, (R, N), dev),
+        _arg(row_of, "row_of", torch.int32, (T, k), dev), _arg(w, "w", torch.float32, (T, k), dev),
+        _arg(drows, "drows", torch.bfloat16, (R, N), dev), _arg(dw, "dw", torch.float32, (T, k), dev), T, k, N, R,
+        _raw_stream(stream)))
