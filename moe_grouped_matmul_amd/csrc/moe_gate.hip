@@ -43,18 +43,24 @@ constexpr int kGateMaxBlocks = kGateFan * kGateFan;
 constexpr int kGateCounterBytes = 128;  // root counter, then one per group
 constexpr int kBwdThreads = 256;
 
-// ---- keys: 0 is "never chosen" (-inf, NaN)
+// ---- keys.  -inf and NaN (read as -inf) sort below every number; 0 is an
+// empty place; neither is ever chosen: some(key) is false for both.
 template <bool BF16>
 struct Keys;
+
+// order-preserving bits of a float, -0 as +0 (equal logits, equal keys), NaN as -inf
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const int32_t u = (int32_t)__float_as_uint(fmaxf(f + 0.0f, -__builtin_inff()));
+  return (uint32_t)(u ^ ((u >> 31) | (int32_t)0x80000000));
+}
 
 template <>
 struct Keys<true> {
   typedef uint32_t T;
   static __device__ __forceinline__ T make(float f, int e) {
-    const uint32_t u = __float_as_uint(f + 0.0f) >> 16;  // -0 becomes +0: equal logits, equal keys
-    const uint32_t o = u & 0x8000u ? ~u & 0xffffu : u | 0x8000u;
-    return f > -__builtin_inff() ? (o << 16) | (0xffffu - (uint32_t)e) : 0u;  // false for NaN too
+    return (ordered(f) & 0xffff0000u) | (0xffffu - (uint32_t)e);
   }
+  static __device__ __forceinline__ bool some(T k) { return k >= 0x00800000u; }
   static __device__ __forceinline__ float value(T k) {
     const uint32_t o = k >> 16;
     return __uint_as_float((o & 0x8000u ? o & 0x7fffu : ~o & 0xffffu) << 16);
@@ -73,10 +79,12 @@ template <>
 struct Keys<false> {
   typedef double T;
   static __device__ __forceinline__ T make(float f, int e) {
-    const uint32_t u = __float_as_uint(f + 0.0f);
-    const uint32_t o = u & 0x80000000u ? ~u : u | 0x80000000u;
-    const uint64_t b = 0x3ff0000000000000ull | ((uint64_t)o << 10) | (uint64_t)(1023 - e);
-    return f > -__builtin_inff() ? __builtin_bit_cast(double, b) : 0.0;
+    const uint32_t o = ordered(f);
+    const uint32_t hi = __builtin_amdgcn_alignbit(0x3ff00000u >> 10, o, 22);  // exponent of 1.0, then o's upper 10 bits
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | ((o << 10) | (uint32_t)(1023 - e)));
+  }
+  static __device__ __forceinline__ bool some(T k) {
+    return k >= __builtin_bit_cast(double, 0x3ff0000000000000ull | ((uint64_t)0x00800000u << 10));
   }
   static __device__ __forceinline__ float value(T k) {
     const uint32_t o = (uint32_t)(__builtin_bit_cast(uint64_t, k) >> 10);
@@ -114,6 +122,15 @@ __device__ __forceinline__ typename Keys<BF16>::T group_max(typename Keys<BF16>:
   }
   return v;
 }
+// sum over the four rows of 16 lanes
+__device__ __forceinline__ float rows_sum(float v) {
+  const uint32_t a = __float_as_uint(v);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);  // each pair of rows: the even one, the odd one
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  const uint32_t b = __float_as_uint(v);
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
 template <int C>
 __device__ __forceinline__ float dppf(float a) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(a), C, 0xf, 0xf, true));
@@ -143,14 +160,13 @@ __device__ __forceinline__ float group_fmax(float v) {
   return v;
 }
 
-// e^x for x <= 0 (NaN stays NaN): 2^(x log2 e) with the rounding error of the
-// product put back, since |x| may be large; 0 below 2^-126
+// e^x for x <= 0 (NaN stays NaN): 2^n 2^f with n the integer nearest x log2 e
+// and f = x log2 e - n rounded once, so the error does not grow with the product
 __device__ __forceinline__ float exp_neg(float x) {
-  x = x < -200.f ? -200.f : x;
-  const float t = x * 1.44269502f;
-  const float r = __builtin_fmaf(x, 1.44269502f, -t) + x * 1.92596303e-8f;
-  const float y = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(y, r * 0.693147182f, y);
+  x = __builtin_elementwise_maximum(x, -200.f);
+  const float n = __builtin_rintf(x * 1.44269502f);
+  const float f = __builtin_fmaf(x, 1.44269502f, -n);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
 template <bool BF16, int M>
@@ -311,18 +327,20 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(GateParams p) {
     }
     float m = 0.f;
     Key mine = 0;  // lane j < k: the j-th choice
-    for (int j = 0; j < p.k; ++j) {
-      const Key top = group_max<LPT, BF16>(key[0]);
-      const bool win = key[0] == top;
 #pragma unroll
-      for (int i = 0; i + 1 < L; ++i) {  // values first: a choice of array elements would be a variable index
-        const Key a = key[i], b = key[i + 1];
-        key[i] = win ? b : a;
+    for (int j = 0; j < KCAP; ++j) {
+      if (j < p.k) {  // uniform
+        const Key top = group_max<LPT, BF16>(key[0]);
+        const bool win = key[0] == top;
+        // what round j leaves at place i > KCAP - 2 - j no later round reads
+#pragma unroll
+        for (int i = 0; i < L && i < KCAP - 1 - j; ++i) {  // values first: a choice of array elements would be a variable index
+          const Key a = key[i], b = i + 1 < L ? key[i + 1 < L ? i + 1 : 0] : Key(0);
+          key[i] = win ? b : a;
+        }
+        if (j == 0 && KT::some(top)) m = KT::value(top);
+        if (sub == j) mine = top;
       }
-      const Key last = key[L - 1];
-      key[L - 1] = win ? Key(0) : last;
-      if (j == 0 && top != Key(0)) m = KT::value(top);
-      if (sub == j) mine = top;
     }
     float ex[VPL];
     float s = 0.f;
@@ -332,7 +350,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(GateParams p) {
       s += ex[v];
     }
     s = group_sum<LPT>(s);
-    const bool have = mine != Key(0);
+    const bool have = KT::some(mine);
     const float em = have ? exp_neg(KT::value(mine) - m) : 0.f;
     const float den = p.renorm ? group_sum<LPT>(em) : s;
     const float inv = s > 0.f ? 1.0f / s : (s == s ? 0.f : s);  // no choice: 0; NaN stays NaN
@@ -350,10 +368,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(GateParams p) {
 #pragma unroll
   for (int v = 0; v < VPL; ++v) {
     float x = sum[v];
-    if constexpr (LPT == 16) {
-      x += __shfl_xor(x, 16);
-      x += __shfl_xor(x, 32);
-    }
+    if constexpr (LPT == 16) x = rows_sum(x);
     if ((threadIdx.x & 63) < LPT) psum[wave][R::expert(sub, v)] = x;
   }
   __syncthreads();
