@@ -7,8 +7,16 @@
 // and its choices take its rows in (token, choice) order, so the layout is a
 // function of idx alone.
 //
-// Three launches: counts per block of choices (and the fill of the row
-// arrays), a scan over blocks and experts, and the placement.
+// A workgroup places 2048 choices.  Up to that many, one launch does
+// everything; beyond, a first launch writes the counts of each block of
+// choices and every workgroup of the second sums the column of counts of each
+// expert before its own block and over all blocks (a thread per expert), so no
+// workgroup waits for another.  Inside a workgroup every wave counts its own
+// run of choices, the waves' counts are summed in order, and a wave ranks 64
+// choices at a time by matching their experts bit by bit.  Rows that hold
+// nothing are known from the counts alone, so their -1 needs no order against
+// the placement; the workgroups share them.  The traffic is a few hundred
+// kilobytes: the time is launch latency and the dependent steps.
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
@@ -16,10 +24,10 @@
 namespace dg {
 namespace {
 
-constexpr int kLayMaxGroups = 1024;
-constexpr int kLayThreads = 256;
+constexpr int kLayThreads = 1024;  // also the most experts: a thread per expert
 constexpr int kLayWaves = kLayThreads / 64;
-constexpr int kLayItems = 2048;  // choices per block
+constexpr int kLayItems = 2048;  // choices per workgroup
+constexpr int kLayBatch = 32;    // counts a thread has in flight
 constexpr int kLayWaveItems = kLayItems / kLayWaves;
 
 __device__ __forceinline__ int local_expert(int v, int first, int G) {
@@ -27,116 +35,161 @@ __device__ __forceinline__ int local_expert(int v, int first, int G) {
   return v >= 0 && g >= 0 && g < G ? g : -1;
 }
 
-// ws[block][g]: choices of expert g in the block; row arrays filled with -1
+// ws[block][g]: choices of expert g in the block
 __global__ void __launch_bounds__(kLayThreads) layout_count_kernel(LayoutParams p) {
-  __shared__ int hist[kLayMaxGroups];
-  const int b = (int)blockIdx.x;
-  for (int g = threadIdx.x; g < p.G; g += kLayThreads) hist[g] = 0;
+  __shared__ int hist[kLayThreads];
+  hist[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)b * kLayItems;
-  for (int64_t i = i0 + threadIdx.x; i < p.n && i < i0 + kLayItems; i += kLayThreads) {
-    const int g = local_expert(p.idx[i], p.first, p.G);
+  const int64_t i0 = (int64_t)blockIdx.x * kLayItems + threadIdx.x;
+  int v[kLayItems / kLayThreads];
+#pragma unroll
+  for (int c = 0; c < kLayItems / kLayThreads; ++c) {
+    const int64_t i = i0 + c * kLayThreads;
+    v[c] = i < p.n ? p.idx[i] : -1;
+  }
+#pragma unroll
+  for (int c = 0; c < kLayItems / kLayThreads; ++c) {
+    const int g = local_expert(v[c], p.first, p.G);
     if (g >= 0) atomicAdd(&hist[g], 1);
   }
   __syncthreads();
-  int* out = static_cast<int*>(p.ws) + (int64_t)b * p.G;
-  for (int g = threadIdx.x; g < p.G; g += kLayThreads) out[g] = hist[g];
-  for (int64_t r = (int64_t)b * kLayThreads + threadIdx.x; r < p.rows; r += (int64_t)gridDim.x * kLayThreads) {
-    p.row_token[r] = -1;
-    if (p.m_indices) p.m_indices[r] = -1;
-  }
+  if ((int)threadIdx.x < p.G) static_cast<int*>(p.ws)[(int64_t)blockIdx.x * p.G + threadIdx.x] = hist[threadIdx.x];
 }
 
-// in place: ws[block][g] becomes the first row of the block's choices of g (relative to the
-// expert's first row when masked: the rank is needed there); counts written
-__global__ void __launch_bounds__(kLayMaxGroups) layout_scan_kernel(LayoutParams p, int blocks) {
-  __shared__ int wsum[kLayMaxGroups / 64];
-  const int g = threadIdx.x;
-  int* ws = static_cast<int*>(p.ws);
-  int run = 0;
-  if (g < p.G) {
-    for (int b = 0; b < blocks; ++b) {
-      const int c = ws[(int64_t)b * p.G + g];
-      ws[(int64_t)b * p.G + g] = run;
-      run += c;
-    }
-    p.counts[g] = p.max_m && run > p.max_m ? (int)p.max_m : run;
-  }
-  if (p.max_m) return;
-  // exclusive prefix of the segment lengths
-  int v = g < p.G ? (run + 127) / 128 * 128 : 0;
-  const int own = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(v, o);
-    if ((g & 63) >= o) v += u;
-  }
-  if ((g & 63) == 63) wsum[g >> 6] = v;
-  __syncthreads();
-  int start = v - own;
-  for (int i = 0; i < (g >> 6); ++i) start += wsum[i];
-  if (g < p.G)
-    for (int b = 0; b < blocks; ++b) {
-      ws[(int64_t)b * p.G + g] += start;  // n + 128 G < 2^31: every row number is an int
-    }
-}
-
-__global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams p) {
-  __shared__ int next[kLayWaves][kLayMaxGroups];  // next row (rank when masked) of each expert, per wave
+// workgroups [0, blocks) place their block; all share the rows that hold nothing
+__global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams p, int blocks) {
+  __shared__ int next[kLayWaves][kLayThreads];  // next row (rank when masked) of each expert, per wave
+  __shared__ int start_of[kLayThreads + 1];     // first row of each expert's segment (contiguous)
+  __shared__ int count_of[kLayThreads];
+  __shared__ int wsum[kLayWaves];
   const int b = (int)blockIdx.x;
-  const int wave = threadIdx.x >> 6;
-  const int lane = threadIdx.x & 63;
-  const int* base = static_cast<const int*>(p.ws) + (int64_t)b * p.G;
-  for (int i = threadIdx.x; i < kLayWaves * p.G; i += kLayThreads) next[i / p.G][i % p.G] = 0;
-  __syncthreads();
-  const int64_t w0 = (int64_t)b * kLayItems + (int64_t)wave * kLayWaveItems;
-  const int64_t w1 = w0 + kLayWaveItems < p.n ? w0 + kLayWaveItems : p.n;
-  for (int64_t i = w0 + lane; i < w1; i += 64) {
-    const int g = local_expert(p.idx[i], p.first, p.G);
-    if (g >= 0) atomicAdd(&next[wave][g], 1);
-  }
-  __syncthreads();
-  for (int g = threadIdx.x; g < p.G; g += kLayThreads) {
-    int run = base[g];
+  const int tid = threadIdx.x;
+  const int wave = tid >> 6;
+  const int lane = tid & 63;
+  const int G = p.G;
+  const bool placing = b < blocks;
+  const bool single = blocks == 1;
+  if (tid < G) {
 #pragma unroll
-    for (int w = 0; w < kLayWaves; ++w) {
-      const int c = next[w][g];
-      next[w][g] = run;
-      run += c;
-    }
+    for (int w = 0; w < kLayWaves; ++w) next[w][tid] = 0;
   }
   __syncthreads();
-  int bits = 1;
-  while ((1 << bits) <= p.G) ++bits;  // codes 0 .. G (G: none)
-  for (int64_t i = w0; i < w1; i += 64) {  // uniform: the wave's choices in order
-    const bool in = i + lane < w1;
-    const int g = in ? local_expert(p.idx[i + lane], p.first, p.G) : -1;
-    const int code = g < 0 ? p.G : g;
-    unsigned long long same = ~0ull;  // lanes with this lane's expert
-    for (int k = 0; k < bits; ++k) {
-      const unsigned long long m = __ballot((code >> k) & 1);
-      same &= (code >> k) & 1 ? m : ~m;
-    }
-    const int before = __popcll(same & ((1ull << lane) - 1ull));
-    int row = -1;
-    if (g >= 0) {
-      const int first = next[wave][g];
-      const int64_t at = (int64_t)first + before;
-      if (p.max_m)
-        row = at < p.max_m ? (int)((int64_t)g * p.max_m + at) : -1;
-      else
-        row = at < p.rows ? (int)at : -1;
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (g >= 0 && before == 0) next[wave][g] += __popcll(same);
-    __builtin_amdgcn_wave_barrier();
-    if (in) {
-      p.row_of[i + lane] = row;
-      if (row >= 0) {
-        p.row_token[row] = (int)((i + lane) / p.k);
-        if (p.m_indices) p.m_indices[row] = g;
+  // counts of the wave's own choices (one block: every workgroup counts it, for the totals)
+  const int64_t w0 = (single ? 0 : (int64_t)b * kLayItems) + (int64_t)wave * kLayWaveItems;
+  int e[kLayWaveItems / 64];
+#pragma unroll
+  for (int c = 0; c < kLayWaveItems / 64; ++c) {
+    const int64_t i = w0 + 64 * c + lane;
+    e[c] = (placing || single) && i < p.n ? local_expert(p.idx[i], p.first, G) : -1;
+  }
+#pragma unroll
+  for (int c = 0; c < kLayWaveItems / 64; ++c)
+    if (e[c] >= 0) atomicAdd(&next[wave][e[c]], 1);
+  // choices of expert tid before this block, and in all
+  int before = 0, total = 0;
+  if (!single && tid < G) {
+    const int* col = static_cast<const int*>(p.ws) + tid;
+    for (int c0 = 0; c0 < blocks; c0 += kLayBatch) {
+      int v[kLayBatch];
+#pragma unroll
+      for (int c = 0; c < kLayBatch; ++c) v[c] = c0 + c < blocks ? col[(int64_t)(c0 + c) * G] : 0;
+#pragma unroll
+      for (int c = 0; c < kLayBatch; ++c) {
+        before += c0 + c < b ? v[c] : 0;
+        total += v[c];
       }
     }
+  }
+  __syncthreads();
+  if (single && tid < G) {
+#pragma unroll
+    for (int w = 0; w < kLayWaves; ++w) total += next[w][tid];
+  }
+  // first rows: exclusive prefix of the padded segment lengths
+  int start = 0;
+  if (!p.max_m) {
+    const int own = (total + 127) & ~127;
+    int v = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane == 63) wsum[wave] = v;
+    __syncthreads();
+    start = v - own;
+#pragma unroll
+    for (int w = 0; w < kLayWaves; ++w) start += w < wave ? wsum[w] : 0;
+    start_of[tid] = start;
+    if (tid == kLayThreads - 1) start_of[kLayThreads] = start + own;
+  }
+  if (tid < G) {
+    const int held = p.max_m && total > p.max_m ? (int)p.max_m : total;
+    count_of[tid] = held;
+    if (b == 0) p.counts[tid] = held;
+    int run = start + before;
+#pragma unroll
+    for (int w = 0; w < kLayWaves; ++w) {
+      const int c = next[w][tid];
+      next[w][tid] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  if (placing) {
+    int bits = 1;
+    while ((1 << bits) <= G) ++bits;  // codes 0 .. G (G: none)
+#pragma unroll
+    for (int c = 0; c < kLayWaveItems / 64; ++c) {  // the wave's choices in order
+      const int64_t i = w0 + 64 * c + lane;
+      if (w0 + 64 * c >= p.n) break;  // uniform
+      const int g = e[c];
+      const int code = g < 0 ? G : g;
+      unsigned long long same = ~0ull;  // lanes with this lane's expert
+      for (int k = 0; k < bits; ++k) {
+        const unsigned long long m = __ballot((code >> k) & 1);
+        same &= (code >> k) & 1 ? m : ~m;
+      }
+      const int rank = __popcll(same & ((1ull << lane) - 1ull));
+      int row = -1;
+      if (g >= 0) {
+        const int64_t at = (int64_t)next[wave][g] + rank;
+        if (p.max_m) row = at < p.max_m ? (int)((int64_t)g * p.max_m + at) : -1;
+        else row = at < p.rows ? (int)at : -1;
+      }
+      __builtin_amdgcn_wave_barrier();  // LDS accesses of a wave are in order: read above, then advanced
+      if (g >= 0 && rank == 0) next[wave][g] += __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      if (i < p.n) {
+        p.row_of[i] = row;
+        if (row >= 0) {
+          p.row_token[row] = (int)((uint32_t)i / (uint32_t)p.k);
+          if (p.m_indices) p.m_indices[row] = g;
+        }
+      }
+    }
+  }
+  // rows that hold nothing, shared by all workgroups
+  const int64_t stride = (int64_t)gridDim.x * kLayThreads;
+  if (p.max_m) {
+    for (int64_t r = (int64_t)b * kLayThreads + tid; r < p.rows; r += stride) {
+      const uint32_t g = (uint32_t)r / (uint32_t)p.max_m;
+      if ((int)((uint32_t)r - g * (uint32_t)p.max_m) >= count_of[g]) p.row_token[r] = -1;
+    }
+    return;
+  }
+  for (int g = b * kLayWaves + wave; g < G; g += (int)gridDim.x * kLayWaves) {  // a wave behind each expert's choices
+    const int64_t lo = (int64_t)start_of[g] + count_of[g];
+    int64_t hi = (int64_t)start_of[g] + ((count_of[g] + 127) & ~127);
+    if (hi > p.rows) hi = p.rows;
+    for (int64_t r = lo + lane; r < hi; r += 64) {
+      p.row_token[r] = -1;
+      p.m_indices[r] = -1;
+    }
+  }
+  for (int64_t r = start_of[kLayThreads] + (int64_t)b * kLayThreads + tid; r < p.rows; r += stride) {  // behind the last segment
+    p.row_token[r] = -1;
+    p.m_indices[r] = -1;
   }
 }
 
@@ -149,9 +202,11 @@ size_t layout_workspace_bytes(int64_t n, int64_t G) {
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
   const int blocks = (int)(p.n > 0 ? (p.n + kLayItems - 1) / kLayItems : 1);
-  hipLaunchKernelGGL(layout_count_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p);
-  hipLaunchKernelGGL(layout_scan_kernel, dim3(1), dim3(kLayMaxGroups), 0, stream, p, blocks);
-  if (p.n > 0) hipLaunchKernelGGL(layout_place_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p);
+  if (blocks > 1) hipLaunchKernelGGL(layout_count_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p);
+  // further workgroups where the rows outnumber the choices
+  const int64_t f = (p.rows + 4 * kLayThreads - 1) / (4 * kLayThreads);
+  const int fill = (int)(f < 256 ? f : 256);
+  hipLaunchKernelGGL(layout_place_kernel, dim3(blocks > fill ? blocks : fill), dim3(kLayThreads), 0, stream, p, blocks);
   return hipGetLastError();
 }
 
