@@ -144,7 +144,7 @@ def load_library():
 
 
 def _check(rc):
-    if rc != DG_OK:
+    if rc:  # not DG_OK
         msg = load_library().dg_get_last_error().decode()
         raise DGError(rc, msg)
 
@@ -519,35 +519,37 @@ def dg_m_grouped_fp8_gemm_nt_masked_ue8m0(A, sfa, B, sfb, D, masked_m, expected_
 
 
 # ---- mixture-of-experts operators and microscaled 4-bit products.  Their calls
-# are short (a decode step makes several), so arguments are checked in one pass
-# without repeated device queries.
+# are short (a decode step makes several), so an argument is checked in one
+# expression and looked at in detail only to word the error.
 
 _FLOATS = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
 
 
 def _arg(t, name, dtype, shape, dev):
     """Pointer of tensor t, checked: dtype, shape, contiguity, current device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor on the current device cuda:{dev} (it is on {t.device})")
     if t.shape != shape:
         raise ValueError(f"shape mismatch: {name} must be {tuple(shape)} (got {tuple(t.shape)})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _float_arg(t, name):
-    if t.dtype not in _FLOATS:
+    dt = _FLOATS.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
-    return _FLOATS[t.dtype]
+    return dt
 
 
 def _dims(t, name, *allowed):
-    if t.dim() not in allowed:
-        raise ValueError(f"{name} must have {' or '.join(map(str, allowed))} dims (got shape {tuple(t.shape)})")
-    return t.shape
+    s = t.shape
+    if len(s) not in allowed:
+        raise ValueError(f"{name} must have {' or '.join(map(str, allowed))} dims (got shape {tuple(s)})")
+    return s
 
 
 def _ws_arg(ws, dev):
@@ -555,11 +557,12 @@ def _ws_arg(ws, dev):
         return None, 0
     if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, dev):
+    # the current stream's handle without a Stream object around it
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def dg_quant_mxfp4(x, q, sf, row_token=None, stream=None):
@@ -583,7 +586,7 @@ def dg_quant_mxfp4(x, q, sf, row_token=None, stream=None):
     G, R = (1, lead[0]) if len(lead) == 1 else lead
     _check(load_library().dg_quant_mxfp4(
         _arg(x, "x", x.dtype, x.shape, dev), dt, _arg(q, "q", torch.uint8, lead + (K // 2,), dev),
-        _arg(sf, "sf", torch.int32, lead[:-1] + (K // 128, R), dev), rt, G, T, R, K, _raw_stream(stream)))
+        _arg(sf, "sf", torch.int32, lead[:-1] + (K // 128, R), dev), rt, G, T, R, K, _raw_stream(stream, dev)))
 
 
 def dg_dequant_mxfp4(q, sf, y, stream=None):
@@ -594,7 +597,7 @@ def dg_dequant_mxfp4(q, sf, y, stream=None):
     G, R = (1, lead[0]) if len(lead) == 1 else lead
     _check(load_library().dg_dequant_mxfp4(
         _arg(q, "q", torch.uint8, lead + (K // 2,), dev), _arg(sf, "sf", torch.int32, lead[:-1] + (K // 128, R), dev),
-        _arg(y, "y", y.dtype, y.shape, dev), dt, G, R, K, _raw_stream(stream)))
+        _arg(y, "y", y.dtype, y.shape, dev), dt, G, R, K, _raw_stream(stream, dev)))
 
 
 def dg_mxfp4_gemm_nt(A, sfa, B, sfb, D, workspace=None, stream=None):
@@ -608,7 +611,7 @@ def dg_mxfp4_gemm_nt(A, sfa, B, sfb, D, workspace=None, stream=None):
     _check(load_library().dg_mxfp4_gemm_nt(
         _arg(A, "A", torch.uint8, (M, kb), dev), _arg(sfa, "sfa", torch.int32, (K // 128, M), dev),
         _arg(B, "B", torch.uint8, (N, kb), dev), _arg(sfb, "sfb", torch.int32, (K // 128, N), dev),
-        _arg(D, "D", torch.bfloat16, (M, N), dev), M, N, K, ws, ws_bytes, _raw_stream(stream)))
+        _arg(D, "D", torch.bfloat16, (M, N), dev), M, N, K, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def dg_m_grouped_mxfp4_gemm_nt_contiguous(A, sfa, B, sfb, D, m_indices, stream=None):
@@ -622,7 +625,7 @@ def dg_m_grouped_mxfp4_gemm_nt_contiguous(A, sfa, B, sfb, D, m_indices, stream=N
         _arg(A, "A", torch.uint8, (M, kb), dev), _arg(sfa, "sfa", torch.int32, (K // 128, M), dev),
         _arg(B, "B", torch.uint8, (G, N, kb), dev), _arg(sfb, "sfb", torch.int32, (G, K // 128, N), dev),
         _arg(D, "D", torch.bfloat16, (M, N), dev), _arg(m_indices, "m_indices", torch.int32, (M,), dev), M, N, K, G,
-        None, 0, _raw_stream(stream)))
+        None, 0, _raw_stream(stream, dev)))
 
 
 def dg_m_grouped_mxfp4_gemm_nt_masked(A, sfa, B, sfb, D, masked_m, expected_m=0, stream=None):
@@ -636,7 +639,7 @@ def dg_m_grouped_mxfp4_gemm_nt_masked(A, sfa, B, sfb, D, masked_m, expected_m=0,
         _arg(A, "A", torch.uint8, (G, max_m, kb), dev), _arg(sfa, "sfa", torch.int32, (G, K // 128, max_m), dev),
         _arg(B, "B", torch.uint8, (G, N, kb), dev), _arg(sfb, "sfb", torch.int32, (G, K // 128, N), dev),
         _arg(D, "D", torch.bfloat16, (G, max_m, N), dev), _arg(masked_m, "masked_m", torch.int32, (G,), dev), G, max_m,
-        N, K, int(expected_m), None, 0, _raw_stream(stream)))
+        N, K, int(expected_m), None, 0, _raw_stream(stream, dev)))
 
 
 def dg_moe_gate(logits, topk_idx, topk_w, counts, prob_sum, loss, renorm=True, w_scale=1.0, loss_coef=0.0, valid=None,
@@ -656,7 +659,7 @@ def dg_moe_gate(logits, topk_idx, topk_w, counts, prob_sum, loss, renorm=True, w
         _arg(logits, "logits", logits.dtype, (T, E), dev), dt, vp, _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev),
         _arg(topk_w, "topk_w", torch.float32, (T, k), dev), _arg(counts, "counts", torch.int32, (E + 1,), dev),
         _arg(prob_sum, "prob_sum", torch.float32, (E,), dev), _arg(loss, "loss", torch.float32, (1,), dev), T, E, k,
-        int(renorm), w_scale, loss_coef, ws, ws_bytes, _raw_stream(stream)))
+        int(renorm), w_scale, loss_coef, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def dg_moe_gate_bwd(logits, topk_idx, topk_w, counts, dw, dloss, dlogits, renorm=True, w_scale=1.0, loss_coef=0.0,
@@ -673,7 +676,7 @@ def dg_moe_gate_bwd(logits, topk_idx, topk_w, counts, dw, dloss, dlogits, renorm
         None if dw is None else _arg(dw, "dw", torch.float32, (T, k), dev),
         None if dloss is None else _arg(dloss, "dloss", torch.float32, (1,), dev),
         _arg(dlogits, "dlogits", logits.dtype, (T, E), dev), T, E, k, int(renorm), w_scale, loss_coef,
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 def dg_moe_layout_contiguous(topk_idx, counts, m_indices, row_token, row_of, first_expert=0, workspace=None, stream=None):
@@ -688,7 +691,7 @@ def dg_moe_layout_contiguous(topk_idx, counts, m_indices, row_token, row_of, fir
     _check(load_library().dg_moe_layout_contiguous(
         _arg(topk_idx, "topk_idx", i32, (T, k), dev), _arg(counts, "counts", i32, (G,), dev),
         _arg(m_indices, "m_indices", i32, (M,), dev), _arg(row_token, "row_token", i32, (M,), dev),
-        _arg(row_of, "row_of", i32, (T, k), dev), T, k, first_expert, G, M, ws, ws_bytes, _raw_stream(stream)))
+        _arg(row_of, "row_of", i32, (T, k), dev), T, k, first_expert, G, M, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def dg_moe_layout_masked(topk_idx, masked_m, row_token, row_of, first_expert=0, workspace=None, stream=None):
@@ -702,7 +705,7 @@ def dg_moe_layout_masked(topk_idx, masked_m, row_token, row_of, first_expert=0, 
     _check(load_library().dg_moe_layout_masked(
         _arg(topk_idx, "topk_idx", i32, (T, k), dev), _arg(masked_m, "masked_m", i32, (G,), dev),
         _arg(row_token, "row_token", i32, (G, max_m), dev), _arg(row_of, "row_of", i32, (T, k), dev), T, k, first_expert,
-        G, max_m, ws, ws_bytes, _raw_stream(stream)))
+        G, max_m, ws, ws_bytes, _raw_stream(stream, dev)))
 
 
 def dg_moe_combine(rows, row_of, w, y, stream=None):
@@ -715,7 +718,7 @@ def dg_moe_combine(rows, row_of, w, y, stream=None):
     _check(load_library().dg_moe_combine(
         _arg(rows, "rows", torch.bfloat16, (R, N), dev), _arg(row_of, "row_of", torch.int32, (T, k), dev),
         _arg(w, "w", torch.float32, (T, k), dev), _arg(y, "y", y.dtype, (T, N), dev), dt, T, k, N, R,
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
 
 
 def dg_moe_combine_bwd(dy, rows, row_of, w, drows, dw, stream=None):
@@ -729,4 +732,4 @@ def dg_moe_combine_bwd(dy, rows, row_of, w, drows, dw, stream=None):
         _arg(dy, "dy", dy.dtype, (T, N), dev), dt, _arg(rows, "rows", torch.bfloat16, (R, N), dev),
         _arg(row_of, "row_of", torch.int32, (T, k), dev), _arg(w, "w", torch.float32, (T, k), dev),
         _arg(drows, "drows", torch.bfloat16, (R, N), dev), _arg(dw, "dw", torch.float32, (T, k), dev), T, k, N, R,
-        _raw_stream(stream)))
+        _raw_stream(stream, dev)))
