@@ -338,8 +338,9 @@ int dg_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, int dtype, in
  *   [G][K/128][max_m]): both operands scaled per row and 32 elements
  * The matrix cores apply the scales; sums are fp32, rounded once to bf16.
  * A row or column with a NaN code (255) gives NaN.  K is a positive multiple
- * of 128 up to 2^24, N of 16; no other limit on sizes (operands past 4 GiB are
- * addressed in 64 bits).  Deterministic.
+ * of 128 up to 2^24, N of 16, and the scale words of one operand (masked: of one
+ * expert) take less than 4 GiB; larger codes and outputs are addressed in 64
+ * bits.  Deterministic.
  * workspace (dense only): as for dg_fp8_gemm_nt: optional, zero-filled before
  * its first use and left reusable, full size
  * dg_get_workspace_size(DG_OP_MXFP4_GEMM_NT, M, N, K, 1).
@@ -457,7 +458,10 @@ size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t
  *                     4 wn columns (wn 16 or 32), a K split of s (bounded by
  *                     the K blocks and the workspace) and ring depth p (one
  *                     of the compiled depths; other values are ignored);
- *                     results stay within the same bounds
+ *                     "mxfp4=<bm>x<bn>" makes the microscaled 4-bit
+ *                     products use tiles of that shape (64x64, 128x256 or
+ *                     256x256) where their form has it; results stay within
+ *                     the same bounds
  *   DG_PRINT_CONFIGS  print every launch's plan on stderr
  *   DG_CHECK_LAYOUT   the contiguous forms copy m_indices to the host
  *                     (synchronising the stream; skipped while the stream is

@@ -21,7 +21,7 @@ LIB_NAME = "libdg_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip",
+SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "mxfp4_wide.hip",
            "moe_gate.hip", "moe_layout.hip", "moe_combine.hip", "api.cpp", "api_moe.cpp"]
 # per-source flags: the persistent kernels need the iterative ILP scheduler to
 # stay within 256 VGPRs (two waves per SIMD) without spilling
@@ -35,17 +35,19 @@ COMMON = [
     "-Wall",
     # packed fp32 VALU forms are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # MFMA results in VGPRs: the promotion FMAs read them without
-    # v_accvgpr_read copies and consecutive MFMAs get distinct destinations
-    "-mllvm", "-amdgpu-mfma-vgpr-form=1",
     "-I", os.path.join(ROOT, "include"),
     "-I", CSRC,
 ]
+# MFMA results in VGPRs: the promotion FMAs read them without
+# v_accvgpr_read copies and consecutive MFMAs get distinct destinations.  Not
+# for the kernel whose accumulators fill the 256 accumulation registers.
+MFMA_IN_VGPRS = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+MFMA_IN_AGPRS = {"mxfp4_wide.hip"}
 
 
 def _compile(src, build_dir, extra):
     obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *COMMON, *SOURCE_FLAGS.get(src, []), *extra, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *COMMON, *([] if src in MFMA_IN_AGPRS else MFMA_IN_VGPRS), *SOURCE_FLAGS.get(src, []), *extra, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".hip"):
         cmd.insert(1, "-Rpass-analysis=kernel-resource-usage")
     r = subprocess.run(cmd, capture_output=True, text=True)

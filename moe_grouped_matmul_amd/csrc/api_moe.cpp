@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <cstdlib>
+#include <cstring>
 
 #include "dg.h"
 #include "host.hpp"
@@ -32,6 +34,17 @@ int check_dtype(int dtype) {
 
 // ---- microscaled 4-bit products
 
+// DG_FORCE_CONFIG's "mxfp4=<bm>x<bn>": the tile shape wherever the form has it, -1 without one.
+int mx_forced_tile() {
+  const char* e = std::getenv("DG_FORCE_CONFIG");
+  const char* at = e ? std::strstr(e, "mxfp4=") : nullptr;
+  int bm = 0, bn = 0;
+  if (!at || std::sscanf(at + 6, "%dx%d", &bm, &bn) != 2) return -1;
+  for (int t : {kMx64x64, kMx128x256, kMx256x256})
+    if (bm == mx_bm(t) && bn == mx_bn(t)) return t;
+  return -1;
+}
+
 struct MxPlan {
   int tile = kMx64x64;
   int m_tiles = 0;
@@ -50,6 +63,7 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   if (M > 128 && t256 * 10 >= (int64_t)cus * 6) pl.tile = kMx256x256;
   else if (M > 64 && t128 * 10 >= (int64_t)cus * 6) pl.tile = kMx128x256;
   else pl.tile = kMx64x64;
+  if (const int f = mx_forced_tile(); f >= 0) pl.tile = f;
   pl.m_tiles = (int)ceil_div(M, mx_bm(pl.tile));
   pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
   int64_t s = 1;
@@ -62,6 +76,12 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   pl.steps_per_split = (int)ceil_div(steps, s);
   pl.splits = (int)ceil_div(steps, pl.steps_per_split);  // every split non-empty
   return pl;
+}
+
+// Contiguous: 256 x 256 tiles where they fill most of the CUs and the experts' segments are long on average (a tile
+// over a boundary between experts takes two passes).
+bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t G, int cus) {
+  return rows >= 1024 * G && ceil_div(rows, 256) * ceil_div(N, 256) * 10 >= (int64_t)cus * 6;
 }
 
 int check_mx_shape(int64_t N, int64_t K) {
@@ -93,6 +113,8 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   if (form != kMxDense && !aligned(index, 4)) return fail(DG_ERR_ALIGN, "index arrays must be 4-byte aligned");
   if (ws && (!aligned(ws, 16) || ws_bytes % 4))
     return fail(DG_ERR_WORKSPACE, "workspace must be 16-byte aligned with a size that is a multiple of 4");
+  // scale words of an operand (masked: of one expert) are addressed with 32-bit offsets, up to three rows of them past K
+  if (rows * (K / 128 + 4) * 4 >= kOffLim || N * (K / 128 + 4) * 4 >= kOffLim) return fail(DG_ERR_SHAPE, "scale arrays exceed 4 GiB");
   int cus = 0;
   if ((rc = check_device(&cus))) return rc;
   cus = effective_cus(cus);
@@ -101,6 +123,9 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     pl = plan_mx_dense(rows, N, K, cus, ws ? ws_bytes : 0);
   } else {
     pl.tile = form == kMxMasked && rows <= 256 ? kMx64x64 : kMx128x256;
+    if (form == kMxContiguous && mx_contiguous_wide(rows, N, G, cus)) pl.tile = kMx256x256;
+    const int f = mx_forced_tile();
+    if (f == kMx128x256 || (f == kMx256x256 && form == kMxContiguous) || (f == kMx64x64 && form == kMxMasked)) pl.tile = f;
     pl.m_tiles = (int)ceil_div(rows, mx_bm(pl.tile));
     pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
     pl.steps_per_split = (int)ceil_div(K, 256);
@@ -127,6 +152,11 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     std::fprintf(stderr, "[dg] mxfp4%s rows=%lld N=%lld K=%lld G=%lld tile=%dx%d tiles=%lld splits=%d\n",
                  form == kMxDense ? "" : form == kMxMasked ? "_masked" : "_contiguous", (long long)rows, (long long)N,
                  (long long)K, (long long)G, mx_bm(pl.tile), mx_bn(pl.tile), (long long)pl.m_tiles * pl.n_tiles, pl.splits);
+  if (pl.tile == kMx256x256) {
+    const int64_t tiles = (int64_t)pl.m_tiles * pl.n_tiles;
+    const int64_t least = form == kMxContiguous ? ceil_div(tiles, kMxWideMaxTiles) : 1;  // the pass table's size
+    return launched(launch_mxfp4_wide(form, (int)std::min(tiles, std::max<int64_t>(cus, least)), p, hs(stream)));
+  }
   return launched(launch_mxfp4_gemm(form, pl.tile, p, hs(stream)));
 }
 

@@ -38,6 +38,11 @@ constexpr int kMxMaxCounters = 1024;
 constexpr size_t kMxCounterBytes = 4 * kMxMaxCounters;
 // Workspace of a dense launch with splits > 1: one counter per tile, then the partials.
 size_t mx_workspace_bytes(int tile, int m_tiles, int n_tiles, int splits);
+// The persistent kernel of 256 x 256 tiles (mxfp4_wide.hip), dense or
+// contiguous: `grid` workgroups, at most kMxWideMaxTiles tiles each in the
+// contiguous form.
+constexpr int kMxWideMaxTiles = 64;
+hipError_t launch_mxfp4_wide(int form, int grid, const MxGemmParams& p, hipStream_t stream);
 hipError_t launch_mxfp4_gemm(int form, int tile, const MxGemmParams& p, hipStream_t stream);
 
 // ---- quantiser (mxfp4_quant.hip)

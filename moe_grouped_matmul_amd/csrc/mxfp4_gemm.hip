@@ -384,8 +384,7 @@ hipError_t launch_mxfp4_gemm(int form, int tile, const MxGemmParams& p, hipStrea
     return tile == kMx64x64 ? launch_mx<64, 64, 1, 4, 4, kMxMasked>(p, stream)
                             : launch_mx<128, 256, 2, 4, 3, kMxMasked>(p, stream);
   if (tile == kMx64x64) return launch_mx<64, 64, 1, 4, 4, kMxDense>(p, stream);
-  if (tile == kMx128x256) return launch_mx<128, 256, 2, 4, 3, kMxDense>(p, stream);
-  return launch_mx<256, 256, 4, 2, 2, kMxDense>(p, stream);
+  return launch_mx<128, 256, 2, 4, 3, kMxDense>(p, stream);
 }
 
 }  // namespace dg

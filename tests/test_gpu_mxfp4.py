@@ -149,6 +149,30 @@ def test_dense(M, N, K, exact):
         _check(_bits(D), ref, mag, K, exact, (M, N, K, w is None))
 
 
+TILES = ["64x64", "128x256", "256x256"]
+
+
+@pytest.mark.parametrize("tile", TILES)
+@pytest.mark.parametrize("M,N,K", [(1, 16, 128), (130, 272, 896), (600, 784, 1152), (257, 1040, 256), (1030, 2064, 2304)])
+def test_dense_tile_shapes(monkeypatch, tile, M, N, K):
+    """Every tile shape at sizes its rule would not give it: partial tiles, K an odd number of 128s, several tiles a workgroup."""
+    monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
+    rng = np.random.default_rng(M + N + K)
+    for exact in (True, False):
+        a, sa = _operand(rng, (), M, K, exact)
+        b, sb = _operand(rng, (), N, K, exact)
+        ref, mag = mxfp4.gemm_mxfp4(a, sa, b, sb)
+        for cus in (0, 3):  # 3: a persistent workgroup walks many tiles
+            dg.dg_set_num_cus(cus)
+            try:
+                D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
+                ws = torch.zeros(32 << 20, dtype=torch.uint8, device=DEV)
+                dg.dg_mxfp4_gemm_nt(*map(_t, (a, sa, b, sb)), D, workspace=ws)
+            finally:
+                dg.dg_set_num_cus(0)
+            _check(_bits(D), ref, mag, K, exact, (tile, M, N, K, cus))
+
+
 def test_dense_long_k_and_shared_workspace_bit_identical():
     M, N, K = 17, 320, 16384
     rng = np.random.default_rng(0)
@@ -196,10 +220,13 @@ CONTIG = [([5, 130, 1], 144, 256, 0), ([128, 256, 1, 300], 272, 640, 3), ([0, 0,
           ([1500, 2, 900, 1100], 4096, 384, 2)]
 
 
+@pytest.mark.parametrize("tile", [None, "128x256", "256x256"])
 @pytest.mark.parametrize("exact", [True, False])
 @pytest.mark.parametrize("counts,N,K,tail", CONTIG)
-def test_contiguous(counts, N, K, tail, exact):
+def test_contiguous(monkeypatch, counts, N, K, tail, exact, tile):
     """Segments padded to 128 rows, `tail` further padding blocks; padding rows are left untouched whatever they hold."""
+    if tile:
+        monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
     rng = np.random.default_rng(N + K)
     G = len(counts)
     idx = np.concatenate([np.concatenate((np.full(c, g), np.full(-c % 128, -1))) for g, c in enumerate(counts)] +
@@ -226,9 +253,12 @@ MASKED = [(3, 16, [16, 0, 5], 144, 256), (4, 70, [70, 1, 64, 33], 272, 896), (2,
           (2, 40, [-3, 99], 400, 1152), (2, 600, [530, 257], 272, 640)]
 
 
+@pytest.mark.parametrize("tile", [None, "64x64", "128x256"])
 @pytest.mark.parametrize("exact", [True, False])
 @pytest.mark.parametrize("G,max_m,m,N,K", MASKED)
-def test_masked(G, max_m, m, N, K, exact):
+def test_masked(monkeypatch, G, max_m, m, N, K, exact, tile):
+    if tile:
+        monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
     rng = np.random.default_rng(N + K + G)
     a, sa = _operand(rng, (G,), max_m, K, exact)
     b, sb = _operand(rng, (G,), N, K, exact)
