@@ -458,10 +458,10 @@ size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t
  *                     4 wn columns (wn 16 or 32), a K split of s (bounded by
  *                     the K blocks and the workspace) and ring depth p (one
  *                     of the compiled depths; other values are ignored);
- *                     "mxfp4=<bm>x<bn>" makes the microscaled 4-bit
+ *                     "mxfp4=<bm>x<bn>[x<s>]" makes the microscaled 4-bit
  *                     products use tiles of that shape (64x64, 128x256 or
- *                     256x256) where their form has it; results stay within
- *                     the same bounds
+ *                     256x256) where their form has it, 64x64 tiles with a
+ *                     K split of s; results stay within the same bounds
  *   DG_PRINT_CONFIGS  print every launch's plan on stderr
  *   DG_CHECK_LAYOUT   the contiguous forms copy m_indices to the host
  *                     (synchronising the stream; skipped while the stream is

@@ -34,12 +34,13 @@ int check_dtype(int dtype) {
 
 // ---- microscaled 4-bit products
 
-// DG_FORCE_CONFIG's "mxfp4=<bm>x<bn>": the tile shape wherever the form has it, -1 without one.
-int mx_forced_tile() {
+// DG_FORCE_CONFIG's "mxfp4=<bm>x<bn>[x<splits>]": the tile shape wherever the form has it, -1 without one.
+int mx_forced_tile(int* splits = nullptr) {
   const char* e = std::getenv("DG_FORCE_CONFIG");
   const char* at = e ? std::strstr(e, "mxfp4=") : nullptr;
-  int bm = 0, bn = 0;
-  if (!at || std::sscanf(at + 6, "%dx%d", &bm, &bn) != 2) return -1;
+  int bm = 0, bn = 0, sp = 0;
+  if (!at || std::sscanf(at + 6, "%dx%dx%d", &bm, &bn, &sp) < 2) return -1;
+  if (splits) *splits = sp;
   for (int t : {kMx64x64, kMx128x256, kMx256x256})
     if (bm == mx_bm(t) && bn == mx_bn(t)) return t;
   return -1;
@@ -53,23 +54,40 @@ struct MxPlan {
   int steps_per_split = 0;
 };
 
-// Dense: 256 x 256 tiles where they fill most of the CUs, else 128 x 256 ones, else 64 x 64 tiles with K
-// split until two workgroups per CU have work.
+// Estimated time (us) of a call over tiles of one shape: rounds of tiles over the CUs (two 64 x 64 workgroups to a CU),
+// a step of 256 K elements costing 0.45, 1.05 and 1.5 us a round, and the start, epilogue and last write-back. Fitted to
+// 12 shapes of 200-4096 rows with every tile shape forced; the tile of least estimate was the fastest one timed, or
+// within 5% of it, on each (4096 x 2112 x 7168: 60, 64 and 44 us; 1024 x 4096 x 7168: 29, 34 and 43; 2048 x 4096 x
+// 7168: 54, 36 and 45).
+double mx_cost_us(int tile, int64_t tiles, int64_t K, int cus) {
+  const double steps = (double)ceil_div(K, 256);
+  if (tile == kMx64x64) return (double)ceil_div(tiles, 2 * cus) * (0.45 * steps + 1.5) + 3.0;
+  if (tile == kMx128x256) return (double)ceil_div(tiles, cus) * 1.05 * steps + 8.0;
+  return (double)ceil_div(tiles, cus) * 1.5 * steps + 10.0;
+}
+
+// Dense: the tile shape of least estimated time; 64 x 64 tiles that leave CUs idle split K, each part at least four
+// steps (64 x 2112 x 7168: 11.2 us whole, 8.5 in four parts, 8.9 in eight; more parts than CUs were slower everywhere).
 MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) {
   MxPlan pl;
   const int64_t steps = ceil_div(K, 256);
-  const int64_t t256 = ceil_div(M, 256) * ceil_div(N, 256);
-  const int64_t t128 = ceil_div(M, 128) * ceil_div(N, 256);
-  if (M > 128 && t256 * 10 >= (int64_t)cus * 6) pl.tile = kMx256x256;
-  else if (M > 64 && t128 * 10 >= (int64_t)cus * 6) pl.tile = kMx128x256;
-  else pl.tile = kMx64x64;
-  if (const int f = mx_forced_tile(); f >= 0) pl.tile = f;
+  double best = -1.0;
+  for (int t : {kMx64x64, kMx128x256, kMx256x256}) {
+    const double c = mx_cost_us(t, ceil_div(M, mx_bm(t)) * ceil_div(N, mx_bn(t)), K, cus);
+    if (best < 0 || c < best) {
+      best = c;
+      pl.tile = t;
+    }
+  }
+  int forced_splits = 0;
+  if (const int f = mx_forced_tile(&forced_splits); f >= 0) pl.tile = f;
   pl.m_tiles = (int)ceil_div(M, mx_bm(pl.tile));
   pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
   int64_t s = 1;
   if (pl.tile == kMx64x64) {
     const int64_t tiles = (int64_t)pl.m_tiles * pl.n_tiles;
-    s = std::min({2 * cus / std::max<int64_t>(tiles, 1), steps / 4, (int64_t)16});
+    s = std::min({cus / std::max<int64_t>(tiles, 1), steps / 4, (int64_t)8});
+    if (forced_splits > 0) s = std::min<int64_t>(forced_splits, steps);
     if (s < 1 || tiles > kMxMaxCounters) s = 1;
     while (s > 1 && mx_workspace_bytes(pl.tile, pl.m_tiles, pl.n_tiles, (int)s) > ws_bytes) --s;
   }
@@ -78,10 +96,12 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   return pl;
 }
 
-// Contiguous: 256 x 256 tiles where they fill most of the CUs and the experts' segments are long on average (a tile
-// over a boundary between experts takes two passes).
-bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t G, int cus) {
-  return rows >= 1024 * G && ceil_div(rows, 256) * ceil_div(N, 256) * 10 >= (int64_t)cus * 6;
+// Contiguous: 256 x 256 tiles where they are estimated faster than 128 x 256 ones; a tile over a boundary between
+// experts takes two passes, and every other boundary is expected inside one.
+bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
+  const int64_t n_tiles = ceil_div(N, 256);
+  return mx_cost_us(kMx256x256, (ceil_div(rows, 256) + (G - 1) / 2) * n_tiles, K, cus) <
+         mx_cost_us(kMx128x256, ceil_div(rows, 128) * n_tiles, K, cus);
 }
 
 int check_mx_shape(int64_t N, int64_t K) {
@@ -122,8 +142,11 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   if (form == kMxDense) {
     pl = plan_mx_dense(rows, N, K, cus, ws ? ws_bytes : 0);
   } else {
-    pl.tile = form == kMxMasked && rows <= 256 ? kMx64x64 : kMx128x256;
-    if (form == kMxContiguous && mx_contiguous_wide(rows, N, G, cus)) pl.tile = kMx256x256;
+    // 128 x 256 tiles read each weight once and each row from few workgroups; 64 x 64 ones where those are too few
+    // to occupy the CUs (32 experts x 128 rows, 4096 x 7168: 94 against 144 us)
+    const int64_t t128 = G * ceil_div(rows, 128) * ceil_div(N, 256);
+    pl.tile = form == kMxMasked && t128 < cus ? kMx64x64 : kMx128x256;
+    if (form == kMxContiguous && mx_contiguous_wide(rows, N, K, G, cus)) pl.tile = kMx256x256;
     const int f = mx_forced_tile();
     if (f == kMx128x256 || (f == kMx256x256 && form == kMxContiguous) || (f == kMx64x64 && form == kMxMasked)) pl.tile = f;
     pl.m_tiles = (int)ceil_div(rows, mx_bm(pl.tile));
@@ -148,6 +171,9 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   p.n_tiles = pl.n_tiles;
   p.splits = pl.splits;
   p.steps_per_split = pl.steps_per_split;
+  // one row tile reads each weight once; weights that the 256 MB Infinity Cache cannot hold from one call to the next
+  // are streamed past it (32 experts of 4096 x 7168: 103 -> 94 us; 7168 x 16384, which it holds: 16 -> 19 us, so not there)
+  p.stream_weights = pl.m_tiles == 1 && G * N * (K / 2) >= (int64_t)256 << 20;
   if (print_configs())
     std::fprintf(stderr, "[dg] mxfp4%s rows=%lld N=%lld K=%lld G=%lld tile=%dx%d tiles=%lld splits=%d\n",
                  form == kMxDense ? "" : form == kMxMasked ? "_masked" : "_contiguous", (long long)rows, (long long)N,

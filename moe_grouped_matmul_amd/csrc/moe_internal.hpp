@@ -27,6 +27,7 @@ struct MxGemmParams {
   int n_tiles;
   int splits;
   int steps_per_split;  // K steps of 256
+  bool stream_weights;  // weight loads carry the non-temporal policy
 };
 
 enum MxForm { kMxDense = 0, kMxContiguous = 1, kMxMasked = 2 };

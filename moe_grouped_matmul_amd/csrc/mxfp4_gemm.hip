@@ -33,6 +33,7 @@ namespace {
 constexpr int kMxRsrcWord3 = 0x00020000;  // raw (untyped) buffer
 constexpr uint32_t kMxOOB = 0xFFFFFF00u;  // an offset past every buffer range used here
 constexpr int kMxCoherent = 16;           // sc1: split-K partials, coherent across the XCDs
+constexpr int kMxStream = 2;              // nt: weights that one workgroup reads once
 
 typedef unsigned int mxu32x4 __attribute__((ext_vector_type(4)));
 
@@ -45,7 +46,7 @@ struct Const {
   static constexpr int value = V;
 };
 
-template <int BM, int BN, int WM, int WN, int P, int FORM>
+template <int BM, int BN, int WM, int WN, int P, int FORM, bool NT>
 __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = WM * WN;
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p
 #pragma unroll
     for (int i = 0; i < B_INS; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (DG_LDS void*)(sl + BM * 128 + (i * NW + wave) * 1024), 16, b_off[i] | past, ks,
-                                               0, 0);
+                                               0, NT ? kMxStream : 0);
 #pragma unroll
     for (int i = 0; i < S_INS; ++i) {
       const int s = i * NW + wave;  // uniform
@@ -367,7 +368,11 @@ hipError_t launch_mx(const MxGemmParams& p, hipStream_t stream) {
     const int64_t units = (int64_t)p.n_tiles * (FORM == kMxMasked ? p.G : p.splits);
     grid = (units + 7) / 8 * 8 * p.m_tiles;
   }
-  hipLaunchKernelGGL((mxfp4_gemm_kernel<BM, BN, WM, WN, P, FORM>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, p);
+  if (FORM != kMxContiguous && p.stream_weights)
+    hipLaunchKernelGGL((mxfp4_gemm_kernel<BM, BN, WM, WN, P, FORM, FORM != kMxContiguous>), dim3((unsigned)grid),
+                       dim3(64 * WM * WN), 0, stream, p);
+  else
+    hipLaunchKernelGGL((mxfp4_gemm_kernel<BM, BN, WM, WN, P, FORM, false>), dim3((unsigned)grid), dim3(64 * WM * WN), 0, stream, p);
   return hipGetLastError();
 }
 
