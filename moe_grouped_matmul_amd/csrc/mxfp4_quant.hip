@@ -31,127 +31,191 @@ __device__ __forceinline__ int mx_code(uint32_t u) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Grid (ceil(R / 16) * (K / 128), G); a 256-thread workgroup quantises 128
-// columns of 16 consecutive rows: 16 lanes per row, 8 elements per lane, four
-// lanes per block, so the 16 rows' scale words are 64 contiguous bytes.
+// A 256-thread workgroup handles 4 PER rows x 512 columns of one group: each
+// of its four waves PER rows, every load and store of the wide side a whole
+// kilobyte (fp32 input: two, each lane 16 bytes of either), the rows of a wave
+// in flight together.  Rows per wave by measurement, 8 x 4096 x 7168: fp32
+// input 1, 2, 4 rows 190, 204, 209 us (5.6 TB/s at 1); bf16 input 113-122, 105,
+// 106 us (5.6 TB/s); reading back 146-158, 105, 106 us (5.6 TB/s).
+constexpr int kQCols = 512;
+
+// first row and column of this workgroup
+template <int ROWS>
+__device__ __forceinline__ int64_t q_place(int K, int* col) {
+  const int tiles = (K + kQCols - 1) / kQCols;
+  const int64_t rb = (int64_t)blockIdx.x / tiles;
+  *col = (int)((int64_t)blockIdx.x - rb * tiles) * kQCols;
+  return rb * ROWS;
+}
+
+// maximum with the lane that DPP control C exchanges with
+template <int C>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t u) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, C, 0xf, 0xf, true);
+  return o > u ? o : u;
+}
+
 // row_token: row r takes row row_token[r] of x, rows whose entry is outside
-// [0, T) are not written.
-template <bool BF16>
+// [0, T) are not written
+template <bool BF16, int PER>
 __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,
                                                           int32_t* __restrict__ sf, const int32_t* __restrict__ row_token,
                                                           int64_t T, int64_t R, int K) {
-  const int KB = K >> 7;
-  const int64_t rb = (int64_t)blockIdx.x / KB;
-  const int kb = (int)((int64_t)blockIdx.x - rb * KB);
-  const int sub = threadIdx.x & 15;
-  const int64_t r = rb * 16 + (threadIdx.x >> 4);
+  // 16-byte pieces of a row per lane, their elements, and the lanes of a block
+  constexpr int NP = BF16 ? 1 : 2;
+  constexpr int NE = BF16 ? 8 : 4;
+  constexpr int LPB = 32 / NE;
+  constexpr int ROWS = 4 * PER;
+  __shared__ uint32_t words[4][ROWS];
+  __shared__ int live[ROWS];
+  int col0;
+  const int64_t r0 = q_place<ROWS>(K, &col0);
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
   const int64_t g = blockIdx.y;
-  bool active = r < R;
-  int64_t src = g * R + r;
-  if (row_token) {
-    src = active ? row_token[g * R + r] : -1;
-    active = src >= 0 && src < T;
-  }
-  if (!active) src = 0;
-  const int64_t off = src * (int64_t)K + ((int64_t)kb << 7) + (sub << 3);
-  float v[8];
-  if (active) {
-    if constexpr (BF16) {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + off);
-      v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
-      v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + off);
-      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + off + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  const int KB = K >> 7;
+  bool active[PER];
+  uint4 raw[PER][NP];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int64_t r = r0 + wave * PER + i;
+    bool row = r < R;
+    int64_t src = g * R + r;
+    if (row_token) {
+      src = row ? row_token[g * R + r] : -1;
+      row = src >= 0 && src < T;
     }
-  } else {
+    active[i] = row;
+    if (lane == 0) live[wave * PER + i] = row;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  }
-  // magnitudes compare as integers, NaN above infinity above every number
-  uint32_t u = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
-    u = a > u ? a : u;
+    for (int h = 0; h < NP; ++h) {
+      const int col = col0 + h * 256 + lane * NE;
+      raw[i][h] = uint4{0u, 0u, 0u, 0u};
+      if (row && col < K)
+        raw[i][h] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + (src * (int64_t)K + col) * (BF16 ? 2 : 4));
+    }
   }
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const uint32_t a = __shfl_xor(u, o);
-    u = a > u ? a : u;
+  for (int i = 0; i < PER; ++i) {
+    const int row = wave * PER + i;
+#pragma unroll
+    for (int h = 0; h < NP; ++h) {
+      const uint4 w = raw[i][h];
+      float v[NE];
+      if constexpr (BF16) {
+        v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x); v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+        v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z); v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+      } else {
+        v[0] = __uint_as_float(w.x); v[1] = __uint_as_float(w.y); v[2] = __uint_as_float(w.z); v[3] = __uint_as_float(w.w);
+      }
+      // magnitudes compare as integers, NaN above infinity above every number
+      uint32_t u = 0;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const uint32_t a = __float_as_uint(v[e]) & 0x7fffffffu;
+        u = a > u ? a : u;
+      }
+      u = dpp_max<0xB1>(u);                       // pairs of lanes
+      u = dpp_max<0x4E>(u);                       // pairs of pairs
+      if constexpr (LPB == 8) u = dpp_max<0x141>(u);  // the quads of eight
+      const int c = mx_code(u);
+      uint32_t out = 0;
+      if (c != 255) {
+        const float inv = __builtin_ldexpf(1.0f, 127 - c);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0] * inv, v[1] * inv, 1.0f, 0);
+        out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2] * inv, v[3] * inv, 1.0f, 1);
+        if constexpr (BF16) {
+          out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4] * inv, v[5] * inv, 1.0f, 2);
+          out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6] * inv, v[7] * inv, 1.0f, 3);
+        }
+      }
+      const int col = col0 + h * 256 + lane * NE;
+      uint8_t* dst = q + (g * R + r0 + row) * (int64_t)(K >> 1) + (col >> 1);
+      if constexpr (BF16) {
+        if (active[i] && col < K) *reinterpret_cast<uint32_t*>(dst) = out;
+      } else {  // the even lane stores its neighbour's four codes too
+        out |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)out, 0xB1, 0xf, 0xf, true) << 16;
+        if (active[i] && col < K && (lane & 1) == 0) *reinterpret_cast<uint32_t*>(dst) = out;
+      }
+      const int blk = (h * 256 + lane * NE) >> 5;  // of the row's 16
+      if (lane % LPB == 0) reinterpret_cast<uint8_t*>(&words[blk >> 2][row])[blk & 3] = (uint8_t)c;
+    }
   }
-  const int c = mx_code(u);
-  const float inv = c == 255 ? 0.f : __builtin_ldexpf(1.0f, 127 - c);
-  uint32_t out = 0;
-  if (c != 255) {
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[0] * inv, v[1] * inv, 1.0f, 0);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[2] * inv, v[3] * inv, 1.0f, 1);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[4] * inv, v[5] * inv, 1.0f, 2);
-    out = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(out, v[6] * inv, v[7] * inv, 1.0f, 3);
+  __syncthreads();
+  if (threadIdx.x < 4 * ROWS) {  // the rows' words of one 128 are contiguous
+    const int row = threadIdx.x & (ROWS - 1);
+    const int kb = (col0 >> 7) + threadIdx.x / ROWS;
+    if (live[row] && kb < KB) sf[(g * KB + kb) * R + r0 + row] = (int32_t)words[threadIdx.x / ROWS][row];
   }
-  // the four blocks' codes (lanes 0, 4, 8, 12 of the row) into one word
-  uint32_t word = (uint32_t)c << (8 * (sub >> 2));
-  word |= __shfl_xor(word, 4);
-  word |= __shfl_xor(word, 8);
-  if (!active) return;
-  *reinterpret_cast<uint32_t*>(q + (g * R + r) * (int64_t)(K >> 1) + ((int64_t)kb << 6) + (sub << 2)) = out;
-  if (sub == 0) sf[(g * KB + kb) * R + r] = (int32_t)word;
 }
 
-// the same grid; a lane reads 8 codes and its block's scale byte
-template <bool BF16>
+template <bool BF16, int PER>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t* __restrict__ q, const int32_t* __restrict__ sf,
                                                             void* __restrict__ y, int64_t R, int K) {
-  const int KB = K >> 7;
-  const int64_t rb = (int64_t)blockIdx.x / KB;
-  const int kb = (int)((int64_t)blockIdx.x - rb * KB);
-  const int sub = threadIdx.x & 15;
-  const int64_t r = rb * 16 + (threadIdx.x >> 4);
+  int col;
+  int64_t r0 = q_place<4 * PER>(K, &col);
+  const int lane = threadIdx.x & 63;
   const int64_t g = blockIdx.y;
-  if (r >= R) return;
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(q + (g * R + r) * (int64_t)(K >> 1) + ((int64_t)kb << 6) + (sub << 2));
-  const uint32_t c = ((uint32_t)sf[(g * KB + kb) * R + r] >> (8 * (sub >> 2))) & 255u;
-  const float s = c == 255 ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(1.0f, (int)c - 127);
-  float v[8];
+  r0 += (threadIdx.x >> 6) * PER;
+  col += lane * 8;
+  uint32_t code[PER], word[PER];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // e2m1 magnitude m: m < 2 is m / 2 (subnormal), else 2^(m / 2 - 1) * (1 + (m % 2) / 2)
-    const uint32_t n = (w >> (4 * i)) & 15u;
-    const uint32_t m = n & 7u;
-    const float a = m < 2 ? 0.5f * (float)m : __uint_as_float((126u << 23) + (m << 22));
-    v[i] = (n & 8u ? -a : a) * s;
+  for (int i = 0; i < PER; ++i) {
+    const bool in = col < K && r0 + i < R;
+    code[i] = in ? *reinterpret_cast<const uint32_t*>(q + (g * R + r0 + i) * (int64_t)(K >> 1) + (col >> 1)) : 0u;
+    word[i] = in ? (uint32_t)sf[(g * (K >> 7) + (col >> 7)) * R + r0 + i] : 0u;
   }
-  const int64_t off = (g * R + r) * (int64_t)K + ((int64_t)kb << 7) + (sub << 3);
-  if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off) =
-        uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-  } else {
-    float* d = static_cast<float*>(y) + off;
-    *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const uint32_t w = code[i];
+    const uint32_t c = (word[i] >> (8 * ((lane >> 2) & 3))) & 255u;
+    const float s = c == 255 ? __uint_as_float(0x7fc00000u) : __builtin_ldexpf(1.0f, (int)c - 127);
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // e2m1 magnitude m: m < 2 is m / 2 (subnormal), else 2^(m / 2 - 1) * (1 + (m % 2) / 2)
+      const uint32_t n = (w >> (4 * e)) & 15u;
+      const uint32_t m = n & 7u;
+      const uint32_t a = m < 2 ? m * 0x3f000000u : (126u << 23) + (m << 22);
+      v[e] = __uint_as_float(a | ((n & 8u) << 28)) * s;
+    }
+    if (col >= K || r0 + i >= R) continue;
+    const int64_t off = (g * R + r0 + i) * (int64_t)K + col;
+    if constexpr (BF16) {
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off) =
+          uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    } else {
+      float* d = static_cast<float*>(y) + off;
+      *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    }
   }
+}
+
+template <int PER>
+dim3 q_grid(int64_t G, int64_t R, int64_t K) {
+  return dim3((unsigned)((R + 4 * PER - 1) / (4 * PER) * ((K + kQCols - 1) / kQCols)), (unsigned)G);
 }
 
 }  // namespace
 
 hipError_t launch_quant_mxfp4(const void* x, bool bf16, uint8_t* q, int32_t* sf, const int32_t* row_token, int64_t G,
                               int64_t T, int64_t R, int64_t K, hipStream_t stream) {
-  const dim3 grid((unsigned)((R + 15) / 16 * (K / 128)), (unsigned)G);
   if (bf16)
-    hipLaunchKernelGGL(quant_mxfp4_kernel<true>, grid, dim3(256), 0, stream, x, q, sf, row_token, T, R, (int)K);
+    hipLaunchKernelGGL((quant_mxfp4_kernel<true, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, x, q, sf, row_token, T, R,
+                       (int)K);
   else
-    hipLaunchKernelGGL(quant_mxfp4_kernel<false>, grid, dim3(256), 0, stream, x, q, sf, row_token, T, R, (int)K);
+    hipLaunchKernelGGL((quant_mxfp4_kernel<false, 1>), q_grid<1>(G, R, K), dim3(256), 0, stream, x, q, sf, row_token, T, R,
+                       (int)K);
   return hipGetLastError();
 }
 
 hipError_t launch_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, bool bf16, int64_t G, int64_t R,
                                 int64_t K, hipStream_t stream) {
-  const dim3 grid((unsigned)((R + 15) / 16 * (K / 128)), (unsigned)G);
   if (bf16)
-    hipLaunchKernelGGL(dequant_mxfp4_kernel<true>, grid, dim3(256), 0, stream, q, sf, y, R, (int)K);
+    hipLaunchKernelGGL((dequant_mxfp4_kernel<true, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, q, sf, y, R, (int)K);
   else
-    hipLaunchKernelGGL(dequant_mxfp4_kernel<false>, grid, dim3(256), 0, stream, q, sf, y, R, (int)K);
+    hipLaunchKernelGGL((dequant_mxfp4_kernel<false, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, q, sf, y, R, (int)K);
   return hipGetLastError();
 }
 
