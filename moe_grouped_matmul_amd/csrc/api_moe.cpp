@@ -255,7 +255,8 @@ int check_combine(int dtype, int64_t T, int64_t k, int64_t N, int64_t R) {
   if (T > kIntMax) return fail(DG_ERR_SHAPE, "T too large");
   if ((rc = check_topk(T, k))) return rc;
   if (N <= 0 || N % 16) return fail(DG_ERR_SHAPE, "N must be a positive multiple of 16 (got %lld)", (long long)N);
-  if (N > (int64_t)1 << 30 || R < 0 || R > kIntMax) return fail(DG_ERR_SHAPE, "N or row count out of range");
+  if (N > (int64_t)1 << 30 || R < 0 || R > kIntMax || T * ceil_div(N, 2048) > kIntMax)
+    return fail(DG_ERR_SHAPE, "N or row count out of range");
   return DG_OK;
 }
 

@@ -22,30 +22,46 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
-// one workgroup per token, 8 columns per thread and pass
+// T * ceil(N / 2048) workgroups: a thread holds 8 columns of one token and has the
+// rows of eight choices in flight; a choice without a row reads nothing.
+constexpr int kCombBatch = 8;
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, void* __restrict__ y, int k, int N,
-                                                      int64_t R) {
-  const int64_t t = blockIdx.x;
-  for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < k; ++j) {
-      const int64_t r = row_of[t * k + j];
-      if (r < 0 || r >= R) continue;
-      const float wj = w[t * k + j];
-      float v[8];
-      bf16x8(*reinterpret_cast<const uint4*>(rows + r * N + c), v);
+                                                      int64_t R, int parts) {
+  const int64_t t = blockIdx.x / parts;
+  const int c = (int)(blockIdx.x - t * parts) * 2048 + threadIdx.x * 8;
+  if (c >= N) return;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < k; j0 += kCombBatch) {
+    uint4 raw[kCombBatch];
+    float wj[kCombBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(wj, v[i], s[i]);
+    for (int j = 0; j < kCombBatch; ++j) {
+      raw[j] = uint4{0u, 0u, 0u, 0u};
+      wj[j] = 0.f;
+      if (j0 + j < k) {  // uniform, and so is the row
+        const int64_t r = row_of[t * k + j0 + j];
+        if (r >= 0 && r < R) {
+          wj[j] = w[t * k + j0 + j];
+          raw[j] = *reinterpret_cast<const uint4*>(rows + r * N + c);
+        }
+      }
     }
-    if constexpr (BF16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + t * N + c) = pack8(s);
-    } else {
-      float* d = static_cast<float*>(y) + t * N + c;
-      *reinterpret_cast<float4*>(d) = make_float4(s[0], s[1], s[2], s[3]);
-      *reinterpret_cast<float4*>(d + 4) = make_float4(s[4], s[5], s[6], s[7]);
+#pragma unroll
+    for (int j = 0; j < kCombBatch; ++j) {
+      float v[8];
+      bf16x8(raw[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = __builtin_fmaf(wj[j], v[i], s[i]);
     }
+  }
+  if constexpr (BF16) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + t * N + c) = pack8(s);
+  } else {
+    float* d = static_cast<float*>(y) + t * N + c;
+    *reinterpret_cast<float4*>(d) = make_float4(s[0], s[1], s[2], s[3]);
+    *reinterpret_cast<float4*>(d + 4) = make_float4(s[4], s[5], s[6], s[7]);
   }
 }
 
@@ -93,10 +109,13 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
 
 hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
                           int64_t k, int64_t N, int64_t R, hipStream_t stream) {
+  const int parts = (int)((N + 2047) / 2048);
   if (bf16_y)
-    hipLaunchKernelGGL(combine_kernel<true>, dim3((unsigned)T), dim3(256), 0, stream, rows, row_of, w, y, (int)k, (int)N, R);
+    hipLaunchKernelGGL(combine_kernel<true>, dim3((unsigned)(T * parts)), dim3(256), 0, stream, rows, row_of, w, y, (int)k,
+                       (int)N, R, parts);
   else
-    hipLaunchKernelGGL(combine_kernel<false>, dim3((unsigned)T), dim3(256), 0, stream, rows, row_of, w, y, (int)k, (int)N, R);
+    hipLaunchKernelGGL(combine_kernel<false>, dim3((unsigned)(T * parts)), dim3(256), 0, stream, rows, row_of, w, y, (int)k,
+                       (int)N, R, parts);
   return hipGetLastError();
 }
 
