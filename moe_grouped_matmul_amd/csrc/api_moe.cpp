@@ -96,11 +96,11 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   return pl;
 }
 
-// Contiguous: 256 x 256 tiles where they are estimated faster than 128 x 256 ones; a tile over a boundary between
-// experts takes two passes, and every other boundary is expected inside one.
+// Contiguous: 256 x 256 tiles where they are estimated faster than 128 x 256 ones; an expert with an odd number of
+// 128-row blocks, every other one, costs half a tile more.
 bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
   const int64_t n_tiles = ceil_div(N, 256);
-  return mx_cost_us(kMx256x256, (ceil_div(rows, 256) + (G - 1) / 2) * n_tiles, K, cus) <
+  return mx_cost_us(kMx256x256, (ceil_div(rows, 256) + G / 4) * n_tiles, K, cus) <
          mx_cost_us(kMx128x256, ceil_div(rows, 128) * n_tiles, K, cus);
 }
 
@@ -148,7 +148,7 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     pl.tile = form == kMxMasked && t128 < cus ? kMx64x64 : kMx128x256;
     if (form == kMxContiguous && mx_contiguous_wide(rows, N, K, G, cus)) pl.tile = kMx256x256;
     const int f = mx_forced_tile();
-    if (f == kMx128x256 || (f == kMx256x256 && form == kMxContiguous) || (f == kMx64x64 && form == kMxMasked)) pl.tile = f;
+    if (f == kMx128x256 || f == (form == kMxContiguous ? kMx256x256 : kMx64x64)) pl.tile = f;
     pl.m_tiles = (int)ceil_div(rows, mx_bm(pl.tile));
     pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
     pl.steps_per_split = (int)ceil_div(K, 256);
@@ -158,6 +158,7 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   MxGemmParams p{};
   p.A = A;
   p.sfa = sfa;
+  p.sfa_ld = rows;
   p.B = B;
   p.sfb = sfb;
   p.D = D;
@@ -178,12 +179,20 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     std::fprintf(stderr, "[dg] mxfp4%s rows=%lld N=%lld K=%lld G=%lld tile=%dx%d tiles=%lld splits=%d\n",
                  form == kMxDense ? "" : form == kMxMasked ? "_masked" : "_contiguous", (long long)rows, (long long)N,
                  (long long)K, (long long)G, mx_bm(pl.tile), mx_bn(pl.tile), (long long)pl.m_tiles * pl.n_tiles, pl.splits);
-  if (pl.tile == kMx256x256) {
-    const int64_t tiles = (int64_t)pl.m_tiles * pl.n_tiles;
-    const int64_t least = form == kMxContiguous ? ceil_div(tiles, kMxWideMaxTiles) : 1;  // the pass table's size
-    return launched(launch_mxfp4_wide(form, (int)std::min(tiles, std::max<int64_t>(cus, least)), p, hs(stream)));
+  if (pl.tile != kMx256x256) return launched(launch_mxfp4_gemm(form, pl.tile, p, hs(stream)));
+  // persistent tiles; the contiguous form lists a launch's 128-row blocks in LDS, so longer calls run in chunks of rows
+  const int64_t chunk = form == kMxContiguous ? (int64_t)kMxWideMaxBlocks * 128 : rows;
+  for (int64_t r0 = 0; r0 < rows; r0 += chunk) {
+    p.rows = std::min(chunk, rows - r0);
+    p.A = A + r0 * (K / 2);
+    p.sfa = sfa + r0;
+    p.D = D + r0 * N;
+    p.index = index ? index + r0 : nullptr;
+    const int64_t tiles = ceil_div(p.rows, 128) * pl.n_tiles;
+    const hipError_t e = launch_mxfp4_wide(form, (int)std::min<int64_t>(tiles, cus), p, hs(stream));
+    if (e != hipSuccess) return launched(e);
   }
-  return launched(launch_mxfp4_gemm(form, pl.tile, p, hs(stream)));
+  return ok();
 }
 
 int check_quant(int dtype, int64_t G, int64_t R, int64_t K) {

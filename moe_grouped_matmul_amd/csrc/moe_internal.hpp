@@ -19,7 +19,8 @@ struct MxGemmParams {
   uint16_t* D;
   void* ws;              // dense, splits > 1: counters then fp32 partials
   const int32_t* index;  // m_indices (contiguous) or masked_m (masked)
-  int64_t rows;          // M, M_total or max_m
+  int64_t rows;          // M, M_total or max_m (of one launch)
+  int64_t sfa_ld;        // words between consecutive 128s of A's scales: the caller's row count
   int N;
   int K;
   int G;
@@ -39,10 +40,10 @@ constexpr int kMxMaxCounters = 1024;
 constexpr size_t kMxCounterBytes = 4 * kMxMaxCounters;
 // Workspace of a dense launch with splits > 1: one counter per tile, then the partials.
 size_t mx_workspace_bytes(int tile, int m_tiles, int n_tiles, int splits);
-// The persistent kernel of 256 x 256 tiles (mxfp4_wide.hip), dense or
-// contiguous: `grid` workgroups, at most kMxWideMaxTiles tiles each in the
-// contiguous form.
-constexpr int kMxWideMaxTiles = 64;
+// The persistent kernel of 256 x 256 and 128 x 256 tiles (mxfp4_wide.hip),
+// dense or contiguous, over p.n_tiles column tiles with `grid` workgroups.  One
+// contiguous launch has at most kMxWideMaxBlocks 128-row blocks.
+constexpr int kMxWideMaxBlocks = 2048;
 hipError_t launch_mxfp4_wide(int form, int grid, const MxGemmParams& p, hipStream_t stream);
 hipError_t launch_mxfp4_gemm(int form, int tile, const MxGemmParams& p, hipStream_t stream);
 

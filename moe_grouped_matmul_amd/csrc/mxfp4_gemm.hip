@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p
   const int N = p.N;
   const int kbytes = p.K >> 1;  // bytes per operand row
   const int KB = p.K >> 7;      // scale words per row
-  const int64_t ld = p.rows;    // words between the scale words of consecutive halves of A
+  const int64_t ld = p.rows;    // rows of A (of one expert)
   int rows = (int)(p.rows - (int64_t)mt * BM < BM ? p.rows - (int64_t)mt * BM : BM);
   int64_t row0 = (int64_t)mt * BM;
   const uint8_t* A = p.A;
@@ -388,8 +388,8 @@ hipError_t launch_mxfp4_gemm(int form, int tile, const MxGemmParams& p, hipStrea
   if (form == kMxMasked)
     return tile == kMx64x64 ? launch_mx<64, 64, 1, 4, 4, kMxMasked>(p, stream)
                             : launch_mx<128, 256, 2, 4, 3, kMxMasked>(p, stream);
-  if (tile == kMx64x64) return launch_mx<64, 64, 1, 4, 4, kMxDense>(p, stream);
-  return launch_mx<128, 256, 2, 4, 3, kMxDense>(p, stream);
+  return tile == kMx64x64 ? launch_mx<64, 64, 1, 4, 4, kMxDense>(p, stream)
+                          : launch_mx<128, 256, 2, 4, 3, kMxDense>(p, stream);
 }
 
 }  // namespace dg

@@ -1,16 +1,14 @@
 // Large products of microscaled 4-bit operands for gfx950 (the operation of
-// mxfp4_gemm.hip): a persistent workgroup of four waves, one per SIMD, walks
-// 256 x 256 output tiles.
+// mxfp4_gemm.hip), dense and contiguous: a persistent workgroup of four waves,
+// one per SIMD, walks output tiles of 256 x 256 and then of 128 x 256.
 //
-// Each wave holds 128 x 128 of the tile: 8 x 8 accumulators of
-// v_mfma_scale_f32_16x16x128_f8f6f4 in the 256 accumulation registers, so a
-// step of 256 K elements reads (128 + 128) x 128 bytes of LDS for 128 matrix
-// instructions.  Eight waves of 64 x 128 would read half as much again, and
-// LDS reads plus the writes of the loads would then take as many cycles as the
-// matrix instructions do.  With one wave per SIMD nothing hides a wait, so the
-// operands of a half step (128 K elements, 64 matrix instructions) are read
-// during the half step before it, a few instructions after each
-// matrix instruction:
+// A wave holds 128 rows of the tile and 128 of its columns (256 x 256) or 64
+// (128 x 256): 8 x 8 or 8 x 4 accumulators of v_mfma_scale_f32_16x16x128_f8f6f4
+// in the accumulation registers.  For the large tile a step of 256 K elements
+// reads (128 + 128) x 128 bytes of LDS per 128 matrix instructions.  With one
+// wave per SIMD nothing hides a wait, so the operands of a half step (128 K
+// elements) are read during the half step before it, a few instructions after
+// each matrix instruction:
 //
 //   matrix instructions   first half of j | second half of j | first half of j + 1
 //   LDS reads             second half of j | first half of j + 1
@@ -20,9 +18,18 @@
 // of step j + 1 have landed, so the slot of step j is free for step j + 2 and
 // two slots (136 KB) keep a whole step of loads in flight.
 //
-// Contiguous form: only aligned 128-row blocks hold rows of one expert, so a
-// tile whose two blocks belong to different experts is two passes.  Every
-// workgroup lists its passes (tile, expert, rows tagged with it) in LDS first.
+// Measured (4096 x 4096 x 7168): 3050 cycles a step, of which the matrix cores
+// are busy 2048 and the waves wait 130, at a clock of 1.9 GHz.  32 x 32 x 64
+// instructions take 2850 cycles a step at 1.7 GHz and the same time: the clock
+// follows the power, and that is what bounds the kernel.
+//
+// Tiles.  Contiguous: only aligned 128-row blocks hold rows of one expert, so
+// every workgroup reads m_indices at its start and pairs the blocks of each run
+// of one expert from the run's first block on; an odd one is a tile of 128
+// rows.  Dense: a last tile of up to 128 rows.  The large tiles are walked in
+// rounds of one per workgroup; the tiles of a last, partial round and the small
+// ones go to the workgroups with the least work, the former cut in two where
+// everything left then fits one round of small tiles.
 
 #include <utility>
 
@@ -69,6 +76,8 @@ struct Scales {
   int a[8], b[8];
 };
 
+constexpr int kNone = 0xFFFF;
+
 template <int FORM>
 __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -78,19 +87,16 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   constexpr int S_INS = 2 * (BM + BN) / 64 / NW;
   constexpr int SLOT_S = (BM + BN) * 128;
   constexpr int SLOT = SLOT_S + 2 * (BM + BN) * 4;
-  constexpr int MAXT = kMxWideMaxTiles;
+  constexpr int MAXB = CONTIG ? kMxWideMaxBlocks : 1;
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[SLOT];
   __shared__ __attribute__((aligned(1024))) uint8_t slot1[SLOT];
-  __shared__ int pass_tile[CONTIG ? 2 * MAXT : 1];
-  __shared__ int pass_exp[CONTIG ? 2 * MAXT : 1];
-  __shared__ unsigned long long pass_mask[CONTIG ? 2 * MAXT : 1][4];  // tagged rows, 64 a word
-  __shared__ int tile_np[CONTIG ? MAXT + 1 : 1];
+  __shared__ uint16_t expert_of[MAXB];  // contiguous: of each 128-row block
+  __shared__ uint16_t large_at[MAXB], small_at[MAXB];  // first blocks of the tiles
+  __shared__ int listed[2];
 
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1;
-  const int wn = wave & 1;
   const int q = lane >> 4;
   const int q16 = lane & 15;
   const int N = p.N;
@@ -98,76 +104,125 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   const int KB = p.K >> 7;
   const int steps = (KB + 3) >> 2 << 1;  // of 256 elements, even: a last one past K is zeros
   const int64_t M = p.rows;
-  const int T = p.m_tiles * p.n_tiles;
+  const uint32_t ld = (uint32_t)p.sfa_ld;
+  const int n_tiles = p.n_tiles;
   const int G = (int)gridDim.x;
   const int bid = (int)blockIdx.x;
-  const int n_tiles = bid < T ? (T - bid + G - 1) / G : 0;  // tiles of this workgroup
-  if (n_tiles == 0) return;
-  auto tile_mn = [&](int s, int* mt, int* nt) { grouped_mn(round_tile(bid, s, G, T), p.m_tiles, p.n_tiles, 4, mt, nt); };
 
-  int nseg = n_tiles;
+  // row tiles: large ones and small ones
+  int n_large, n_small;
   if constexpr (CONTIG) {
-    // experts of the tile's two 128-row blocks (-1: no tagged row) and the lane's four rows
-    auto experts = [&](int s, int* x, int* e) {
-      int mt, nt;
-      tile_mn(s, &mt, &nt);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t r = (int64_t)mt * BM + 64 * k + lane;
-        const int v = r < M ? p.index[r] : -1;
-        x[k] = v >= 0 && v < p.G ? v : -1;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int v = x[2 * h] > x[2 * h + 1] ? x[2 * h] : x[2 * h + 1];
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-          const int u = __shfl_xor(v, o);
-          v = u > v ? u : v;
-        }
-        e[h] = v;
-      }
-      return (e[0] >= 0 ? 1 : 0) + (e[1] >= 0 && e[1] != e[0] ? 1 : 0);
-    };
-    for (int s = wave; s < n_tiles; s += NW) {
-      int x[4], e[2];
-      const int n = experts(s, x, e);
-      if (lane == 0) tile_np[s] = n;
+    const int nb = (int)((M + 127) >> 7);
+    // a block's expert is that of its first row, or (padding there) of any row: a thread per block, then a wave per
+    // block for those without one, eight blocks in flight
+    for (int b = tid; b < nb; b += 64 * NW) {
+      const int x = p.index[(int64_t)b * 128];
+      expert_of[b] = (uint16_t)(x >= 0 && x < p.G ? x : kNone);
     }
     __syncthreads();
-    if (wave == 0) {  // exclusive prefix (n_tiles <= MAXT = 64)
-      const int own = lane < n_tiles ? tile_np[lane] : 0;
-      int c = own;
+    for (int b0 = wave; b0 < nb; b0 += 8 * NW) {
+      int x[8][2];
 #pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(c, o);
-        if (lane >= o) c += u;
-      }
-      if (lane < n_tiles) tile_np[lane] = c - own;
-      if (lane == 63) tile_np[MAXT] = c;
-    }
-    __syncthreads();
-    for (int s = wave; s < n_tiles; s += NW) {
-      int x[4], e[2];
-      const int n = experts(s, x, e);
-      const int first = tile_np[s];
-      for (int i = 0; i < n; ++i) {
-        const int ex = i == 0 && e[0] >= 0 ? e[0] : e[1];
-        unsigned long long m[4];
+      for (int i = 0; i < 8; ++i) {
+        const int b = b0 + i * NW;
+        const bool open = b < nb && __builtin_amdgcn_readfirstlane((int)expert_of[b < nb ? b : 0]) == kNone;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m[k] = __ballot(x[k] == ex);
-        if (lane == 0) {
-          pass_tile[first + i] = s;
-          pass_exp[first + i] = ex;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) pass_mask[first + i][k] = m[k];
+        for (int h = 0; h < 2; ++h) {
+          const int64_t r = (int64_t)b * 128 + 64 * h + lane;
+          x[i][h] = open && r < M ? p.index[r] : -1;
         }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int v = x[i][h];
+          const unsigned long long m = __ballot(v >= 0 && v < p.G);
+          if (m != 0ull && lane == __builtin_ctzll(m)) expert_of[b0 + i * NW] = (uint16_t)v;
+        }
     }
     __syncthreads();
-    nseg = __builtin_amdgcn_readfirstlane(tile_np[MAXT]);
-    if (nseg == 0) return;  // only padding
+    if (wave == 0) {
+      int run = 0, nl = 0, ns = 0;  // first block of the current run, tiles so far
+      for (int b0 = 0; b0 < nb; b0 += 64) {
+        const int b = b0 + lane;
+        const int e = b < nb ? expert_of[b] : kNone;
+        const int before = b > 0 && b < nb ? expert_of[b - 1] : kNone;
+        const int after = b + 1 < nb ? expert_of[b + 1] : kNone;
+        int first = e != before || b == 0 ? b : -1;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+          const int u = __shfl_up(first, o);
+          if (lane >= o && u > first) first = u;
+        }
+        if (first < 0) first = run;  // the run began in an earlier group of blocks
+        run = __shfl(first, 63);
+        const bool heads = e != kNone && ((b - first) & 1) == 0;
+        const unsigned long long below = (1ull << lane) - 1ull;
+        const unsigned long long ml = __ballot(heads && after == e);
+        const unsigned long long ms = __ballot(heads && after != e);
+        if ((ml >> lane) & 1ull) large_at[nl + __popcll(ml & below)] = (uint16_t)b;
+        if ((ms >> lane) & 1ull) small_at[ns + __popcll(ms & below)] = (uint16_t)b;
+        nl += __popcll(ml);
+        ns += __popcll(ms);
+      }
+      if (lane == 0) {
+        listed[0] = nl;
+        listed[1] = ns;
+      }
+    }
+    __syncthreads();
+    n_large = __builtin_amdgcn_readfirstlane(listed[0]);
+    n_small = __builtin_amdgcn_readfirstlane(listed[1]);
+  } else {
+    n_large = (int)((M + 127) >> 8);  // a rest of up to 128 rows is a small tile
+    n_small = (M & 255) >= 1 && (M & 255) <= 128 ? 1 : 0;
   }
+
+  // tiles of this workgroup: whole rounds of large ones, then what is left
+  const int T = n_large * n_tiles;
+  const int rounds = T / G;
+  const int rest = T - rounds * G;
+  const bool cut = rest > 0 && 2 * rest + n_small * n_tiles <= G;
+  const int S = n_small * n_tiles + (cut ? 2 * rest : 0);  // small tiles, the halves of the cut ones last
+  const int own_large = rounds + (!cut && bid < rest ? 1 : 0);
+  const bool spread = rest > 0 && !cut;  // workgroups without a tile of the last round take two small ones first
+  auto small_id = [&](int i) MW_INLINE {
+    if (!spread) return bid + i * G;
+    if (bid < rest) return 2 * (G - rest) + bid + i * G;
+    return i < 2 ? bid - rest + i * (G - rest) : 2 * (G - rest) + bid + (i - 2) * G;
+  };
+  int own_small = 0;
+  while (small_id(own_small) < S) ++own_small;
+  const int units = own_large + own_small;
+  if (units == 0) return;
+  // unit u: first row, rows, column tile, expert
+  auto unit = [&](int u, int64_t* row0, int* rows, int* nt, int* e) MW_INLINE {
+    int b, blocks = 2;
+    if (u < own_large) {
+      int mt;
+      grouped_mn(round_tile(bid, u, G, T), n_large, n_tiles, 4, &mt, nt);
+      b = CONTIG ? (int)large_at[CONTIG ? mt : 0] : 2 * mt;
+    } else {
+      const int i = small_id(u - own_large);
+      blocks = 1;
+      if (i < n_small * n_tiles) {
+        const int st = i / n_tiles;
+        *nt = i - st * n_tiles;
+        b = CONTIG ? (int)small_at[CONTIG ? st : 0] : 2 * n_large;
+      } else {
+        const int c = i - n_small * n_tiles;
+        int mt;
+        grouped_mn(rounds * G + (c >> 1), n_large, n_tiles, 4, &mt, nt);
+        b = (CONTIG ? (int)large_at[CONTIG ? mt : 0] : 2 * mt) + (c & 1);
+      }
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    *row0 = (int64_t)b * 128;
+    const int64_t left = M - *row0;
+    *rows = left < blocks * 128 ? (left < 0 ? 0 : (int)left) : blocks * 128;
+    *e = CONTIG ? __builtin_amdgcn_readfirstlane((int)expert_of[CONTIG ? b : 0]) : 0;
+  };
 
   // ---- loads.  A 1 KB load fills 8 LDS rows: lane l writes row l / 8, position l % 8, from K chunk (l % 8) ^ (l / 8).
   // Wave w fills rows 64 w + 8 i of A and of B in load i; B's row 64 w + in holds the column that makes a lane's
@@ -184,21 +239,15 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   const uint32_t sb_off = 4u * (uint32_t)(64 * wave + 16 * (q16 >> 2) + 4 * q + (q16 & 3));
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   int is_seg = 0;
+  int64_t row0 = 0;  // of the unit at the issue pointer
+  int rows = 0, nt = 0, e = 0;
   auto is_setup = [&]() MW_INLINE {
-    int mt, nt, e = 0;
-    if constexpr (CONTIG) {
-      tile_mn(__builtin_amdgcn_readfirstlane(pass_tile[is_seg]), &mt, &nt);
-      e = __builtin_amdgcn_readfirstlane(pass_exp[is_seg]);
-    } else {
-      tile_mn(is_seg, &mt, &nt);
-    }
-    const int64_t row0 = (int64_t)mt * BM;
-    const int rows = M - row0 < BM ? (int)(M - row0) : BM;
+    unit(is_seg, &row0, &rows, &nt, &e);
     const int n0 = nt * BN;
     const int cols = N - n0 < BN ? N - n0 : BN;
     ra = mw_rsrc(p.A + row0 * kbytes, (uint32_t)rows * (uint32_t)kbytes);
     rb = mw_rsrc(p.B + ((int64_t)e * N + n0) * kbytes, (uint32_t)cols * (uint32_t)kbytes);
-    rsa = mw_rsrc(p.sfa + row0, ((uint32_t)(KB - 1) * (uint32_t)M + (uint32_t)rows) * 4u);
+    rsa = mw_rsrc(p.sfa + row0, ((uint32_t)(KB - 1) * ld + (uint32_t)rows) * 4u);
     rsb = mw_rsrc(p.sfb + (int64_t)e * N * KB + n0, ((uint32_t)(KB - 1) * (uint32_t)N + (uint32_t)cols) * 4u);
   };
   is_setup();
@@ -223,7 +272,7 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
       constexpr int i = n - 2 * INS;  // half i / 2 of A (even i) or B
       constexpr int at = SLOT_S + (i >> 1) * (BM + BN) * 4 + (i & 1) * BM * 4;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(i & 1 ? rsb : rsa, (DG_LDS void*)(sl + at + wave * 256), 4, i & 1 ? sb_off : sa_off,
-                                               (int)((uint32_t)(2 * k + (i >> 1)) * 4u * (uint32_t)(i & 1 ? (int64_t)N : M)), 0, 0);
+                                               (int)((uint32_t)(2 * k + (i >> 1)) * 4u * (i & 1 ? (uint32_t)N : ld)), 0, 0);
     }
   };
 
@@ -231,21 +280,24 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   // their scale bytes are neighbours and one 2-byte read serves both halves.
   const uint32_t fr0 = (uint32_t)(q16 * 128 + (((2 * q) ^ (lane & 7)) << 4));
   const uint32_t fr1 = (uint32_t)(q16 * 128 + (((2 * q + 1) ^ (lane & 7)) << 4));
-  const uint32_t a_base = (uint32_t)(wm * 128 * 128);
-  const uint32_t b_base = (uint32_t)(BM * 128 + wn * 128 * 128);
+  // the wave's first LDS row of A and of B: (128 rows, 128 columns) of a large tile, (all 128 rows, 64 columns) of a small one
   const uint32_t s_base = (uint32_t)(SLOT_S + (q >> 1) * (BM + BN) * 4 + q16 * 4 + 2 * (q & 1));
-  const uint32_t sa_base = s_base + (uint32_t)(wm * 128 * 4);
-  const uint32_t sb_base = s_base + (uint32_t)((BM + wn * 128) * 4);
-  // operands in the order the matrix instructions need them (A's tiles within the first eight, B's one per eight):
-  // b 0, a 0-7, b 1-7
-  auto read = [&](const uint8_t* sl, uint32_t fr, int n, Half& f) MW_INLINE {
-    if (n == 0) f.b[0] = *reinterpret_cast<const uint4*>(sl + b_base + fr);
-    else if (n < 9) f.a[n - 1] = *reinterpret_cast<const uint4*>(sl + a_base + fr + (n - 1) * 2048);
-    else f.b[n - 8] = *reinterpret_cast<const uint4*>(sl + b_base + fr + (n - 8) * 2048);
+  auto a_row = [&](auto tn) MW_INLINE -> int { return decltype(tn)::value == 8 ? (wave >> 1) * 128 : 0; };
+  auto b_row = [&](auto tn) MW_INLINE -> int { return decltype(tn)::value == 8 ? (wave & 1) * 128 : wave * 64; };
+  // operands of TN column tiles in the order the matrix instructions need them (A's tiles within the first eight, B's one
+  // per eight): b 0, a 0-7, b 1-
+  auto read = [&](auto tn, const uint8_t* sl, uint32_t fr, int n, Half& f) MW_INLINE {
+    const uint8_t* a = sl + a_row(tn) * 128 + fr;
+    const uint8_t* b = sl + BM * 128 + b_row(tn) * 128 + fr;
+    if (n == 0) f.b[0] = *reinterpret_cast<const uint4*>(b);
+    else if (n < 9) f.a[n - 1] = *reinterpret_cast<const uint4*>(a + (n - 1) * 2048);
+    else f.b[n - 8] = *reinterpret_cast<const uint4*>(b + (n - 8) * 2048);
   };
-  auto read_scale = [&](const uint8_t* sl, int n, Scales& s) MW_INLINE {
-    if (n & 1) s.a[n >> 1] = *reinterpret_cast<const uint16_t*>(sl + sa_base + (n >> 1) * 64);
-    else s.b[n >> 1] = *reinterpret_cast<const uint16_t*>(sl + sb_base + (n >> 1) * 64);
+  // scale n < TN of B, then of A
+  auto read_scale = [&](auto tn, const uint8_t* sl, int n, Scales& s) MW_INLINE {
+    constexpr int TN = decltype(tn)::value;
+    if (n < TN) s.b[n] = *reinterpret_cast<const uint16_t*>(sl + s_base + (BM + b_row(tn)) * 4 + n * 64);
+    else s.a[n - TN] = *reinterpret_cast<const uint16_t*>(sl + s_base + a_row(tn) * 4 + (n - TN) * 64);
   };
 
   f32x4 acc[8][8];
@@ -274,32 +326,37 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     __builtin_amdgcn_sched_barrier(0);
   };
 
-  int cp_seg = 0;
-  Half f0, f1;    // first and second half
+  int cp = 0;  // unit being computed
+  Half f0, f1;    // first and second half of a step
   Scales sc[2];   // of the steps in the two slots
 
-  auto store = [&]() MW_INLINE {
-    settle();
-    int mt, nt;
-    unsigned long long tag[2] = {~0ull, ~0ull};
-    if constexpr (CONTIG) {
-      tile_mn(__builtin_amdgcn_readfirstlane(pass_tile[cp_seg]), &mt, &nt);
-      tag[0] = pass_mask[cp_seg][2 * wm];
-      tag[1] = pass_mask[cp_seg][2 * wm + 1];
-    } else {
-      tile_mn(cp_seg, &mt, &nt);
-    }
-    const int64_t row0 = (int64_t)mt * BM + wm * 128;
-    const int col0 = nt * BN + wn * 128 + q * 16;
+  // the lane's rows to store (bit i: row 16 i + l % 16 of the wave's) and where; taken while the tile is still at the
+  // issue pointer, before its last steps
+  uint32_t st_rows = 0;
+  int64_t st_row = 0;
+  int st_col = 0;
+  auto place = [&](auto tn) MW_INLINE {
+    const int r0 = a_row(tn) + q16;
+    st_rows = 0;
+    st_row = row0 + r0;
+    st_col = nt * BN + b_row(tn) + q * 16;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 16 * i + q16;
-      bool ok = row0 + r < M;
-      if constexpr (CONTIG) ok = ok && ((tag[i >> 2] >> (r & 63)) & 1ull);
-      uint16_t* dst = p.D + (row0 + r) * (int64_t)N;
+      bool ok = r0 + 16 * i < rows;
+      // contiguous: only the rows tagged with the tile's expert
+      if constexpr (CONTIG) ok = ok && p.index[ok ? st_row + 16 * i : 0] == e;
+      st_rows |= ok ? 1u << i : 0u;
+    }
+  };
+  auto store = [&](auto tn) MW_INLINE {
+    constexpr int TN = decltype(tn)::value;
+    settle();
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int c = col0 + 64 * g;
+    for (int i = 0; i < 8; ++i) {
+      uint16_t* dst = p.D + (st_row + 16 * i) * (int64_t)N;
+#pragma unroll
+      for (int g = 0; g < TN / 4; ++g) {
+        const int c = st_col + 64 * g;
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -308,7 +365,7 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
           w[2 * j + 1] = pack_bf16x2(v[2], v[3]);
           acc[i][4 * g + j] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        if (ok && c < N) {  // N is a multiple of 16
+        if (((st_rows >> i) & 1u) && c < N) {  // N is a multiple of 16
           *reinterpret_cast<uint4*>(dst + c) = uint4{w[0], w[1], w[2], w[3]};
           *reinterpret_cast<uint4*>(dst + c + 8) = uint4{w[4], w[5], w[6], w[7]};
         }
@@ -317,29 +374,59 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     settle();
   };
 
-  // one step in slot st; the loads of step k at the issue pointer follow into it
-  auto step = [&](auto st, int k) MW_INLINE {
+  // one step in slot st over TN column tiles; the loads of step k at the issue pointer follow into it
+  auto step = [&](auto tn, auto st, int k) MW_INLINE {
+    constexpr int TN = decltype(tn)::value;
     constexpr int own = decltype(st)::value;
     constexpr int other = 1 - own;
+    constexpr int NM = 8 * TN;   // matrix instructions of a half step
+    constexpr int NR = 8 + TN;   // operand reads of a half step, and scale reads of a step
     const uint8_t* slo = slot(st);
     const uint8_t* sln = slot(Const<other>{});
-    unrolled<64>([&](auto c) MW_INLINE {
+    unrolled<NM>([&](auto c) MW_INLINE {
       constexpr int n = decltype(c)::value;
       mfma(Const<0>{}, f0, sc[own], n & 7, n >> 3);
-      if constexpr (n < 48 && n % 3 == 0) read(slo, fr1, n / 3, f1);
+      if constexpr (TN == 8 ? n < 48 && n % 3 == 0 : n < 2 * NR && n % 2 == 0) read(tn, slo, fr1, TN == 8 ? n / 3 : n / 2, f1);
       __builtin_amdgcn_sched_barrier(0);
     });
     wait_vmcnt<0>();   // this wave's loads of the next step have landed
     wait_lgkmcnt0();   // and its reads of this one returned
     __builtin_amdgcn_s_barrier();
-    unrolled<64>([&](auto c) MW_INLINE {
+    unrolled<NM>([&](auto c) MW_INLINE {
       constexpr int n = decltype(c)::value;
       mfma(Const<1>{}, f1, sc[own], n & 7, n >> 3);
-      if constexpr (n < 16) read_scale(sln, n, sc[other]);
-      else if constexpr (n < 48 && n % 2 == 0) read(sln, fr0, (n - 16) / 2, f0);
-      if constexpr ((n & 1) && n / 2 < LOADS) issue(st, k, Const<n / 2>{});
+      if constexpr (n < NR) read_scale(tn, sln, n, sc[other]);
+      if constexpr (TN == 8) {
+        if constexpr (n >= 16 && n < 48 && n % 2 == 0) read(tn, sln, fr0, (n - 16) / 2, f0);
+        if constexpr ((n & 1) && n / 2 < LOADS) issue(st, k, Const<n / 2>{});
+      } else {
+        if constexpr (n >= NR && n < 2 * NR) read(tn, sln, fr0, n - NR, f0);
+        if constexpr (n < LOADS) issue(st, k, c);
+      }
       __builtin_amdgcn_sched_barrier(0);
     });
+  };
+  // first operands of a unit whose step 0 is in slot 0
+  auto begin = [&](auto tn) MW_INLINE {
+    constexpr int NR = 8 + decltype(tn)::value;
+    unrolled<NR>([&](auto c) MW_INLINE { read_scale(tn, slot0, decltype(c)::value, sc[0]); });
+    unrolled<NR>([&](auto c) MW_INLINE { read(tn, slot0, fr0, decltype(c)::value, f0); });
+  };
+  auto walk = [&](auto tn, int end) MW_INLINE {
+    for (; cp < end; ++cp) {
+      int k = 2;  // steps issued of the tile at the issue pointer
+      for (int j = 0; j < steps; j += 2) {
+        if (j + 2 == steps) {  // the next loads are the next tile's (after the last tile: its own again, read by none)
+          k = 0;
+          place(tn);
+          if (++is_seg < units) is_setup();
+        }
+        step(tn, Const<0>{}, k);
+        step(tn, Const<1>{}, k + 1);
+        k += 2;
+      }
+      store(tn);
+    }
   };
 
   settle();
@@ -347,20 +434,13 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   unrolled<LOADS>([&](auto c) MW_INLINE { issue(Const<1>{}, 1, c); });
   wait_vmcnt<LOADS>();
   __builtin_amdgcn_s_barrier();
-  unrolled<16>([&](auto c) MW_INLINE { read_scale(slot0, decltype(c)::value, sc[0]); });
-  unrolled<16>([&](auto c) MW_INLINE { read(slot0, fr0, decltype(c)::value, f0); });
-  for (; cp_seg < nseg; ++cp_seg) {
-    int k = 2;  // steps issued of the tile at the issue pointer
-    for (int j = 0; j < steps; j += 2) {
-      if (j + 2 == steps) {  // the next loads are the next tile's (after the last tile: its own again, read by none)
-        k = 0;
-        if (++is_seg < nseg) is_setup();
-      }
-      step(Const<0>{}, k);
-      step(Const<1>{}, k + 1);
-      k += 2;
-    }
-    store();
+  if (own_large > 0) {
+    begin(Const<8>{});
+    walk(Const<8>{}, own_large);
+  }
+  if (own_small > 0) {  // step 0 of the first small tile landed before the last barrier
+    begin(Const<4>{});
+    walk(Const<4>{}, units);
   }
   wait_vmcnt<0>();  // no LDS writes in flight past this point
 #endif

@@ -162,7 +162,7 @@ def test_dense_tile_shapes(monkeypatch, tile, M, N, K):
         a, sa = _operand(rng, (), M, K, exact)
         b, sb = _operand(rng, (), N, K, exact)
         ref, mag = mxfp4.gemm_mxfp4(a, sa, b, sb)
-        for cus in (0, 3):  # 3: a persistent workgroup walks many tiles
+        for cus in (0, 3, 7, 20):  # few: a persistent workgroup walks many tiles, a partial last round is cut or spread
             dg.dg_set_num_cus(cus)
             try:
                 D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
@@ -237,16 +237,48 @@ def test_contiguous(monkeypatch, counts, N, K, tail, exact, tile):
     b, sb = _operand(rng, (G,), N, K, exact)
     sa = sa.copy()
     sa[:, (idx < 0) | (idx >= G)] = -1  # NaN scales on padding rows
-    D = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
-    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*map(_t, (a, sa, b, sb)), D, _t(idx))
-    got = _bits(D)
-    for g in range(G):
-        at = np.nonzero(idx == g)[0]
-        if len(at):
-            ref, mag = mxfp4.gemm_mxfp4(a[at], sa[:, at], b[g], sb[g])
-            _check(got[at], ref, mag, K, exact, (g, counts[g]))
+    A, SA, B, SB, I = map(_t, (a, sa, b, sb, idx))
     pad = (idx < 0) | (idx >= G)
-    assert np.all(got[pad] == oracle.bf16_rne_bits(np.float32(7.0)))
+    want = [mxfp4.gemm_mxfp4(a[idx == g], sa[:, idx == g], b[g], sb[g]) if (idx == g).any() else None for g in range(G)]
+    for cus in (0, 2, 5):
+        dg.dg_set_num_cus(cus)
+        try:
+            D = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+            dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(A, SA, B, SB, D, I)
+        finally:
+            dg.dg_set_num_cus(0)
+        got = _bits(D)
+        for g in range(G):
+            if want[g]:
+                _check(got[idx == g], *want[g], K, exact, (g, counts[g], cus))
+        assert np.all(got[pad] == oracle.bf16_rne_bits(np.float32(7.0)))
+
+
+def test_contiguous_many_experts_and_long_layout(monkeypatch):
+    """64 experts of 0-3 blocks each, rows tagged anywhere in their block; and a layout longer than one launch holds."""
+    rng = np.random.default_rng(64)
+    G, N, K = 64, 256, 256
+    idx = np.full(128 * 2100, -1, np.int32)
+    at = 0
+    for g in rng.permutation(G):
+        for _ in range(rng.integers(0, 4)):
+            rows = rng.choice(128, rng.integers(1, 129), replace=False)
+            idx[128 * at + rows] = g
+            at += int(rng.integers(1, 3))  # blocks without a row in between
+    idx[-128 * 3:] = 5   # past the first 2048 blocks
+    idx[-1] = -1
+    a, sa = _operand(rng, (), len(idx), K, True)
+    b, sb = _operand(rng, (G,), N, K, True)
+    for tile in ("128x256", "256x256"):
+        monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
+        D = torch.full((len(idx), N), 7.0, dtype=torch.bfloat16, device=DEV)
+        dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*map(_t, (a, sa, b, sb)), D, _t(idx))
+        got = _bits(D)
+        for g in range(G):
+            r = idx == g
+            if r.any():
+                _check(got[r], *mxfp4.gemm_mxfp4(a[r], sa[:, r], b[g], sb[g]), K, True, (tile, g))
+        assert np.all(got[idx < 0] == oracle.bf16_rne_bits(np.float32(7.0)))
 
 
 MASKED = [(3, 16, [16, 0, 5], 144, 256), (4, 70, [70, 1, 64, 33], 272, 896), (2, 300, [300, 129], 528, 384), (5, 1, [1, 0, 1, 1, 0], 16, 128),
