@@ -66,8 +66,9 @@ double mx_cost_us(int tile, int64_t tiles, int64_t K, int cus) {
   return (double)ceil_div(tiles, cus) * 1.5 * steps + 10.0;
 }
 
-// Dense: the tile shape of least estimated time; 64 x 64 tiles that leave CUs idle split K, each part at least four
-// steps (64 x 2112 x 7168: 11.2 us whole, 8.5 in four parts, 8.9 in eight; more parts than CUs were slower everywhere).
+// Dense: the tile shape of least estimated time; 64 x 64 tiles that leave CUs idle split K where that is estimated to
+// pay (64 x 2112 x 7168: 11.7 us whole, 8.6 in four parts; 64 x 7168 x 2048: 6.2 whole, 7.4 in two; more parts than CUs
+// were slower everywhere).
 MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) {
   MxPlan pl;
   const int64_t steps = ceil_div(K, 256);
@@ -86,7 +87,15 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   int64_t s = 1;
   if (pl.tile == kMx64x64) {
     const int64_t tiles = (int64_t)pl.m_tiles * pl.n_tiles;
-    s = std::min({cus / std::max<int64_t>(tiles, 1), steps / 4, (int64_t)8});
+    // a step costs 0.27 us, splitting 2 us and 0.3 us a part; at most one workgroup a CU
+    double least = 0.27 * (double)steps;
+    for (int64_t c = 2; c <= 8 && c * tiles <= cus && c <= steps; ++c) {
+      const double t = 0.27 * (double)ceil_div(steps, c) + 2.0 + 0.3 * (double)c;
+      if (t < least) {
+        least = t;
+        s = c;
+      }
+    }
     if (forced_splits > 0) s = std::min<int64_t>(forced_splits, steps);
     if (s < 1 || tiles > kMxMaxCounters) s = 1;
     while (s > 1 && mx_workspace_bytes(pl.tile, pl.m_tiles, pl.n_tiles, (int)s) > ws_bytes) --s;
