@@ -7,17 +7,23 @@
 // and its choices take its rows in (token, choice) order, so the layout is a
 // function of idx alone.
 //
-// A workgroup places 2048 choices.  Up to that many, one launch does
-// everything; beyond, a first launch writes the counts of each block of
-// choices and every workgroup of the second sums the column of counts of each
-// expert before its own block and over all blocks (a thread per expert), so no
-// workgroup waits for another.  Inside a workgroup every wave counts its own
-// run of choices, the waves' counts are summed in order, and a wave ranks 64
-// choices at a time by matching their experts bit by bit.  Rows that hold
-// nothing are known from the counts alone, so their -1 needs no order against
-// the placement; the workgroups share them.  The traffic is a few hundred
-// kilobytes: the time is launch latency and the dependent steps.
-
+// Up to 2048 choices one workgroup and one launch do everything.  Beyond, a
+// first launch writes the counts of each block of choices (1024, or what makes
+// at most 128 blocks) and every workgroup of the second sums the columns of
+// counts before its own block and over all blocks, so no workgroup waits for
+// another.  Inside a workgroup every wave counts its own run of choices, the
+// waves' counts are summed in order, and a wave ranks 64 choices at a time by
+// matching their experts bit by bit.  Rows that hold nothing are known from
+// the counts alone, so their -1 needs no order against the placement; the
+// workgroups share them.
+//
+// The traffic is a megabyte or two: what bounds it is launch latency, the
+// dependent steps, and the scattered 4-byte stores of row_token and m_indices
+// that one CU passes on (one line a cycle); blocks are many for those and few
+// for the columns of counts that every workgroup reads.  Measured: 256 tokens x
+// 8 in one launch 4.8 us; 16384 x 8 of 64 experts 10 us (2.5 the counts);
+// 131072 x 8 of 256 experts 28 us with 128 blocks, 29 with 256, 49 with 512;
+// a million x 8 222 us, 2.1 ms with blocks of 2048.
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
 
@@ -26,41 +32,49 @@ namespace {
 
 constexpr int kLayThreads = 1024;  // also the most experts: a thread per expert
 constexpr int kLayWaves = kLayThreads / 64;
-constexpr int kLayItems = 2048;  // choices per workgroup
-constexpr int kLayBatch = 32;    // counts a thread has in flight
-constexpr int kLayWaveItems = kLayItems / kLayWaves;
+constexpr int kLaySingle = 2;       // 64-choice chunks of a wave where one workgroup places all
+constexpr int kLayMaxBlocks = 128;  // their counts are read by every workgroup
+constexpr int kLayBatch = 8;        // counts a thread has in flight
+constexpr int kLaySlices = 16;      // threads that share an expert's column of counts
 
 __device__ __forceinline__ int local_expert(int v, int first, int G) {
   const int g = v - first;  // v < 0 (no expert) never lands in range: first >= 0
   return v >= 0 && g >= 0 && g < G ? g : -1;
 }
 
+// 64-choice chunks of each wave; one block: kLaySingle
+int chunks_of(int64_t n) {
+  if (n <= (int64_t)kLaySingle * kLayThreads) return kLaySingle;
+  return (int)((n + (int64_t)kLayThreads * kLayMaxBlocks - 1) / ((int64_t)kLayThreads * kLayMaxBlocks));
+}
+int blocks_of(int64_t n) {
+  const int64_t per = (int64_t)chunks_of(n) * kLayThreads;
+  return n > 0 ? (int)((n + per - 1) / per) : 1;
+}
+
 // ws[block][g]: choices of expert g in the block
-__global__ void __launch_bounds__(kLayThreads) layout_count_kernel(LayoutParams p) {
+__global__ void __launch_bounds__(kLayThreads) layout_count_kernel(LayoutParams p, int chunks) {
   __shared__ int hist[kLayThreads];
   hist[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t i0 = (int64_t)blockIdx.x * kLayItems + threadIdx.x;
-  int v[kLayItems / kLayThreads];
-#pragma unroll
-  for (int c = 0; c < kLayItems / kLayThreads; ++c) {
-    const int64_t i = i0 + c * kLayThreads;
-    v[c] = i < p.n ? p.idx[i] : -1;
-  }
-#pragma unroll
-  for (int c = 0; c < kLayItems / kLayThreads; ++c) {
-    const int g = local_expert(v[c], p.first, p.G);
+  const int64_t i0 = (int64_t)blockIdx.x * chunks * kLayThreads + threadIdx.x;
+  for (int c = 0; c < chunks; ++c) {
+    const int64_t i = i0 + (int64_t)c * kLayThreads;
+    const int g = i < p.n ? local_expert(p.idx[i], p.first, p.G) : -1;
     if (g >= 0) atomicAdd(&hist[g], 1);
   }
   __syncthreads();
   if ((int)threadIdx.x < p.G) static_cast<int*>(p.ws)[(int64_t)blockIdx.x * p.G + threadIdx.x] = hist[threadIdx.x];
 }
 
-// workgroups [0, blocks) place their block; all share the rows that hold nothing
-__global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams p, int blocks) {
+// workgroups [0, blocks) place their block; all share the rows that hold
+// nothing.  C: chunks of a wave, held in registers (0: `chunks`, read twice)
+template <int C>
+__global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams p, int blocks, int chunks, int slots) {
   __shared__ int next[kLayWaves][kLayThreads];  // next row (rank when masked) of each expert, per wave
   __shared__ int start_of[kLayThreads + 1];     // first row of each expert's segment (contiguous)
   __shared__ int count_of[kLayThreads];
+  __shared__ int part[2][kLayThreads];          // a slice's sum of a column, before this block and in all
   __shared__ int wsum[kLayWaves];
   const int b = (int)blockIdx.x;
   const int tid = threadIdx.x;
@@ -69,35 +83,61 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
   const int G = p.G;
   const bool placing = b < blocks;
   const bool single = blocks == 1;
+  const int nc = C ? C : chunks;
   if (tid < G) {
 #pragma unroll
     for (int w = 0; w < kLayWaves; ++w) next[w][tid] = 0;
   }
-  __syncthreads();
-  // counts of the wave's own choices (one block: every workgroup counts it, for the totals)
-  const int64_t w0 = (single ? 0 : (int64_t)b * kLayItems) + (int64_t)wave * kLayWaveItems;
-  int e[kLayWaveItems / 64];
-#pragma unroll
-  for (int c = 0; c < kLayWaveItems / 64; ++c) {
+  // the wave's own choices (one block: every workgroup counts it, for the totals)
+  const int64_t w0 = (int64_t)(single ? 0 : b) * nc * kLayThreads + (int64_t)wave * nc * 64;
+  const auto choice = [&](int c) {
     const int64_t i = w0 + 64 * c + lane;
-    e[c] = (placing || single) && i < p.n ? local_expert(p.idx[i], p.first, G) : -1;
-  }
+    return (placing || single) && i < p.n ? local_expert(p.idx[i], p.first, G) : -1;
+  };
+  int e[C ? C : 1];
+  if constexpr (C > 0) {
 #pragma unroll
-  for (int c = 0; c < kLayWaveItems / 64; ++c)
-    if (e[c] >= 0) atomicAdd(&next[wave][e[c]], 1);
-  // choices of expert tid before this block, and in all
+    for (int c = 0; c < C; ++c) e[c] = choice(c);
+  }
+  // choices of each expert before this block, and in all: `slots` (a power of
+  // two) experts side by side, each column cut into slices of blocks
+  if (!single) {
+    const int g = tid & (slots - 1);
+    const int slice = tid / slots;
+    const int slices = kLayThreads / slots < kLaySlices ? kLayThreads / slots : kLaySlices;
+    int before = 0, total = 0;
+    if (g < G && slice < slices) {
+      const int* col = static_cast<const int*>(p.ws) + g;
+      for (int c0 = slice; c0 < blocks; c0 += kLayBatch * slices) {
+        int v[kLayBatch];
+#pragma unroll
+        for (int c = 0; c < kLayBatch; ++c) v[c] = c0 + c * slices < blocks ? col[(int64_t)(c0 + c * slices) * G] : 0;
+#pragma unroll
+        for (int c = 0; c < kLayBatch; ++c) {
+          before += c0 + c * slices < b ? v[c] : 0;
+          total += v[c];
+        }
+      }
+    }
+    part[0][tid] = before;
+    part[1][tid] = total;
+  }
+  __syncthreads();
+  if constexpr (C > 0) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (e[c] >= 0) atomicAdd(&next[wave][e[c]], 1);
+  } else {
+    for (int c = 0; c < nc; ++c) {
+      const int g = choice(c);
+      if (g >= 0) atomicAdd(&next[wave][g], 1);
+    }
+  }
   int before = 0, total = 0;
   if (!single && tid < G) {
-    const int* col = static_cast<const int*>(p.ws) + tid;
-    for (int c0 = 0; c0 < blocks; c0 += kLayBatch) {
-      int v[kLayBatch];
-#pragma unroll
-      for (int c = 0; c < kLayBatch; ++c) v[c] = c0 + c < blocks ? col[(int64_t)(c0 + c) * G] : 0;
-#pragma unroll
-      for (int c = 0; c < kLayBatch; ++c) {
-        before += c0 + c < b ? v[c] : 0;
-        total += v[c];
-      }
+    for (int i = tid; i < kLayThreads && i < slots * kLaySlices; i += slots) {
+      before += part[0][i];
+      total += part[1][i];
     }
   }
   __syncthreads();
@@ -139,11 +179,8 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
   if (placing) {
     int bits = 1;
     while ((1 << bits) <= G) ++bits;  // codes 0 .. G (G: none)
-#pragma unroll
-    for (int c = 0; c < kLayWaveItems / 64; ++c) {  // the wave's choices in order
+    const auto place = [&](int c, int g) __attribute__((always_inline)) {
       const int64_t i = w0 + 64 * c + lane;
-      if (w0 + 64 * c >= p.n) break;  // uniform
-      const int g = e[c];
       const int code = g < 0 ? G : g;
       unsigned long long same = ~0ull;  // lanes with this lane's expert
       for (int k = 0; k < bits; ++k) {
@@ -167,6 +204,14 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
           if (p.m_indices) p.m_indices[row] = g;
         }
       }
+    };
+    // the wave's choices in order
+    if constexpr (C > 0) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (w0 + 64 * c < p.n) place(c, e[c]);  // uniform
+    } else {
+      for (int c = 0; c < nc && w0 + 64 * c < p.n; ++c) place(c, choice(c));
     }
   }
   // rows that hold nothing, shared by all workgroups
@@ -195,18 +240,19 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
 
 }  // namespace
 
-size_t layout_workspace_bytes(int64_t n, int64_t G) {
-  const int64_t blocks = n > 0 ? (n + kLayItems - 1) / kLayItems : 1;
-  return (size_t)(blocks * G * 4);
-}
+size_t layout_workspace_bytes(int64_t n, int64_t G) { return (size_t)blocks_of(n) * (size_t)G * 4; }
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
-  const int blocks = (int)(p.n > 0 ? (p.n + kLayItems - 1) / kLayItems : 1);
-  if (blocks > 1) hipLaunchKernelGGL(layout_count_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p);
+  const int blocks = blocks_of(p.n);
+  const int chunks = chunks_of(p.n);
+  int slots = 1;
+  while (slots < p.G) slots *= 2;
+  if (blocks > 1) hipLaunchKernelGGL(layout_count_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p, chunks);
   // further workgroups where the rows outnumber the choices
   const int64_t f = (p.rows + 4 * kLayThreads - 1) / (4 * kLayThreads);
   const int fill = (int)(f < 256 ? f : 256);
-  hipLaunchKernelGGL(layout_place_kernel, dim3(blocks > fill ? blocks : fill), dim3(kLayThreads), 0, stream, p, blocks);
+  auto kernel = chunks == kLaySingle ? layout_place_kernel<kLaySingle> : chunks == 1 ? layout_place_kernel<1> : layout_place_kernel<0>;
+  hipLaunchKernelGGL(kernel, dim3(blocks > fill ? blocks : fill), dim3(kLayThreads), 0, stream, p, blocks, chunks, slots);
   return hipGetLastError();
 }
 

@@ -150,6 +150,6 @@ def test_workspaces_and_plans(lib):
         assert plan(op, 64, 2110, 7168) == "" and plan(op, 64, 2112, 100) == "" and size(op, 0, 16, 128) == 0
         assert size(dg.DG_OP_MOE_GATE, 1, 8, 2) > 0 and size(dg.DG_OP_MOE_GATE, 1, 2000, 2) == 0
         assert size(dg.DG_OP_MOE_GATE, 1 << 20, 256, 8) == size(dg.DG_OP_MOE_GATE, 1 << 21, 256, 8)
-        assert size(dg.DG_OP_MOE_LAYOUT, 16384, 0, 8, 64) == 64 * 64 * 4 and size(dg.DG_OP_MOE_LAYOUT, 4, 0, 17, 64) == 0
+        assert size(dg.DG_OP_MOE_LAYOUT, 16384, 0, 8, 64) == 128 * 64 * 4 and size(dg.DG_OP_MOE_LAYOUT, 4, 0, 17, 64) == 0
     finally:
         dg.dg_set_num_cus(0)

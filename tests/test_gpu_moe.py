@@ -194,6 +194,27 @@ def test_layout(T, k, E, first, G):
             assert np.array_equal(o[n].cpu().numpy().ravel(), want[n].ravel()), (n, max_m)
 
 
+@pytest.mark.parametrize("T,k,E,first,G", [(40000, 4, 96, 0, 96), (70001, 4, 48, 8, 32)])
+def test_layout_of_many_choices(T, k, E, first, G):
+    """Blocks of several runs of choices each: two of them, and more than are kept in registers."""
+    idx = np.argsort(np.random.default_rng(T).random((T, E)), 1)[:, :k].astype(np.int32)
+    ws = _ws(dg.DG_OP_MOE_LAYOUT, T, 0, k, G)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    M = (T * k + 127 * G + 127) // 128 * 128
+    for _ in range(2):
+        o = dict(counts=torch.full((G,), 77, **i32), m_indices=torch.full((M,), 77, **i32), row_token=torch.full((M,), 77, **i32), row_of=torch.full((T, k), 77, **i32))
+        dg.dg_moe_layout_contiguous(_t(idx), *o.values(), first_expert=first, workspace=ws)
+        want = moe.layout(idx, first, G, rows=M)
+        for n in o:
+            assert np.array_equal(o[n].cpu().numpy(), want[n]), n
+    max_m = T * k // E
+    m, rt, ro = torch.full((G,), 77, **i32), torch.full((G, max_m), 77, **i32), torch.full((T, k), 77, **i32)
+    dg.dg_moe_layout_masked(_t(idx), m, rt, ro, first_expert=first, workspace=ws)
+    want = moe.layout(idx, first, G, max_m=max_m)
+    for got, n in ((m, "counts"), (rt, "row_token"), (ro, "row_of")):
+        assert np.array_equal(got.cpu().numpy().ravel(), want[n].ravel()), n
+
+
 def test_layout_no_tokens_and_one_expert_takes_all():
     i32 = dict(dtype=torch.int32, device=DEV)
     ws = _ws(dg.DG_OP_MOE_LAYOUT, 5000, 0, 2, 3)
