@@ -143,7 +143,7 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   if (ws && (!aligned(ws, 16) || ws_bytes % 4))
     return fail(DG_ERR_WORKSPACE, "workspace must be 16-byte aligned with a size that is a multiple of 4");
   // scale words of an operand (masked: of one expert) are addressed with 32-bit offsets, up to three rows of them past K
-  if (rows * (K / 128 + 4) * 4 >= kOffLim || N * (K / 128 + 4) * 4 >= kOffLim) return fail(DG_ERR_SHAPE, "scale arrays exceed 4 GiB");
+  if (rows * (K / 128 + 8) * 4 >= kOffLim || N * (K / 128 + 8) * 4 >= kOffLim) return fail(DG_ERR_SHAPE, "scale arrays exceed 4 GiB");
   int cus = 0;
   if ((rc = check_device(&cus))) return rc;
   cus = effective_cus(cus);
@@ -197,8 +197,8 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     p.sfa = sfa + r0;
     p.D = D + r0 * N;
     p.index = index ? index + r0 : nullptr;
-    const int64_t tiles = ceil_div(p.rows, 128) * pl.n_tiles;
-    const hipError_t e = launch_mxfp4_wide(form, (int)std::min<int64_t>(tiles, cus), p, hs(stream));
+    const int64_t quarters = ceil_div(p.rows, 128) * 2 * pl.n_tiles;  // the smallest pieces a tile is cut into
+    const hipError_t e = launch_mxfp4_wide(form, (int)std::min<int64_t>(quarters, cus), p, hs(stream));
     if (e != hipSuccess) return launched(e);
   }
   return ok();

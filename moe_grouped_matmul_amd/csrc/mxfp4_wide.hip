@@ -29,8 +29,13 @@
 // rows.  Dense: a last tile of up to 128 rows.  The large tiles are walked in
 // rounds of one per workgroup; the tiles of a last, partial round and the small
 // ones go to the workgroups with the least work, the former cut in two where
-// everything left then fits one round of small tiles.
-
+// everything left then fits one round of small tiles, and small ones that fill
+// half a round or less are cut once more, into 128 x 128 quarters.  A quarter's
+// step is short against the latency of its loads, so its slots hold two steps
+// (rows 128 on are the same rows further along K) and it meets a barrier every
+// other one.  Measured, 8 experts x 16384 rows, 4096 x 7168: 276 us without
+// quarters, 270 with quarters of one step a slot, 267 us (3.6 PFLOP/s); 8192
+// rows 163, 156, 148; one expert of 4352 rows 78, 74.5, 67.
 #include <utility>
 
 #include "dg_internal.hpp"
@@ -192,19 +197,26 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     if (bid < rest) return 2 * (G - rest) + bid + i * G;
     return i < 2 ? bid - rest + i * (G - rest) : 2 * (G - rest) + bid + (i - 2) * G;
   };
+  // of the small tiles that do not fill a round, 128 x 128 quarters where those fit one
+  const int free = spread ? 2 * (G - rest) : 0;
+  const int last = S > free ? (S - free) % G : 0;
+  const int whole_small = 2 * last <= G ? S - last : S;
   int own_small = 0;
-  while (small_id(own_small) < S) ++own_small;
-  const int units = own_large + own_small;
+  while (small_id(own_small) < whole_small) ++own_small;
+  const int pieces = own_large + own_small;
+  const int units = pieces + (bid < 2 * (S - whole_small) ? 1 : 0);
   if (units == 0) return;
-  // unit u: first row, rows, column tile, expert
-  auto unit = [&](int u, int64_t* row0, int* rows, int* nt, int* e) MW_INLINE {
-    int b, blocks = 2;
+  // unit u: first row, rows, first column, columns, expert
+  auto unit = [&](int u, int64_t* row0, int* rows, int* n0, int* cols, int* e) MW_INLINE {
+    const bool quarter = u >= pieces;
+    int b, blocks = 2, tile;
+    int* nt = &tile;
     if (u < own_large) {
       int mt;
       grouped_mn(round_tile(bid, u, G, T), n_large, n_tiles, 4, &mt, nt);
       b = CONTIG ? (int)large_at[CONTIG ? mt : 0] : 2 * mt;
     } else {
-      const int i = small_id(u - own_large);
+      const int i = quarter ? whole_small + (bid >> 1) : small_id(u - own_large);
       blocks = 1;
       if (i < n_small * n_tiles) {
         const int st = i / n_tiles;
@@ -221,6 +233,9 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     *row0 = (int64_t)b * 128;
     const int64_t left = M - *row0;
     *rows = left < blocks * 128 ? (left < 0 ? 0 : (int)left) : blocks * 128;
+    *n0 = tile * BN + (quarter ? 128 * (bid & 1) : 0);
+    const int width = quarter ? 128 : BN;
+    *cols = N - *n0 < width ? N - *n0 : width;
     *e = CONTIG ? __builtin_amdgcn_readfirstlane((int)expert_of[CONTIG ? b : 0]) : 0;
   };
 
@@ -232,23 +247,33 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   // no product is left in fp32, so neither a half step nor a whole one past K adds anything.
   const int l8 = lane >> 3;
   const int chunk = (lane & 7) ^ l8;
-  const uint32_t a_off = (uint32_t)(64 * wave + l8) * (uint32_t)kbytes + 16u * chunk;
-  const uint32_t b_off = (uint32_t)(64 * wave + 16 * (l8 >> 2) + (l8 & 3)) * (uint32_t)kbytes + 16u * chunk;
-  // scale words of rows 64 w + lane, B's in LDS row order
-  const uint32_t sa_off = 4u * (uint32_t)tid;
-  const uint32_t sb_off = 4u * (uint32_t)(64 * wave + 16 * (q16 >> 2) + 4 * q + (q16 & 3));
+  // Of a quarter the waves 2 and 3 fill rows 128 on with the same rows' next step: two steps to a slot.
+  uint32_t a_off, b_off, sa_off, sb_off;
+  int stride = 1;  // steps in a slot, of the unit at the issue pointer
+  auto lane_offsets = [&](int w, int ahead) MW_INLINE {
+    a_off = (uint32_t)(64 * w + l8) * (uint32_t)kbytes + 16u * chunk + 128u * ahead;
+    b_off = (uint32_t)(64 * w + 16 * (l8 >> 2) + (l8 & 3)) * (uint32_t)kbytes + 16u * chunk + 128u * ahead;
+    // scale words of rows 64 w + lane, B's in LDS row order
+    sa_off = 4u * (uint32_t)(64 * w + lane) + 8u * ahead * ld;
+    sb_off = 4u * (uint32_t)(64 * w + 16 * (q16 >> 2) + 4 * q + (q16 & 3)) + 8u * ahead * (uint32_t)N;
+  };
+  lane_offsets(wave, 0);
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
   int is_seg = 0;
   int64_t row0 = 0;  // of the unit at the issue pointer
-  int rows = 0, nt = 0, e = 0;
+  int rows = 0, n0 = 0, e = 0;
   auto is_setup = [&]() MW_INLINE {
-    unit(is_seg, &row0, &rows, &nt, &e);
-    const int n0 = nt * BN;
-    const int cols = N - n0 < BN ? N - n0 : BN;
+    int cols;
+    unit(is_seg, &row0, &rows, &n0, &cols, &e);
+    if (is_seg >= pieces) {
+      stride = 2;
+      lane_offsets(wave & 1, wave >> 1);
+    }
     ra = mw_rsrc(p.A + row0 * kbytes, (uint32_t)rows * (uint32_t)kbytes);
+    if (cols < 0) cols = 0;  // the second quarter of a narrow last tile
     rb = mw_rsrc(p.B + ((int64_t)e * N + n0) * kbytes, (uint32_t)cols * (uint32_t)kbytes);
     rsa = mw_rsrc(p.sfa + row0, ((uint32_t)(KB - 1) * ld + (uint32_t)rows) * 4u);
-    rsb = mw_rsrc(p.sfb + (int64_t)e * N * KB + n0, ((uint32_t)(KB - 1) * (uint32_t)N + (uint32_t)cols) * 4u);
+    rsb = mw_rsrc(p.sfb + (int64_t)e * N * KB + n0, cols ? ((uint32_t)(KB - 1) * (uint32_t)N + (uint32_t)cols) * 4u : 0u);
   };
   is_setup();
 
@@ -280,24 +305,25 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   // their scale bytes are neighbours and one 2-byte read serves both halves.
   const uint32_t fr0 = (uint32_t)(q16 * 128 + (((2 * q) ^ (lane & 7)) << 4));
   const uint32_t fr1 = (uint32_t)(q16 * 128 + (((2 * q + 1) ^ (lane & 7)) << 4));
-  // the wave's first LDS row of A and of B: (128 rows, 128 columns) of a large tile, (all 128 rows, 64 columns) of a small one
+  // the wave's first LDS row of A and of B: (128 rows, 128 columns) of a large tile, (all 128 rows, 64
+  // columns) of a small one, (all 128 rows, 32 columns) of a quarter
   const uint32_t s_base = (uint32_t)(SLOT_S + (q >> 1) * (BM + BN) * 4 + q16 * 4 + 2 * (q & 1));
   auto a_row = [&](auto tn) MW_INLINE -> int { return decltype(tn)::value == 8 ? (wave >> 1) * 128 : 0; };
-  auto b_row = [&](auto tn) MW_INLINE -> int { return decltype(tn)::value == 8 ? (wave & 1) * 128 : wave * 64; };
+  auto b_row = [&](auto tn) MW_INLINE -> int { return decltype(tn)::value == 8 ? (wave & 1) * 128 : wave * 8 * decltype(tn)::value * 2; };
   // operands of TN column tiles in the order the matrix instructions need them (A's tiles within the first eight, B's one
   // per eight): b 0, a 0-7, b 1-
-  auto read = [&](auto tn, const uint8_t* sl, uint32_t fr, int n, Half& f) MW_INLINE {
-    const uint8_t* a = sl + a_row(tn) * 128 + fr;
-    const uint8_t* b = sl + BM * 128 + b_row(tn) * 128 + fr;
+  auto read = [&](auto tn, const uint8_t* sl, uint32_t fr, int n, Half& f, int row = 0) MW_INLINE {
+    const uint8_t* a = sl + (row + a_row(tn)) * 128 + fr;
+    const uint8_t* b = sl + (row + BM + b_row(tn)) * 128 + fr;
     if (n == 0) f.b[0] = *reinterpret_cast<const uint4*>(b);
     else if (n < 9) f.a[n - 1] = *reinterpret_cast<const uint4*>(a + (n - 1) * 2048);
     else f.b[n - 8] = *reinterpret_cast<const uint4*>(b + (n - 8) * 2048);
   };
   // scale n < TN of B, then of A
-  auto read_scale = [&](auto tn, const uint8_t* sl, int n, Scales& s) MW_INLINE {
+  auto read_scale = [&](auto tn, const uint8_t* sl, int n, Scales& s, int row = 0) MW_INLINE {
     constexpr int TN = decltype(tn)::value;
-    if (n < TN) s.b[n] = *reinterpret_cast<const uint16_t*>(sl + s_base + (BM + b_row(tn)) * 4 + n * 64);
-    else s.a[n - TN] = *reinterpret_cast<const uint16_t*>(sl + s_base + a_row(tn) * 4 + (n - TN) * 64);
+    if (n < TN) s.b[n] = *reinterpret_cast<const uint16_t*>(sl + s_base + (row + BM + b_row(tn)) * 4 + n * 64);
+    else s.a[n - TN] = *reinterpret_cast<const uint16_t*>(sl + s_base + (row + a_row(tn)) * 4 + (n - TN) * 64);
   };
 
   f32x4 acc[8][8];
@@ -339,7 +365,8 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     const int r0 = a_row(tn) + q16;
     st_rows = 0;
     st_row = row0 + r0;
-    st_col = nt * BN + b_row(tn) + q * 16;
+    // a quarter's wave has two of the four column tiles whose outputs are consecutive
+    st_col = n0 + q * 16 + (decltype(tn)::value == 2 ? (wave >> 1) * 64 + (wave & 1) * 8 : b_row(tn));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       bool ok = r0 + 16 * i < rows;
@@ -370,6 +397,11 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
           *reinterpret_cast<uint4*>(dst + c + 8) = uint4{w[4], w[5], w[6], w[7]};
         }
       }
+      if constexpr (TN == 2) {
+        const f32x4 u = acc[i][0], v = acc[i][1];
+        if (((st_rows >> i) & 1u) && st_col < N)
+          *reinterpret_cast<uint4*>(dst + st_col) = uint4{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+      }
     }
     settle();
   };
@@ -386,7 +418,8 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     unrolled<NM>([&](auto c) MW_INLINE {
       constexpr int n = decltype(c)::value;
       mfma(Const<0>{}, f0, sc[own], n & 7, n >> 3);
-      if constexpr (TN == 8 ? n < 48 && n % 3 == 0 : n < 2 * NR && n % 2 == 0) read(tn, slo, fr1, TN == 8 ? n / 3 : n / 2, f1);
+      constexpr int every = TN == 8 ? 3 : 2;
+      if constexpr (n < every * NR && n % every == 0) read(tn, slo, fr1, n / every, f1);
       __builtin_amdgcn_sched_barrier(0);
     });
     wait_vmcnt<0>();   // this wave's loads of the next step have landed
@@ -406,6 +439,51 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
       __builtin_amdgcn_sched_barrier(0);
     });
   };
+  // the two steps in slot st of a quarter
+  auto quarter_step = [&](auto st, int k) MW_INLINE {
+    constexpr Const<2> tn;
+    constexpr int own = decltype(st)::value;
+    constexpr int other = 1 - own;
+    constexpr int NM = 16, NR = 10;
+    const uint8_t* slo = slot(st);
+    const uint8_t* sln = slot(Const<other>{});
+    Scales s2;
+    unrolled<NM>([&](auto c) MW_INLINE {
+      constexpr int n = decltype(c)::value;
+      mfma(Const<0>{}, f0, sc[own], n & 7, n >> 3);
+      if constexpr (n < NR) {
+        read(tn, slo, fr1, n, f1);
+        read_scale(tn, slo, n, s2, 128);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    unrolled<NM>([&](auto c) MW_INLINE {
+      constexpr int n = decltype(c)::value;
+      mfma(Const<1>{}, f1, sc[own], n & 7, n >> 3);
+      if constexpr (n < NR) read(tn, slo, fr0, n, f0, 128);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    unrolled<NM>([&](auto c) MW_INLINE {
+      constexpr int n = decltype(c)::value;
+      mfma(Const<0>{}, f0, s2, n & 7, n >> 3);
+      if constexpr (n < NR) read(tn, slo, fr1, n, f1, 128);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    unrolled<NM>([&](auto c) MW_INLINE {
+      constexpr int n = decltype(c)::value;
+      mfma(Const<1>{}, f1, s2, n & 7, n >> 3);
+      issue(st, k, c);
+      if constexpr (n + NM < LOADS) issue(st, k, Const<n + NM>{});
+      if constexpr (n < NR) {
+        read_scale(tn, sln, n, sc[other]);
+        read(tn, sln, fr0, n, f0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
   // first operands of a unit whose step 0 is in slot 0
   auto begin = [&](auto tn) MW_INLINE {
     constexpr int NR = 8 + decltype(tn)::value;
@@ -414,16 +492,22 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   };
   auto walk = [&](auto tn, int end) MW_INLINE {
     for (; cp < end; ++cp) {
-      int k = 2;  // steps issued of the tile at the issue pointer
-      for (int j = 0; j < steps; j += 2) {
-        if (j + 2 == steps) {  // the next loads are the next tile's (after the last tile: its own again, read by none)
+      constexpr int per = decltype(tn)::value == 2 ? 4 : 2;  // steps in the two slots
+      int k = per;  // steps issued of the tile at the issue pointer
+      for (int j = 0; j < steps; j += per) {
+        if (j + per >= steps) {  // the next loads are the next tile's (after the last tile: its own again, read by none)
           k = 0;
           place(tn);
           if (++is_seg < units) is_setup();
         }
-        step(tn, Const<0>{}, k);
-        step(tn, Const<1>{}, k + 1);
-        k += 2;
+        if constexpr (per == 4) {
+          quarter_step(Const<0>{}, k);
+          quarter_step(Const<1>{}, k + stride);
+        } else {
+          step(tn, Const<0>{}, k);
+          step(tn, Const<1>{}, k + stride);
+        }
+        k += 2 * stride;
       }
       store(tn);
     }
@@ -431,7 +515,7 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
 
   settle();
   unrolled<LOADS>([&](auto c) MW_INLINE { issue(Const<0>{}, 0, c); });
-  unrolled<LOADS>([&](auto c) MW_INLINE { issue(Const<1>{}, 1, c); });
+  unrolled<LOADS>([&](auto c) MW_INLINE { issue(Const<1>{}, stride, c); });
   wait_vmcnt<LOADS>();
   __builtin_amdgcn_s_barrier();
   if (own_large > 0) {
@@ -440,7 +524,11 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   }
   if (own_small > 0) {  // step 0 of the first small tile landed before the last barrier
     begin(Const<4>{});
-    walk(Const<4>{}, units);
+    walk(Const<4>{}, pieces);
+  }
+  if (units > pieces) {
+    begin(Const<2>{});
+    walk(Const<2>{}, units);
   }
   wait_vmcnt<0>();  // no LDS writes in flight past this point
 #endif

@@ -162,7 +162,7 @@ def test_dense_tile_shapes(monkeypatch, tile, M, N, K):
         a, sa = _operand(rng, (), M, K, exact)
         b, sb = _operand(rng, (), N, K, exact)
         ref, mag = mxfp4.gemm_mxfp4(a, sa, b, sb)
-        for cus in (0, 3, 7, 20):  # few: a persistent workgroup walks many tiles, a partial last round is cut or spread
+        for cus in (0, 3, 7, 20, 45):  # few: a persistent workgroup walks many tiles, a partial last round is cut or spread
             dg.dg_set_num_cus(cus)
             try:
                 D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device=DEV)
@@ -240,7 +240,7 @@ def test_contiguous(monkeypatch, counts, N, K, tail, exact, tile):
     A, SA, B, SB, I = map(_t, (a, sa, b, sb, idx))
     pad = (idx < 0) | (idx >= G)
     want = [mxfp4.gemm_mxfp4(a[idx == g], sa[:, idx == g], b[g], sb[g]) if (idx == g).any() else None for g in range(G)]
-    for cus in (0, 2, 5):
+    for cus in (0, 2, 5, 9, 23, 60):
         dg.dg_set_num_cus(cus)
         try:
             D = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
