@@ -54,16 +54,30 @@ struct MxPlan {
   int steps_per_split = 0;
 };
 
-// Estimated time (us) of a call over tiles of one shape: rounds of tiles over the CUs (two 64 x 64 workgroups to a CU),
-// a step of 256 K elements costing 0.45, 1.05 and 1.5 us a round, and the start, epilogue and last write-back. Fitted to
-// 12 shapes of 200-4096 rows with every tile shape forced; the tile of least estimate was the fastest one timed, or
-// within 5% of it, on each (4096 x 2112 x 7168: 60, 64 and 44 us; 1024 x 4096 x 7168: 29, 34 and 43; 2048 x 4096 x
-// 7168: 54, 36 and 45).
+// Estimated times (us) of a call. 64 x 64 and 128 x 256 tiles: rounds of tiles over the CUs (two 64 x 64 workgroups to a
+// CU), a step of 256 K elements costing 0.45 and 1.05 us a round, and the start, epilogue and last write-back.
 double mx_cost_us(int tile, int64_t tiles, int64_t K, int cus) {
   const double steps = (double)ceil_div(K, 256);
   if (tile == kMx64x64) return (double)ceil_div(tiles, 2 * cus) * (0.45 * steps + 1.5) + 3.0;
-  if (tile == kMx128x256) return (double)ceil_div(tiles, cus) * 1.05 * steps + 8.0;
-  return (double)ceil_div(tiles, cus) * 1.5 * steps + 10.0;
+  return (double)ceil_div(tiles, cus) * 1.05 * steps + 8.0;
+}
+// The persistent kernel's: whole rounds of 256 x 256 tiles, then as it distributes the rest (the same rules). A step of
+// a large tile costs 1.1 us and 0.62 more as all CUs run one (the clock), of a 128 x 256 tile 1.25, of a 128 x 128
+// quarter 0.45. Fitted, with the above, to 19 dense shapes of 200-4096 rows with every tile shape forced: the tile of
+// least estimate was the fastest on each (1024 x 4096 x 4096: 20, 22 and 16 us; 1024 x 2048 x 7168: 16, 31 and 20;
+// 2048 x 4096 x 2048: 24, 16 and 17; 2500 x 4096 x 7168: 66, 66 and 45).
+double mx_wide_us(int64_t large, int64_t small, int64_t K, int cus) {
+  const double steps = (double)ceil_div(K, 256);
+  const int64_t rounds = large / cus;
+  const int64_t rest = large % cus;
+  const bool cut = rest > 0 && 2 * rest + small <= cus;
+  const bool spread = rest > 0 && !cut;
+  const int64_t halves = std::max<int64_t>(0, small + (cut ? 2 * rest : 0) - (spread ? 2 * (cus - rest) : 0));
+  const int64_t last = halves % cus;
+  double t = 1.72 * (double)rounds + 1.25 * (double)(halves / cus);
+  if (spread) t += 1.1 + 0.62 * (rounds ? 1.0 : (double)rest / (double)cus);
+  if (last) t += 2 * last <= cus ? 0.45 : 1.25;
+  return t * steps + 6.5;
 }
 
 // Dense: the tile shape of least estimated time; 64 x 64 tiles that leave CUs idle split K where that is estimated to
@@ -74,7 +88,10 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   const int64_t steps = ceil_div(K, 256);
   double best = -1.0;
   for (int t : {kMx64x64, kMx128x256, kMx256x256}) {
-    const double c = mx_cost_us(t, ceil_div(M, mx_bm(t)) * ceil_div(N, mx_bn(t)), K, cus);
+    const int64_t n_tiles = ceil_div(N, mx_bn(t));
+    const bool odd = M % 256 >= 1 && M % 256 <= 128;  // the last row tile has up to 128 rows
+    const double c = t == kMx256x256 ? mx_wide_us((M + 127) / 256 * n_tiles, odd ? n_tiles : 0, K, cus)
+                                     : mx_cost_us(t, ceil_div(M, mx_bm(t)) * n_tiles, K, cus);
     if (best < 0 || c < best) {
       best = c;
       pl.tile = t;
@@ -105,12 +122,13 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   return pl;
 }
 
-// Contiguous: 256 x 256 tiles where they are estimated faster than 128 x 256 ones; an expert with an odd number of
-// 128-row blocks, every other one, costs half a tile more.
+// Contiguous: the persistent kernel where it is estimated faster than 128 x 256 tiles; every other expert's number of
+// 128-row blocks is odd, and reading m_indices takes a few microseconds.
 bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
   const int64_t n_tiles = ceil_div(N, 256);
-  return mx_cost_us(kMx256x256, (ceil_div(rows, 256) + G / 4) * n_tiles, K, cus) <
-         mx_cost_us(kMx128x256, ceil_div(rows, 128) * n_tiles, K, cus);
+  const int64_t blocks = ceil_div(rows, 128);
+  const int64_t odd = std::min(blocks, (G + 1) / 2);
+  return mx_wide_us((blocks - odd + 1) / 2 * n_tiles, odd * n_tiles, K, cus) + 4.0 < mx_cost_us(kMx128x256, blocks * n_tiles, K, cus);
 }
 
 int check_mx_shape(int64_t N, int64_t K) {
