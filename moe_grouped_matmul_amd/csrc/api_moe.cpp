@@ -122,13 +122,29 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
   return pl;
 }
 
-// Contiguous: the persistent kernel where it is estimated faster than 128 x 256 tiles; every other expert's number of
-// 128-row blocks is odd, and reading m_indices takes a few microseconds.
-bool mx_contiguous_wide(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
-  const int64_t n_tiles = ceil_div(N, 256);
+// Contiguous: the tile shape of least estimated time. Every other expert's number of 128-row blocks is taken to be odd,
+// the persistent kernel reads m_indices first (4 us), and the weights of all experts and the output pass at 2.8, 3.5 or
+// 4.3 TB/s at most (experts of few rows, whose weights no other row tile repeats: 64 experts, 256 rows, 4096 x 7168 in
+// 313, 217 and 214 us). Over 18 layouts of 8-8192 rows and 2-64 experts the choice was the fastest of the three or
+// within 10% of it: 2000 rows of 16 experts, 512 x 7168, 16, 31 and 25 us; 1000 of 4, 4096 x 2048, 20, 15 and 20; 8192
+// of 16, 4096 x 1024, 96, 59 and 50.
+int mx_contiguous_tile(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
   const int64_t blocks = ceil_div(rows, 128);
   const int64_t odd = std::min(blocks, (G + 1) / 2);
-  return mx_wide_us((blocks - odd + 1) / 2 * n_tiles, odd * n_tiles, K, cus) + 4.0 < mx_cost_us(kMx128x256, blocks * n_tiles, K, cus);
+  const double mb = 1e-6 * ((double)G * (double)N * (double)K / 2 + 2.0 * (double)rows * (double)N);
+  int tile = kMx64x64;
+  double best = -1.0;
+  for (int t : {kMx64x64, kMx128x256, kMx256x256}) {
+    const int64_t n_tiles = ceil_div(N, mx_bn(t));
+    const double c = t == kMx256x256   ? std::max(mx_wide_us((blocks - odd + 1) / 2 * n_tiles, odd * n_tiles, K, cus) + 4.0, mb / 4.3 + 10.5)
+                     : t == kMx128x256 ? std::max(mx_cost_us(t, blocks * n_tiles, K, cus), mb / 3.5 + 8.0)
+                                       : std::max(mx_cost_us(t, 2 * blocks * n_tiles, K, cus), mb / 2.8 + 3.0);
+    if (best < 0 || c < best) {
+      best = c;
+      tile = t;
+    }
+  }
+  return tile;
 }
 
 int check_mx_shape(int64_t N, int64_t K) {
@@ -169,13 +185,12 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   if (form == kMxDense) {
     pl = plan_mx_dense(rows, N, K, cus, ws ? ws_bytes : 0);
   } else {
-    // 128 x 256 tiles read each weight once and each row from few workgroups; 64 x 64 ones where those are too few
-    // to occupy the CUs (32 experts x 128 rows, 4096 x 7168: 94 against 144 us)
-    const int64_t t128 = G * ceil_div(rows, 128) * ceil_div(N, 256);
-    pl.tile = form == kMxMasked && t128 < cus ? kMx64x64 : kMx128x256;
-    if (form == kMxContiguous && mx_contiguous_wide(rows, N, K, G, cus)) pl.tile = kMx256x256;
+    // masked: by the estimates at full experts (32 experts x 128 rows, 4096 x 7168, in 64 x 64 and 128 x 256 tiles: 144 and
+    // 94 us; 8 x 256, 3584 x 1536: 22 and 13; 8 x 256, 1024 x 2048: 8.5 and 12.5)
+    const auto cost = [&](int t) { return mx_cost_us(t, G * ceil_div(rows, mx_bm(t)) * ceil_div(N, mx_bn(t)), K, cus); };
+    pl.tile = form == kMxContiguous ? mx_contiguous_tile(rows, N, K, G, cus) : cost(kMx64x64) < cost(kMx128x256) ? kMx64x64 : kMx128x256;
     const int f = mx_forced_tile();
-    if (f == kMx128x256 || f == (form == kMxContiguous ? kMx256x256 : kMx64x64)) pl.tile = f;
+    if (f >= 0 && (form == kMxContiguous || f != kMx256x256)) pl.tile = f;
     pl.m_tiles = (int)ceil_div(rows, mx_bm(pl.tile));
     pl.n_tiles = (int)ceil_div(N, mx_bn(pl.tile));
     pl.steps_per_split = (int)ceil_div(K, 256);

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p
     D += (int64_t)e * ld * N;
   }
   if constexpr (FORM == kMxContiguous) {
-    static_assert(FORM != kMxContiguous || BM == 128, "a contiguous tile is one aligned block");
+    static_assert(128 % BM == 0, "a contiguous tile lies in one aligned block");
     int x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -384,7 +384,9 @@ size_t mx_workspace_bytes(int tile, int m_tiles, int n_tiles, int splits) {
 }
 
 hipError_t launch_mxfp4_gemm(int form, int tile, const MxGemmParams& p, hipStream_t stream) {
-  if (form == kMxContiguous) return launch_mx<128, 256, 2, 4, 3, kMxContiguous>(p, stream);
+  if (form == kMxContiguous)
+    return tile == kMx64x64 ? launch_mx<64, 64, 1, 4, 4, kMxContiguous>(p, stream)
+                            : launch_mx<128, 256, 2, 4, 3, kMxContiguous>(p, stream);
   if (form == kMxMasked)
     return tile == kMx64x64 ? launch_mx<64, 64, 1, 4, 4, kMxMasked>(p, stream)
                             : launch_mx<128, 256, 2, 4, 3, kMxMasked>(p, stream);

@@ -220,7 +220,7 @@ CONTIG = [([5, 130, 1], 144, 256, 0), ([128, 256, 1, 300], 272, 640, 3), ([0, 0,
           ([1500, 2, 900, 1100], 4096, 384, 2)]
 
 
-@pytest.mark.parametrize("tile", [None, "128x256", "256x256"])
+@pytest.mark.parametrize("tile", [None, "64x64", "128x256", "256x256"])
 @pytest.mark.parametrize("exact", [True, False])
 @pytest.mark.parametrize("counts,N,K,tail", CONTIG)
 def test_contiguous(monkeypatch, counts, N, K, tail, exact, tile):
@@ -269,7 +269,7 @@ def test_contiguous_many_experts_and_long_layout(monkeypatch):
     idx[-1] = -1
     a, sa = _operand(rng, (), len(idx), K, True)
     b, sb = _operand(rng, (G,), N, K, True)
-    for tile in ("128x256", "256x256"):
+    for tile in TILES:
         monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
         D = torch.full((len(idx), N), 7.0, dtype=torch.bfloat16, device=DEV)
         dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*map(_t, (a, sa, b, sb)), D, _t(idx))
