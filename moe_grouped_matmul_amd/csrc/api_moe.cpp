@@ -59,25 +59,26 @@ struct MxPlan {
 double mx_cost_us(int tile, int64_t tiles, int64_t K, int cus) {
   const double steps = (double)ceil_div(K, 256);
   if (tile == kMx64x64) return (double)ceil_div(tiles, 2 * cus) * (0.45 * steps + 1.5) + 3.0;
-  return (double)ceil_div(tiles, cus) * 1.05 * steps + 8.0;
+  return (double)ceil_div(tiles, cus) * (1.05 * steps + 3.0) + 5.0;
 }
 // The persistent kernel's: whole rounds of 256 x 256 tiles, then as it distributes the rest (the same rules). A step of
-// a large tile costs 1.1 us and 0.62 more as all CUs run one (the clock), of a 128 x 256 tile 1.25, of a 128 x 128
-// quarter 0.45. Fitted, with the above, to 19 dense shapes of 200-4096 rows with every tile shape forced: the tile of
-// least estimate was the fastest on each (1024 x 4096 x 4096: 20, 22 and 16 us; 1024 x 2048 x 7168: 16, 31 and 20;
-// 2048 x 4096 x 2048: 24, 16 and 17; 2500 x 4096 x 7168: 66, 66 and 45).
+// a large tile costs 0.66 us and 0.9 more as all CUs run one (the clock), of a 128 x 256 tile 1.0, of a 128 x 128
+// quarter 0.5; steps run in twos, a quarter's in fours. Fitted, with the above, to 28 dense shapes of 200-4352 rows with
+// every tile shape forced: the tile of least estimate was the fastest or within 10% of it on each (1024 x 4096 x 4096:
+// 20, 22 and 16 us; 1024 x 2048 x 7168: 16, 31 and 20; 2048 x 4096 x 2048: 24, 16 and 17; 2500 x 4096 x 7168: 66, 66 and
+// 45; 4000 x 4096 x 512: 33, 18 and 15).
 double mx_wide_us(int64_t large, int64_t small, int64_t K, int cus) {
-  const double steps = (double)ceil_div(K, 256);
   const int64_t rounds = large / cus;
   const int64_t rest = large % cus;
   const bool cut = rest > 0 && 2 * rest + small <= cus;
   const bool spread = rest > 0 && !cut;
   const int64_t halves = std::max<int64_t>(0, small + (cut ? 2 * rest : 0) - (spread ? 2 * (cus - rest) : 0));
-  const int64_t last = halves % cus;
-  double t = 1.72 * (double)rounds + 1.25 * (double)(halves / cus);
-  if (spread) t += 1.1 + 0.62 * (rounds ? 1.0 : (double)rest / (double)cus);
-  if (last) t += 2 * last <= cus ? 0.45 : 1.25;
-  return t * steps + 6.5;
+  const bool quarters = halves % cus > 0 && 2 * (halves % cus) <= cus;
+  const int64_t half_rounds = quarters ? halves / cus : ceil_div(halves, cus);
+  double step = 1.56 * (double)rounds + 1.0 * (double)half_rounds;
+  if (spread) step += 0.66 + 0.9 * (rounds ? 1.0 : (double)rest / (double)cus);
+  return step * 2.0 * (double)ceil_div(K, 512) + (quarters ? 2.0 * (double)ceil_div(K, 1024) : 0.0) +
+         (rounds || spread ? 11.0 : half_rounds ? 9.0 : 6.0);
 }
 
 // Dense: the tile shape of least estimated time; 64 x 64 tiles that leave CUs idle split K where that is estimated to
