@@ -18,6 +18,7 @@ namespace {
 using namespace dg;
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
+constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;  // of 256 threads in a launch: thread counts are 32 bits
 constexpr int64_t kMaxExperts = 1024;
 constexpr int64_t kMaxTopK = 16;
 
@@ -197,7 +198,7 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
     pl.steps_per_split = (int)ceil_div(K, 256);
   }
   const int64_t units = (int64_t)pl.n_tiles * (form == kMxMasked ? G : pl.splits);
-  if ((ceil_div(units, 8) * 8) * pl.m_tiles > kIntMax) return fail(DG_ERR_SHAPE, "too many tiles");
+  if (pl.tile != kMx256x256 && (ceil_div(units, 8) * 8) * pl.m_tiles > kMaxWorkgroups / 2) return fail(DG_ERR_SHAPE, "too many tiles");
   MxGemmParams p{};
   p.A = A;
   p.sfa = sfa;
@@ -243,7 +244,8 @@ int check_quant(int dtype, int64_t G, int64_t R, int64_t K) {
   if (rc) return rc;
   if (K <= 0 || K % 128) return fail(DG_ERR_SHAPE, "K must be a positive multiple of 128 (got %lld)", (long long)K);
   if (G < 0 || R < 0) return fail(DG_ERR_SHAPE, "G and row counts must be >= 0");
-  if (K > kIntMax || R > kIntMax || G > 65535 || ceil_div(R, 16) * (K / 128) > kIntMax)
+  // one launch, 4 rows x 512 columns a workgroup
+  if (K > kIntMax || R > kIntMax || G > 65535 || ceil_div(R, 4) * ceil_div(K, 512) > kMaxWorkgroups)
     return fail(DG_ERR_SHAPE, "problem too large");
   return DG_OK;
 }
@@ -307,7 +309,7 @@ int check_combine(int dtype, int64_t T, int64_t k, int64_t N, int64_t R) {
   if (T > kIntMax) return fail(DG_ERR_SHAPE, "T too large");
   if ((rc = check_topk(T, k))) return rc;
   if (N <= 0 || N % 16) return fail(DG_ERR_SHAPE, "N must be a positive multiple of 16 (got %lld)", (long long)N);
-  if (N > (int64_t)1 << 30 || R < 0 || R > kIntMax || T * ceil_div(N, 2048) > kIntMax)
+  if (N > (int64_t)1 << 30 || R < 0 || R > kIntMax)
     return fail(DG_ERR_SHAPE, "N or row count out of range");
   return DG_OK;
 }

@@ -3,8 +3,15 @@
 //   drows[row_of[t, j]] = w[t, j] * dy[t],   dw[t, j] = <rows[row_of[t, j]], dy[t]>
 // over the choices j whose row is in [0, R).  rows and drows are bf16, sums
 // are held in fp32 and rounded once; the order of a token's sum is that of its
-// choices.  HBM-bound: every chosen row is read once (forward and, for dw,
-// backward) or written once (drows).
+// choices.
+//
+// HBM-bound: every chosen row is read once (forward and, for dw, backward) or
+// written once (drows); 8 columns of a token are one 16-byte load per choice,
+// and all choices' loads are issued before the first is used.  Measured, bf16:
+// 4096 tokens x 8 x 7168 forward 125 us (4.2 TB/s), backward 191 us (5.2 TB/s
+// with dy read once; a row's dot and its gradient in one pass); 256 tokens x 8
+// x 7168, read from the Infinity Cache, 7.0 us (14 us with a workgroup per
+// token).
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
@@ -107,27 +114,36 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
 
 }  // namespace
 
+// A launch has at most 2^24 - 1 workgroups of 256 threads; longer calls run in chunks of tokens.
+constexpr int64_t kCombMaxGroups = (int64_t)1 << 23;
+
 hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
                           int64_t k, int64_t N, int64_t R, hipStream_t stream) {
   const int parts = (int)((N + 2047) / 2048);
-  if (bf16_y)
-    hipLaunchKernelGGL(combine_kernel<true>, dim3((unsigned)(T * parts)), dim3(256), 0, stream, rows, row_of, w, y, (int)k,
-                       (int)N, R, parts);
-  else
-    hipLaunchKernelGGL(combine_kernel<false>, dim3((unsigned)(T * parts)), dim3(256), 0, stream, rows, row_of, w, y, (int)k,
-                       (int)N, R, parts);
+  const int64_t chunk = kCombMaxGroups / parts;  // parts <= 2^19
+  for (int64_t t = 0; t < T; t += chunk) {
+    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * parts);
+    void* to = static_cast<uint8_t*>(y) + t * N * (bf16_y ? 2 : 4);
+    if (bf16_y)
+      hipLaunchKernelGGL(combine_kernel<true>, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k, to, (int)k, (int)N, R, parts);
+    else
+      hipLaunchKernelGGL(combine_kernel<false>, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k, to, (int)k, (int)N, R, parts);
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows, const int32_t* row_of, const float* w,
                               uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
                               hipStream_t stream) {
-  if (bf16_y)
-    hipLaunchKernelGGL(combine_bwd_kernel<true>, dim3((unsigned)(T * k)), dim3(256), 0, stream, dy, rows, row_of, w, drows,
-                       dw, (int)k, (int)N, R);
-  else
-    hipLaunchKernelGGL(combine_bwd_kernel<false>, dim3((unsigned)(T * k)), dim3(256), 0, stream, dy, rows, row_of, w, drows,
-                       dw, (int)k, (int)N, R);
+  const int64_t chunk = kCombMaxGroups / k;
+  for (int64_t t = 0; t < T; t += chunk) {
+    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * k);
+    const void* from = static_cast<const uint8_t*>(dy) + t * N * (bf16_y ? 2 : 4);
+    if (bf16_y)
+      hipLaunchKernelGGL(combine_bwd_kernel<true>, dim3(grid), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k, drows, dw + t * k, (int)k, (int)N, R);
+    else
+      hipLaunchKernelGGL(combine_bwd_kernel<false>, dim3(grid), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k, drows, dw + t * k, (int)k, (int)N, R);
+  }
   return hipGetLastError();
 }
 

@@ -29,6 +29,14 @@
 // in LDS, then over groups of 16 workgroups and over the groups, each by the
 // last workgroup to arrive (agent-scope counters, coherent partials) and in a
 // fixed order, so results do not depend on scheduling.
+//
+// Bounds.  Forward: the vector units (sorting and k rounds over 16 values per
+// lane), then the tail over workgroups: 32768 x 256 fp32, k = 8, 22 us, of
+// which the logits' bytes at the copy rate are 7 and the tail about 6 (131 us
+// with a wave per token and no sorted keys, 26 with 16 lanes; 22-bit keys in 32
+// bits with the expert in the low ones and a second comparison 29).  64 x 256
+// bf16 in 4 workgroups 7.2 us, a chain of dependent steps.  Gradient: memory,
+// 17 us for 67 MB (3.9 TB/s).
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"

@@ -22,6 +22,17 @@
 // two 128-element halves.  The weights are the row operand of the MFMA and
 // their rows are permuted inside a wave's columns, so a lane ends with up to
 // 16 consecutive output columns of one row.
+//
+// Two tiles.  128 x 256 (8 waves, 3 slots, one workgroup a CU) reads each
+// weight once where an expert has up to 128 rows: 32 experts x 128 rows, 2048
+// in all, 4096 x 7168, 94 us, 5.5 TB/s of weights, rows and output, which is
+// above the card's large copy.  64 x 64 (4 waves, 4 slots, two workgroups a
+// CU) occupies the CUs where large tiles are few; it is bound by the latency of
+// its few steps: 64 x 7168 x 2048 6.2 us (7.8 MB of weights, which stay in the
+// Infinity Cache between calls; an empty launch takes 2.5), 512 x 4096 x 4096
+// 11.4 us.  K is split where that leaves CUs idle and the sum of the parts, by
+// the last workgroup of a tile, costs less than it saves.  Large dense and
+// contiguous products run on the persistent tiles of mxfp4_wide.hip.
 
 #include "dg_internal.hpp"
 #include "gemm_common.hpp"

@@ -11,7 +11,9 @@
 // Codes are packed two to a byte (the lower nibble first), the scale bytes of
 // four consecutive blocks to an int32 word, words MN-major ([K/128][rows]).
 //
-// Both kernels are HBM-bound.
+// Both kernels are HBM-bound: a row is read once, a block's largest magnitude is a
+// maximum over the 4 lanes (bf16 input, 8 values each) or 8 (fp32, 4 each)
+// that hold it.
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"

@@ -118,6 +118,33 @@ def test_combine():
     assert np.all(np.abs(dw.double().cpu().numpy() - dwant) <= (N / 256 + 20) * U * dmag)
 
 
+def test_combine_of_many_tokens():
+    """More workgroups than one launch takes."""
+    N, R = 16, 40
+    rows = _rand((R, N), 6)
+    h = rows.double().cpu().numpy()
+    for T, k in (((1 << 23) + 7, 1), ((1 << 20) + 9, 8)):
+        at = [0, 1, (1 << 20) - 1, 1 << 20, T - 1]
+        ro = torch.full((T, k), -1, dtype=torch.int32, device=DEV)
+        ro[torch.tensor(at, device=DEV)] = torch.arange(len(at) * k, dtype=torch.int32, device=DEV).reshape(-1, k)
+        w = torch.full((T, k), 0.75, device=DEV)
+        y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device=DEV)
+        dg.dg_moe_combine(rows, ro, w, y)
+        idx, c = np.arange(len(at) * k).reshape(-1, k), np.full((len(at), k), 0.75, np.float32)
+        want, mag = moe.combine(h, idx, c)
+        assert np.all(np.abs(_sample(y, at) - want) <= 2.0 ** -8 * 1.01 * np.abs(want) + (k + 1) * U * mag)
+        assert int((y != 0).any(1).sum()) == len(at)
+        drows, dw = torch.full_like(rows, 7.0), torch.full((T, k), 7.0, device=DEV)
+        dg.dg_moe_combine_bwd(y, rows, ro, w, drows, dw)
+        g, dwant, dmag = moe.combine_grad(_sample(y, at).astype(np.float64), h, idx, c)
+        used = len(at) * k
+        assert np.all(np.abs(drows[:used].double().cpu().numpy() - g[:used]) <= (2.0 ** -8 * 1.01 + U) * np.abs(g[:used]))
+        assert bool((drows[used:] == 7).all())
+        assert np.all(np.abs(_sample(dw, at) - dwant) <= (N / 256 + 20) * U * dmag)
+        dw[torch.tensor(at, device=DEV)] = 0
+        assert not bool(dw.any())
+
+
 def test_gate():
     T, E, k = (1 << 22) + 5, 1024, 2  # 4.3e9 logits in bf16
     x = _rand((T, E), 5)
