@@ -7,17 +7,26 @@
 //
 // HBM-bound: every chosen row is read once (forward and, for dw, backward) or
 // written once (drows); 8 columns of a token are one 16-byte load per choice,
-// and all choices' loads are issued before the first is used.  Measured, bf16:
-// 4096 tokens x 8 x 7168 forward 125 us (4.2 TB/s), backward 191 us (5.2 TB/s
-// with dy read once; a row's dot and its gradient in one pass); 256 tokens x 8
-// x 7168, read from the Infinity Cache, 7.0 us (14 us with a workgroup per
-// token).
-
+// and all choices' loads are issued before the first is used.  Rows that the
+// Infinity Cache cannot hold from one call to the next are streamed past it
+// (non-temporal), and then the backward pass takes a whole token per
+// workgroup, which reads its dy once.  Measured, bf16, 4096 tokens x 8 x 7168:
+// forward 93 us (5.7 TB/s), backward 206 us (4.9 TB/s); 256 tokens x 8 x 7168, held by the Infinity
+// Cache, 7.0 us forward (14 with a workgroup per token).
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
 
 namespace dg {
 namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+template <bool NT>
+__device__ __forceinline__ uint4 load8(const uint16_t* p) {
+  if constexpr (!NT) return *reinterpret_cast<const uint4*>(p);
+  const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  return uint4{v.x, v.y, v.z, v.w};
+}
 
 __device__ __forceinline__ void bf16x8(uint4 w, float* v) {
   v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
@@ -29,10 +38,21 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
+template <bool BF16>
+__device__ __forceinline__ void values8(const void* x, int64_t at, float* d) {
+  if constexpr (BF16) {
+    bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at), d);
+  } else {
+    const float* s = static_cast<const float*>(x) + at;
+    const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
+    d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w; d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
+  }
+}
+
 // T * ceil(N / 2048) workgroups: a thread holds 8 columns of one token and has the
 // rows of eight choices in flight; a choice without a row reads nothing.
 constexpr int kCombBatch = 8;
-template <bool BF16>
+template <bool BF16, bool NT>
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, void* __restrict__ y, int k, int N,
                                                       int64_t R, int parts) {
@@ -51,7 +71,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
         const int64_t r = row_of[t * k + j0 + j];
         if (r >= 0 && r < R) {
           wj[j] = w[t * k + j0 + j];
-          raw[j] = *reinterpret_cast<const uint4*>(rows + r * N + c);
+          raw[j] = load8<NT>(rows + r * N + c);
         }
       }
     }
@@ -90,14 +110,8 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
   float dot = 0.f;
   for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
     float v[8], d[8], o[8];
-    bf16x8(*reinterpret_cast<const uint4*>(rows + r * N + c), v);
-    if constexpr (BF16) {
-      bf16x8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dy) + t * N + c), d);
-    } else {
-      const float* s = static_cast<const float*>(dy) + t * N + c;
-      const float4 a = *reinterpret_cast<const float4*>(s), b = *reinterpret_cast<const float4*>(s + 4);
-      d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w; d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
-    }
+    bf16x8(load8<false>(rows + r * N + c), v);
+    values8<BF16>(dy, t * N + c, d);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       dot = __builtin_fmaf(v[e], d[e], dot);
@@ -112,22 +126,81 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
   if (threadIdx.x == 0) dw[i] = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
+// one workgroup per token, rows and drows streamed
+template <bool BF16>
+__global__ void __launch_bounds__(256) combine_bwd_token_kernel(const void* __restrict__ dy, const uint16_t* __restrict__ rows,
+                                                                const int32_t* __restrict__ row_of,
+                                                                const float* __restrict__ w, uint16_t* __restrict__ drows,
+                                                                float* __restrict__ dw, int k, int N, int64_t R) {
+  __shared__ float part[kCombBatch][4];
+  const int64_t t = blockIdx.x;
+  for (int j0 = 0; j0 < k; j0 += kCombBatch) {
+    float dot[kCombBatch];
+#pragma unroll
+    for (int j = 0; j < kCombBatch; ++j) dot[j] = 0.f;
+    for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
+      uint4 raw[kCombBatch];
+      int64_t r[kCombBatch];  // uniform, -1: no row
+#pragma unroll
+      for (int j = 0; j < kCombBatch; ++j) {
+        r[j] = j0 + j < k ? row_of[t * k + j0 + j] : -1;
+        if (r[j] >= R) r[j] = -1;
+        raw[j] = r[j] >= 0 ? load8<true>(rows + r[j] * N + c) : uint4{0u, 0u, 0u, 0u};
+      }
+      float d[8];
+      values8<BF16>(dy, t * N + c, d);
+#pragma unroll
+      for (int j = 0; j < kCombBatch; ++j) {
+        if (r[j] < 0) continue;
+        const float wj = w[t * k + j0 + j];
+        float v[8], o[8];
+        bf16x8(raw[j], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dot[j] = __builtin_fmaf(v[e], d[e], dot[j]);
+          o[e] = wj * d[e];
+        }
+        const uint4 p = pack8(o);
+        const u32x4 q{p.x, p.y, p.z, p.w};
+        __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(drows + r[j] * N + c));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kCombBatch; ++j) {
+#pragma unroll
+      for (int o = 32; o >= 1; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
+      if ((threadIdx.x & 63) == 0) part[j][threadIdx.x >> 6] = dot[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < kCombBatch && j0 + (int)threadIdx.x < k) {
+      const float* s = part[threadIdx.x];
+      dw[t * k + j0 + threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    __syncthreads();  // before the next eight choices' sums
+  }
+}
+
 }  // namespace
 
 // A launch has at most 2^24 - 1 workgroups of 256 threads; longer calls run in chunks of tokens.
 constexpr int64_t kCombMaxGroups = (int64_t)1 << 23;
 
+// The chosen rows and what else the call touches do not stay in the 256 MB Infinity Cache: from 128 MB of rows (4096 x
+// 7168 with 2, 3, 4, 8 choices, streamed against not: forward 32 / 36, 41 / 46, 50 / 58, 93 / 105 us; forward and
+// backward 97 / 91, 129 / 130, 163 / 169, 299 / 317).
+static bool streams(int64_t T, int64_t k, int64_t N, int64_t R) { return (T * k < R ? T * k : R) * N >= (int64_t)64 << 20; }
+
 hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
                           int64_t k, int64_t N, int64_t R, hipStream_t stream) {
   const int parts = (int)((N + 2047) / 2048);
   const int64_t chunk = kCombMaxGroups / parts;  // parts <= 2^19
+  const bool nt = streams(T, k, N, R);
+  const auto kernel = bf16_y ? (nt ? combine_kernel<true, true> : combine_kernel<true, false>)
+                             : (nt ? combine_kernel<false, true> : combine_kernel<false, false>);
   for (int64_t t = 0; t < T; t += chunk) {
     const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * parts);
-    void* to = static_cast<uint8_t*>(y) + t * N * (bf16_y ? 2 : 4);
-    if (bf16_y)
-      hipLaunchKernelGGL(combine_kernel<true>, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k, to, (int)k, (int)N, R, parts);
-    else
-      hipLaunchKernelGGL(combine_kernel<false>, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k, to, (int)k, (int)N, R, parts);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k,
+                       static_cast<void*>(static_cast<uint8_t*>(y) + t * N * (bf16_y ? 2 : 4)), (int)k, (int)N, R, parts);
   }
   return hipGetLastError();
 }
@@ -135,14 +208,16 @@ hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const flo
 hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows, const int32_t* row_of, const float* w,
                               uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
                               hipStream_t stream) {
-  const int64_t chunk = kCombMaxGroups / k;
+  const bool token = streams(T, k, N, R);
+  const auto kernel = token ? (bf16_y ? combine_bwd_token_kernel<true> : combine_bwd_token_kernel<false>)
+                            : (bf16_y ? combine_bwd_kernel<true> : combine_bwd_kernel<false>);
+  const int64_t per = token ? 1 : k;  // workgroups of a token
+  const int64_t chunk = kCombMaxGroups / per;
   for (int64_t t = 0; t < T; t += chunk) {
-    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * k);
-    const void* from = static_cast<const uint8_t*>(dy) + t * N * (bf16_y ? 2 : 4);
-    if (bf16_y)
-      hipLaunchKernelGGL(combine_bwd_kernel<true>, dim3(grid), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k, drows, dw + t * k, (int)k, (int)N, R);
-    else
-      hipLaunchKernelGGL(combine_bwd_kernel<false>, dim3(grid), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k, drows, dw + t * k, (int)k, (int)N, R);
+    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * per);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream,
+                       static_cast<const void*>(static_cast<const uint8_t*>(dy) + t * N * (bf16_y ? 2 : 4)), rows, row_of + t * k,
+                       w + t * k, drows, dw + t * k, (int)k, (int)N, R);
   }
   return hipGetLastError();
 }

@@ -118,6 +118,33 @@ def test_combine():
     assert np.all(np.abs(dw.double().cpu().numpy() - dwant) <= (N / 256 + 20) * U * dmag)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_combine_of_rows_past_the_cache(dtype):
+    """Rows that are streamed; more choices than are in flight at once, tokens without rows, a last partial run of columns."""
+    T, k, N = 1100, 9, 7184
+    R = T * k
+    rng = np.random.default_rng(8)
+    ro = rng.permutation(R).reshape(T, k).astype(np.int32)
+    ro[rng.random((T, k)) < 0.05] = -1
+    ro[5], ro[T - 1, 0], ro[7, 8] = -1, R, R + 9
+    w = rng.standard_normal((T, k)).astype(np.float32)
+    rows, dy = _rand((R, N), 9), _rand((T, N), 10, dtype)
+    y, drows, dw = torch.full((T, N), 7.0, dtype=dtype, device=DEV), torch.full_like(rows, 7.0), torch.full((T, k), 7.0, device=DEV)
+    dro, dwt = torch.from_numpy(ro).to(DEV), torch.from_numpy(w).to(DEV)
+    dg.dg_moe_combine(rows, dro, dwt, y)
+    dg.dg_moe_combine_bwd(dy, rows, dro, dwt, drows, dw)
+    h = rows.float().cpu().numpy()
+    want, mag = moe.combine(h, ro, w.astype(np.float64))
+    out = 2.0 ** -8 if dtype is torch.bfloat16 else 0.0
+    assert np.all(np.abs(y.double().cpu().numpy() - want) <= out * 1.01 * np.abs(want) + (k + 1) * U * mag)
+    g, dwant, dmag = moe.combine_grad(dy.double().cpu().numpy(), h, ro, w.astype(np.float64))
+    got = drows.float().cpu().numpy()
+    free = np.isnan(g[:, 0])
+    assert free.any() and np.all(got[free] == 7)
+    assert np.all(np.abs(got[~free] - g[~free]) <= (2.0 ** -8 * 1.01 + U) * np.abs(g[~free]))
+    assert np.all(np.abs(dw.double().cpu().numpy() - dwant) <= (N / 256 + 20) * U * dmag)
+
+
 def test_combine_of_many_tokens():
     """More workgroups than one launch takes."""
     N, R = 16, 40
