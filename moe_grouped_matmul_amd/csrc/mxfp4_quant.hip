@@ -21,6 +21,8 @@
 namespace dg {
 namespace {
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
 // c of a block with largest magnitude bits u (sign cleared): with amax = 1.f * 2^(E - 127)
 // and 6 = 1.5 * 2^2 the least exponent is E - 129 where 1.f <= 1.5, else E - 128
 __device__ __forceinline__ int mx_code(uint32_t u) {
@@ -36,9 +38,9 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // A 256-thread workgroup handles 4 PER rows x 512 columns of one group: each
 // of its four waves PER rows, every load and store of the wide side a whole
 // kilobyte (fp32 input: two, each lane 16 bytes of either), the rows of a wave
-// in flight together.  Rows per wave by measurement, 8 x 4096 x 7168: fp32
-// input 1, 2, 4 rows 190, 204, 209 us (5.6 TB/s at 1); bf16 input 113-122, 105,
-// 106 us (5.6 TB/s); reading back 146-158, 105, 106 us (5.6 TB/s).
+// in flight together.  Rows per wave by measurement, 8 x 4096 x 7168, before
+// large arrays were streamed: fp32 input 1, 2, 4 rows 190, 204, 209 us; bf16
+// input 113-122, 105, 106 us; reading back 146-158, 105, 106 us.
 constexpr int kQCols = 512;
 
 // first row and column of this workgroup
@@ -58,8 +60,8 @@ __device__ __forceinline__ uint32_t dpp_max(uint32_t u) {
 }
 
 // row_token: row r takes row row_token[r] of x, rows whose entry is outside
-// [0, T) are not written
-template <bool BF16, int PER>
+// [0, T) are not written.  NT: x is streamed past the caches
+template <bool BF16, int PER, bool NT>
 __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* __restrict__ x, uint8_t* __restrict__ q,
                                                           int32_t* __restrict__ sf, const int32_t* __restrict__ row_token,
                                                           int64_t T, int64_t R, int K) {
@@ -93,8 +95,15 @@ __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* __restrict
     for (int h = 0; h < NP; ++h) {
       const int col = col0 + h * 256 + lane * NE;
       raw[i][h] = uint4{0u, 0u, 0u, 0u};
-      if (row && col < K)
-        raw[i][h] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(x) + (src * (int64_t)K + col) * (BF16 ? 2 : 4));
+      if (row && col < K) {
+        const void* from = static_cast<const uint8_t*>(x) + (src * (int64_t)K + col) * (BF16 ? 2 : 4);
+        if constexpr (NT) {
+          const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4*>(from));
+          raw[i][h] = uint4{v.x, v.y, v.z, v.w};
+        } else {
+          raw[i][h] = *static_cast<const uint4*>(from);
+        }
+      }
     }
   }
 #pragma unroll
@@ -151,7 +160,8 @@ __global__ void __launch_bounds__(256) quant_mxfp4_kernel(const void* __restrict
   }
 }
 
-template <bool BF16, int PER>
+// NT: y is streamed past the caches
+template <bool BF16, int PER, bool NT>
 __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t* __restrict__ q, const int32_t* __restrict__ sf,
                                                             void* __restrict__ y, int64_t R, int K) {
   int col;
@@ -183,13 +193,17 @@ __global__ void __launch_bounds__(256) dequant_mxfp4_kernel(const uint8_t* __res
     }
     if (col >= K || r0 + i >= R) continue;
     const int64_t off = (g * R + r0 + i) * (int64_t)K + col;
+    const auto put = [&](void* to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+      const u32x4 w{a, b, c, d};
+      if constexpr (NT) __builtin_nontemporal_store(w, static_cast<u32x4*>(to));
+      else *static_cast<u32x4*>(to) = w;
+    };
     if constexpr (BF16) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + off) =
-          uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      put(static_cast<uint16_t*>(y) + off, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     } else {
       float* d = static_cast<float*>(y) + off;
-      *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(d + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      put(d, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      put(d + 4, __float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
     }
   }
 }
@@ -199,25 +213,28 @@ dim3 q_grid(int64_t G, int64_t R, int64_t K) {
   return dim3((unsigned)((R + 4 * PER - 1) / (4 * PER) * ((K + kQCols - 1) / kQCols)), (unsigned)G);
 }
 
+// The wide side is streamed from 16 MB on (there and back, streamed against not: 8 x 4096 x 7168 fp32 269 / 310 us, 4096 x
+// 7168 fp32 38 / 43, bf16 28 / 31, 2048 x 7168 bf16 15.8 / 16.6, 1024 x 4096 bf16 the same; 8192 rows gathered, back only,
+// 46 / 63).
+bool streams(int64_t G, int64_t R, int64_t K, bool bf16) { return G * R * K * (bf16 ? 2 : 4) >= (int64_t)16 << 20; }
+
 }  // namespace
 
 hipError_t launch_quant_mxfp4(const void* x, bool bf16, uint8_t* q, int32_t* sf, const int32_t* row_token, int64_t G,
                               int64_t T, int64_t R, int64_t K, hipStream_t stream) {
-  if (bf16)
-    hipLaunchKernelGGL((quant_mxfp4_kernel<true, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, x, q, sf, row_token, T, R,
-                       (int)K);
-  else
-    hipLaunchKernelGGL((quant_mxfp4_kernel<false, 1>), q_grid<1>(G, R, K), dim3(256), 0, stream, x, q, sf, row_token, T, R,
-                       (int)K);
+  const bool nt = !row_token && streams(G, R, K, bf16);  // gathered rows are read again
+  const auto kernel = bf16 ? (nt ? quant_mxfp4_kernel<true, 2, true> : quant_mxfp4_kernel<true, 2, false>)
+                           : (nt ? quant_mxfp4_kernel<false, 1, true> : quant_mxfp4_kernel<false, 1, false>);
+  hipLaunchKernelGGL(kernel, bf16 ? q_grid<2>(G, R, K) : q_grid<1>(G, R, K), dim3(256), 0, stream, x, q, sf, row_token, T, R, (int)K);
   return hipGetLastError();
 }
 
 hipError_t launch_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, bool bf16, int64_t G, int64_t R,
                                 int64_t K, hipStream_t stream) {
-  if (bf16)
-    hipLaunchKernelGGL((dequant_mxfp4_kernel<true, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, q, sf, y, R, (int)K);
-  else
-    hipLaunchKernelGGL((dequant_mxfp4_kernel<false, 2>), q_grid<2>(G, R, K), dim3(256), 0, stream, q, sf, y, R, (int)K);
+  const bool nt = streams(G, R, K, bf16);
+  const auto kernel = bf16 ? (nt ? dequant_mxfp4_kernel<true, 2, true> : dequant_mxfp4_kernel<true, 2, false>)
+                           : (nt ? dequant_mxfp4_kernel<false, 2, true> : dequant_mxfp4_kernel<false, 2, false>);
+  hipLaunchKernelGGL(kernel, q_grid<2>(G, R, K), dim3(256), 0, stream, q, sf, y, R, (int)K);
   return hipGetLastError();
 }
 
