@@ -8,11 +8,13 @@
 // HBM-bound: every chosen row is read once (forward and, for dw, backward) or
 // written once (drows); 8 columns of a token are one 16-byte load per choice,
 // and all choices' loads are issued before the first is used.  Rows that the
-// Infinity Cache cannot hold from one call to the next are streamed past it
-// (non-temporal), and then the backward pass takes a whole token per
-// workgroup, which reads its dy once.  Measured, bf16, 4096 tokens x 8 x 7168:
-// forward 93 us (5.7 TB/s), backward 206 us (4.9 TB/s); 256 tokens x 8 x 7168, held by the Infinity
-// Cache, 7.0 us forward (14 with a workgroup per token).
+// Infinity Cache cannot hold from one call to the next are streamed past it,
+// and y and drows with them (non-temporal), and then the backward pass takes a
+// whole token per workgroup, which reads its dy once.  Measured, bf16, 4096
+// tokens x 8 x 7168: forward 91 us (5.8 TB/s), backward 189 us (5.3 TB/s); 256
+// tokens x 8 x 7168, held by the Infinity Cache, 6.8 us forward (14 with a
+// workgroup per token).
+
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
 
@@ -26,6 +28,13 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
   if constexpr (!NT) return *reinterpret_cast<const uint4*>(p);
   const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   return uint4{v.x, v.y, v.z, v.w};
+}
+
+template <bool NT>
+__device__ __forceinline__ void store16(void* p, uint4 a) {
+  const u32x4 v{a.x, a.y, a.z, a.w};
+  if constexpr (NT) __builtin_nontemporal_store(v, static_cast<u32x4*>(p));
+  else *static_cast<u32x4*>(p) = v;
 }
 
 __device__ __forceinline__ void bf16x8(uint4 w, float* v) {
@@ -84,11 +93,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
     }
   }
   if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(y) + t * N + c) = pack8(s);
+    store16<NT>(static_cast<uint16_t*>(y) + t * N + c, pack8(s));
   } else {
     float* d = static_cast<float*>(y) + t * N + c;
-    *reinterpret_cast<float4*>(d) = make_float4(s[0], s[1], s[2], s[3]);
-    *reinterpret_cast<float4*>(d + 4) = make_float4(s[4], s[5], s[6], s[7]);
+    store16<NT>(d, uint4{__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3])});
+    store16<NT>(d + 4, uint4{__float_as_uint(s[4]), __float_as_uint(s[5]), __float_as_uint(s[6]), __float_as_uint(s[7])});
   }
 }
 
@@ -160,9 +169,7 @@ __global__ void __launch_bounds__(256) combine_bwd_token_kernel(const void* __re
           dot[j] = __builtin_fmaf(v[e], d[e], dot[j]);
           o[e] = wj * d[e];
         }
-        const uint4 p = pack8(o);
-        const u32x4 q{p.x, p.y, p.z, p.w};
-        __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(drows + r[j] * N + c));
+        store16<true>(drows + r[j] * N + c, pack8(o));
       }
     }
 #pragma unroll
@@ -185,16 +192,18 @@ __global__ void __launch_bounds__(256) combine_bwd_token_kernel(const void* __re
 // A launch has at most 2^24 - 1 workgroups of 256 threads; longer calls run in chunks of tokens.
 constexpr int64_t kCombMaxGroups = (int64_t)1 << 23;
 
-// The chosen rows and what else the call touches do not stay in the 256 MB Infinity Cache: from 128 MB of rows (4096 x
-// 7168 with 2, 3, 4, 8 choices, streamed against not: forward 32 / 36, 41 / 46, 50 / 58, 93 / 105 us; forward and
-// backward 97 / 91, 129 / 130, 163 / 169, 299 / 317).
-static bool streams(int64_t T, int64_t k, int64_t N, int64_t R) { return (T * k < R ? T * k : R) * N >= (int64_t)64 << 20; }
+// Rows that do not stay in the 256 MB Infinity Cache with what else is in use: from 96 MB on, from 48 MB on where drows is
+// written too. Streamed against not, forward: 33, 59, 88, 235 million values 13.2 / 12.7, 31 / 36, 39 / 46, 91 / 105 us;
+// with the backward pass: 15, 29, 34, 59, 235 million 22.9 / 20.7, 38 / 41, 42 / 52, 82 / 91, 280 / 317 us.
+static bool streams(int64_t T, int64_t k, int64_t N, int64_t R, int64_t mb) {
+  return (T * k < R ? T * k : R) * N * 2 >= mb << 20;
+}
 
 hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
                           int64_t k, int64_t N, int64_t R, hipStream_t stream) {
   const int parts = (int)((N + 2047) / 2048);
   const int64_t chunk = kCombMaxGroups / parts;  // parts <= 2^19
-  const bool nt = streams(T, k, N, R);
+  const bool nt = streams(T, k, N, R, 96);
   const auto kernel = bf16_y ? (nt ? combine_kernel<true, true> : combine_kernel<true, false>)
                              : (nt ? combine_kernel<false, true> : combine_kernel<false, false>);
   for (int64_t t = 0; t < T; t += chunk) {
@@ -208,7 +217,7 @@ hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const flo
 hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows, const int32_t* row_of, const float* w,
                               uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
                               hipStream_t stream) {
-  const bool token = streams(T, k, N, R);
+  const bool token = streams(T, k, N, R, 48);
   const auto kernel = token ? (bf16_y ? combine_bwd_token_kernel<true> : combine_bwd_token_kernel<false>)
                             : (bf16_y ? combine_bwd_kernel<true> : combine_bwd_kernel<false>);
   const int64_t per = token ? 1 : k;  // workgroups of a token
