@@ -1,4 +1,5 @@
-"""Ahead-of-time build of the gfx950 library ``libdg_mi355x.so`` (in-tree).
+"""Ahead-of-time build of the gfx950 library ``libdg_mi355x.so`` (in-tree),
+and of ``_args.so``, the argument check of its Python binding.
 
 Compiles every HIP source under ``csrc/`` with hipcc for gfx950 and links one
 shared library next to this file.  Kernel register/scratch usage reported by
@@ -11,6 +12,7 @@ Usage: python -m moe_grouped_matmul_amd.build   (or build() from Python)
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB_NAME = "libdg_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+ARGS_PATH = os.path.join(HERE, "_args.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "mxfp4_wide.hip",
@@ -56,6 +59,22 @@ def _compile(src, build_dir, extra):
     return obj, r.stderr
 
 
+def _build_args():
+    """The argument check: host code on torch's headers, no HIP."""
+    import torch
+    from torch.utils import cpp_extension
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = ARGS_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-isystem{p}" for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]],
+           os.path.join(CSRC, "py_args.cpp"), "-o", tmp, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for py_args.cpp:\n{r.stderr}")
+    os.replace(tmp, ARGS_PATH)
+
+
 def build(verbose=False, out_path=None, extra_flags=()):
     """Compile and link; out_path/extra_flags serve experiments with compile-time
     tuning macros (the default build is what the package loads)."""
@@ -63,7 +82,10 @@ def build(verbose=False, out_path=None, extra_flags=()):
     build_dir = BUILD if out_path is None else os.path.join(os.path.dirname(out_path), "_build")
     os.makedirs(build_dir, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        args = ex.submit(_build_args) if out_path is None else None
         results = list(ex.map(lambda s: _compile(s, build_dir, list(extra_flags)), SOURCES))
+        if args is not None:
+            args.result()
     report = []
     for (obj, log), src in zip(results, SOURCES):
         lines = [l for l in log.splitlines() if "remark" in l or "Function Name" in l or ":" in l]

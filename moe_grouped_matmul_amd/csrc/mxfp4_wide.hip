@@ -239,14 +239,17 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
     *e = CONTIG ? __builtin_amdgcn_readfirstlane((int)expert_of[CONTIG ? b : 0]) : 0;
   };
 
-  // ---- loads.  A 1 KB load fills 8 LDS rows: lane l writes row l / 8, position l % 8, from K chunk (l % 8) ^ (l / 8).
+  // ---- loads.  A 1 KB load fills 8 LDS rows: lane l writes row l / 8, position l % 8, from K chunk 2 p % 8 + p / 4 with
+  // p = (l % 8) ^ (l / 8): even chunks, one per lane group of a read, lie in one half of a row's positions and odd ones in
+  // the other, without which a read takes twice its cycles (two lanes to a bank).
   // Wave w fills rows 64 w + 8 i of A and of B in load i; B's row 64 w + in holds the column that makes a lane's
   // outputs consecutive.  A lane's offset is fixed for the whole kernel and everything else is in the scalar offset,
   // which the range check includes: rows past the tile's end read as zeros.  Past K a row runs into the next one
   // (or the end, zeros), but its scale words there are past their range and read as 2^-127: against another 2^-127
   // no product is left in fp32, so neither a half step nor a whole one past K adds anything.
   const int l8 = lane >> 3;
-  const int chunk = (lane & 7) ^ l8;
+  const int pos = (lane & 7) ^ l8;
+  const int chunk = (pos & 3) << 1 | pos >> 2;
   // Of a quarter the waves 2 and 3 fill rows 128 on with the same rows' next step: two steps to a slot.
   uint32_t a_off, b_off, sa_off, sb_off;
   int stride = 1;  // steps in a slot, of the unit at the issue pointer
@@ -303,8 +306,8 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
 
   // ---- LDS reads.  Lane group q = lane / 16 holds blocks 2 q (first half) and 2 q + 1 (second half) of a step's eight:
   // their scale bytes are neighbours and one 2-byte read serves both halves.
-  const uint32_t fr0 = (uint32_t)(q16 * 128 + (((2 * q) ^ (lane & 7)) << 4));
-  const uint32_t fr1 = (uint32_t)(q16 * 128 + (((2 * q + 1) ^ (lane & 7)) << 4));
+  const uint32_t fr0 = (uint32_t)(q16 * 128 + ((q ^ (lane & 7)) << 4));
+  const uint32_t fr1 = (uint32_t)(q16 * 128 + (((q + 4) ^ (lane & 7)) << 4));
   // the wave's first LDS row of A and of B: (128 rows, 128 columns) of a large tile, (all 128 rows, 64
   // columns) of a small one, (all 128 rows, 32 columns) of a quarter
   const uint32_t s_base = (uint32_t)(SLOT_S + (q >> 1) * (BM + BN) * 4 + q16 * 4 + 2 * (q & 1));

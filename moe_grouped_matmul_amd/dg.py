@@ -82,10 +82,17 @@ class DGError(RuntimeError):
 _lib = None
 
 
+def _pointer(*args):
+    """_args.so's function in its place from the first load of the library on."""
+    load_library()
+    return _pointer(*args)
+
+
+
 def load_library():
     """Load (once) and return the ctypes handle of the in-tree library; raises
     if it is missing."""
-    global _lib
+    global _lib, _pointer
     if _lib is not None:
         return _lib
     p = LIB_PATH
@@ -93,6 +100,10 @@ def load_library():
         raise RuntimeError(
             f"{p} not found: build it first (python -m moe_grouped_matmul_amd.build); "
             "there is no fallback path")
+    try:
+        from moe_grouped_matmul_amd import _args
+    except ImportError as e:
+        raise RuntimeError("_args.so not found or not loadable: build it first (python -m moe_grouped_matmul_amd.build)") from e
     lib = ctypes.CDLL(p)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     lib.dg_fp8_gemm_nt.argtypes = [P, P, P, P, P, I64, I64, I64, P, SZ, P]
@@ -139,7 +150,7 @@ def load_library():
                  "dg_moe_combine", "dg_moe_combine_bwd", "dg_set_num_cus", "dg_get_num_cus",
                  "dg_get_m_alignment_for_contiguous_layout"):
         getattr(lib, name).restype = I
-    _lib = lib
+    _lib, _pointer = lib, _args.pointer
     return lib
 
 
@@ -527,8 +538,9 @@ _FLOATS = {torch.float32: DG_F32, torch.bfloat16: DG_BF16}
 
 def _arg(t, name, dtype, shape, dev):
     """Pointer of tensor t, checked: dtype, shape, contiguity, current device."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
+    p = _pointer(t, dtype, shape, dev)
+    if p is not None:
+        return p
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.get_device() != dev:

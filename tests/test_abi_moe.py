@@ -128,6 +128,20 @@ def test_layout_and_combine(lib):
     _expect(lib, b(None, 1, None, None, None, None, None, 0, 2, 16, 9, NULL), OK)
 
 
+def test_argument_check(lib):
+    """The native check of the binding's tensors: a host tensor is none of its, wrong arguments are errors."""
+    import torch
+
+    from moe_grouped_matmul_amd import _args
+
+    t = torch.zeros(3, 4)
+    assert dg._pointer is _args.pointer
+    assert _args.pointer(t, torch.float32, (3, 4), 0) is None
+    for bad in ((t, 1, (3, 4), 0), (1, torch.float32, (3, 4), 0), (t, torch.float32, [3, 4], 0), (t, torch.float32, (3, 4), "x"), (t,)):
+        with pytest.raises(TypeError):
+            _args.pointer(*bad)
+
+
 def test_no_device(lib):
     import torch
 
