@@ -7,13 +7,16 @@
 //
 // HBM-bound: every chosen row is read once (forward and, for dw, backward) or
 // written once (drows); 8 columns of a token are one 16-byte load per choice,
-// and all choices' loads are issued before the first is used.  Rows that the
+// and all choices' loads are issued before the first is used.  A wave takes a
+// run of columns of a token, or a choice of the backward pass: workgroups would
+// idle on short rows (2569 tokens x 8 x 320 with the gradient, a workgroup and
+// a wave each: 20 and 12 us; 256 x 8 x 7168 20.6 and 18.1).  Rows that the
 // Infinity Cache cannot hold from one call to the next are streamed past it,
 // and y and drows with them (non-temporal), and then the backward pass takes a
-// whole token per workgroup, which reads its dy once.  Measured, bf16, 4096
-// tokens x 8 x 7168: forward 91 us (5.8 TB/s), backward 189 us (5.3 TB/s); 256
-// tokens x 8 x 7168, held by the Infinity Cache, 6.8 us forward (14 with a
-// workgroup per token).
+// whole token per workgroup, which reads its dy once (4096 x 8 x 7168 279 us
+// against 291, 1024 x 8 x 4096 38 against 46).  Measured, bf16, 4096 tokens x 8
+// x 7168: forward 90 us (5.9 TB/s), backward 188 us (5.3 TB/s); 256 tokens x 8
+// x 7168, held by the Infinity Cache, 6.8 us forward.
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
@@ -58,16 +61,17 @@ __device__ __forceinline__ void values8(const void* x, int64_t at, float* d) {
   }
 }
 
-// T * ceil(N / 2048) workgroups: a thread holds 8 columns of one token and has the
-// rows of eight choices in flight; a choice without a row reads nothing.
+// A wave takes 512 columns of one token, a thread 8 of them with the rows of eight
+// choices in flight; a choice without a row reads nothing.
 constexpr int kCombBatch = 8;
 template <bool BF16, bool NT>
 __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict__ rows, const int32_t* __restrict__ row_of,
                                                       const float* __restrict__ w, void* __restrict__ y, int k, int N,
-                                                      int64_t R, int parts) {
-  const int64_t t = blockIdx.x / parts;
-  const int c = (int)(blockIdx.x - t * parts) * 2048 + threadIdx.x * 8;
-  if (c >= N) return;
+                                                      int64_t R, int64_t T, int parts) {
+  const unsigned unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int64_t t = unit / (unsigned)parts;
+  const int c = (int)(unit - (unsigned)t * (unsigned)parts) * 512 + (threadIdx.x & 63) * 8;
+  if (t >= T || c >= N) return;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < k; j0 += kCombBatch) {
     uint4 raw[kCombBatch];
@@ -101,23 +105,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint16_t* __restrict
   }
 }
 
-// one workgroup per (token, choice)
+// one wave per (token, choice)
 template <bool BF16>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict__ dy, const uint16_t* __restrict__ rows,
                                                           const int32_t* __restrict__ row_of, const float* __restrict__ w,
                                                           uint16_t* __restrict__ drows, float* __restrict__ dw, int k, int N,
-                                                          int64_t R) {
-  __shared__ float part[4];
-  const int64_t i = blockIdx.x;
-  const int64_t t = i / k;
+                                                          int64_t R, int64_t T) {
+  const unsigned i = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int lane = threadIdx.x & 63;
+  const int64_t t = i / (unsigned)k;
+  if (t >= T) return;
   const int64_t r = row_of[i];
-  if (r < 0 || r >= R) {  // uniform over the workgroup
-    if (threadIdx.x == 0) dw[i] = 0.f;
+  if (r < 0 || r >= R) {  // uniform
+    if (lane == 0) dw[i] = 0.f;
     return;
   }
   const float wj = w[i];
   float dot = 0.f;
-  for (int c = threadIdx.x * 8; c < N; c += 256 * 8) {
+  for (int c = lane * 8; c < N; c += 512) {
     float v[8], d[8], o[8];
     bf16x8(load8<false>(rows + r * N + c), v);
     values8<BF16>(dy, t * N + c, d);
@@ -130,9 +135,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const void* __restrict
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) dot += __shfl_xor(dot, o);
-  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-  __syncthreads();
-  if (threadIdx.x == 0) dw[i] = (part[0] + part[1]) + (part[2] + part[3]);
+  if (lane == 0) dw[i] = dot;
 }
 
 // one workgroup per token, rows and drows streamed
@@ -189,27 +192,28 @@ __global__ void __launch_bounds__(256) combine_bwd_token_kernel(const void* __re
 
 }  // namespace
 
-// A launch has at most 2^24 - 1 workgroups of 256 threads; longer calls run in chunks of tokens.
+// A launch has at most 2^24 - 1 workgroups of 256 threads; longer calls run in chunks of tokens (units of at most 2^23 waves
+// or workgroups).
 constexpr int64_t kCombMaxGroups = (int64_t)1 << 23;
 
 // Rows that do not stay in the 256 MB Infinity Cache with what else is in use: from 96 MB on, from 48 MB on where drows is
 // written too. Streamed against not, forward: 33, 59, 88, 235 million values 13.2 / 12.7, 31 / 36, 39 / 46, 91 / 105 us;
-// with the backward pass: 15, 29, 34, 59, 235 million 22.9 / 20.7, 38 / 41, 42 / 52, 82 / 91, 280 / 317 us.
+// with the backward pass: 15, 29, 34, 59, 235 million 22.9 / 18.1, 35 / 37, 38 / 46, 81 / 93, 279 / 291 us.
 static bool streams(int64_t T, int64_t k, int64_t N, int64_t R, int64_t mb) {
   return (T * k < R ? T * k : R) * N * 2 >= mb << 20;
 }
 
 hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const float* w, void* y, bool bf16_y, int64_t T,
                           int64_t k, int64_t N, int64_t R, hipStream_t stream) {
-  const int parts = (int)((N + 2047) / 2048);
-  const int64_t chunk = kCombMaxGroups / parts;  // parts <= 2^19
+  const int parts = (int)((N + 511) / 512);
+  const int64_t chunk = kCombMaxGroups / parts;  // parts <= 2^21
   const bool nt = streams(T, k, N, R, 96);
   const auto kernel = bf16_y ? (nt ? combine_kernel<true, true> : combine_kernel<true, false>)
                              : (nt ? combine_kernel<false, true> : combine_kernel<false, false>);
   for (int64_t t = 0; t < T; t += chunk) {
-    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * parts);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream, rows, row_of + t * k, w + t * k,
-                       static_cast<void*>(static_cast<uint8_t*>(y) + t * N * (bf16_y ? 2 : 4)), (int)k, (int)N, R, parts);
+    const int64_t n = T - t < chunk ? T - t : chunk;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((n * parts + 3) / 4)), dim3(256), 0, stream, rows, row_of + t * k, w + t * k,
+                       static_cast<void*>(static_cast<uint8_t*>(y) + t * N * (bf16_y ? 2 : 4)), (int)k, (int)N, R, n, parts);
   }
   return hipGetLastError();
 }
@@ -218,15 +222,19 @@ hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows,
                               uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
                               hipStream_t stream) {
   const bool token = streams(T, k, N, R, 48);
-  const auto kernel = token ? (bf16_y ? combine_bwd_token_kernel<true> : combine_bwd_token_kernel<false>)
-                            : (bf16_y ? combine_bwd_kernel<true> : combine_bwd_kernel<false>);
-  const int64_t per = token ? 1 : k;  // workgroups of a token
-  const int64_t chunk = kCombMaxGroups / per;
+  const int64_t chunk = kCombMaxGroups / k;
   for (int64_t t = 0; t < T; t += chunk) {
-    const unsigned grid = (unsigned)((T - t < chunk ? T - t : chunk) * per);
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, stream,
-                       static_cast<const void*>(static_cast<const uint8_t*>(dy) + t * N * (bf16_y ? 2 : 4)), rows, row_of + t * k,
-                       w + t * k, drows, dw + t * k, (int)k, (int)N, R);
+    const int64_t n = T - t < chunk ? T - t : chunk;
+    const void* from = static_cast<const uint8_t*>(dy) + t * N * (bf16_y ? 2 : 4);
+    if (token) {
+      const auto kernel = bf16_y ? combine_bwd_token_kernel<true> : combine_bwd_token_kernel<false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)n), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k, drows, dw + t * k,
+                         (int)k, (int)N, R);
+    } else {
+      const auto kernel = bf16_y ? combine_bwd_kernel<true> : combine_bwd_kernel<false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((n * k + 3) / 4)), dim3(256), 0, stream, from, rows, row_of + t * k, w + t * k,
+                         drows, dw + t * k, (int)k, (int)N, R, n);
+    }
   }
   return hipGetLastError();
 }
