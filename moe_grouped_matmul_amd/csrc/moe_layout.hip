@@ -21,7 +21,7 @@
 // dependent steps, and the scattered 4-byte stores of row_token and m_indices
 // that one CU passes on (one line a cycle); blocks are many for those and few
 // for the columns of counts that every workgroup reads.  Measured: 256 tokens x
-// 8 in one launch 4.8 us; 16384 x 8 of 64 experts 10 us (2.5 the counts);
+// 8 in one launch 4.3 us; 16384 x 8 of 64 experts 9.4 us (2.4 the counts);
 // 131072 x 8 of 256 experts 28 us with 128 blocks, 29 with 256, 49 with 512;
 // a million x 8 222 us, 2.1 ms with blocks of 2048.
 #include "gemm_common.hpp"
