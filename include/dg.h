@@ -318,7 +318,7 @@ int dg_m_grouped_fp8_gemm_nt_masked_ue8m0(const uint8_t* A, const int32_t* sfa, 
  * gets 255 and zero elements.  Elements are x * 2^(127 - c), an exact scaling,
  * rounded to nearest, ties to the even mantissa, the sign of zero kept.
  * Bit-exact and deterministic.  T is ignored when row_token is null.
- * Limits: G <= 65535, R < 2^31, ceil(R / 16) * (K / 128) < 2^31; x, q 16-byte
+ * Limits: G <= 65535, R < 2^31, ceil(R / 4) * ceil(K / 512) < 2^24; x, q 16-byte
  * aligned, sf and row_token 4-byte aligned.
  *
  * dg_dequant_mxfp4: the values back, y [G,R,K] of `dtype` (exact in both, past
@@ -360,7 +360,7 @@ int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t* A, const int32_t* sfa, cons
  * Router: the k experts of each token, their weights, the experts' loads and
  * the balance loss.
  *   logits   [T,E] of `dtype` (DG_F32 or DG_BF16), E in [1, 1024], k in [1, min(E, 16)]
- *   valid    [T] bytes or NULL: tokens with 0 (padding) are not read
+ *   valid    [T] bytes or NULL: tokens with 0 (padding) take no part
  *   topk_idx [T,k] int32 (written): experts of the k largest logits, largest
  *            first, of equal ones the lower expert first; -inf and NaN are
  *            never chosen; -1 where nothing is left to choose

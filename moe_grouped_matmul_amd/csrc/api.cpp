@@ -119,6 +119,40 @@ int effective_cus(int device_cus) {
 
 bool print_configs() { return std::getenv("DG_PRINT_CONFIGS") != nullptr; }
 
+// With DG_CHECK_LAYOUT set: every aligned 128-row block holds rows of at most one
+// expert (indices outside [0, G) are padding and free).  Reads m_indices on
+// the host, so it synchronises the stream; a stream under capture is not
+// checked.
+int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G, void* stream) {
+  if (!std::getenv("DG_CHECK_LAYOUT")) return DG_OK;
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(st, &cap) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: cannot query the stream");
+  }
+  if (cap != hipStreamCaptureStatusNone) return DG_OK;
+  std::vector<int32_t> idx((size_t)M_total);
+  if (hipMemcpyAsync(idx.data(), m_indices, (size_t)M_total * 4, hipMemcpyDeviceToHost, st) != hipSuccess ||
+      hipStreamSynchronize(st) != hipSuccess) {
+    (void)hipGetLastError();
+    return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: reading m_indices failed");
+  }
+  for (int64_t b = 0; b < M_total; b += 128) {
+    int32_t e = -1;
+    for (int64_t r = b; r < std::min(M_total, b + 128); ++r) {
+      const int32_t x = idx[(size_t)r];
+      if (x < 0 || x >= G) continue;
+      if (e >= 0 && x != e)
+        return fail(DG_ERR_INVALID_ARG,
+                    "DG_CHECK_LAYOUT: rows %lld..%lld hold experts %d and %d (segments must be padded to 128 rows)",
+                    (long long)b, (long long)std::min(M_total, b + 128) - 1, e, x);
+      e = x;
+    }
+  }
+  return DG_OK;
+}
+
 }  // namespace dg
 
 namespace {
@@ -592,39 +626,6 @@ ContigPlan plan_contiguous(int64_t rows, int64_t N, int64_t K, int cus) {
   return cp;
 }
 
-// DG_CHECK_LAYOUT: every aligned 128-row block holds rows of at most one
-// expert (indices outside [0, G) are padding and free).  Reads m_indices on
-// the host, so it synchronises the stream; a stream under capture is not
-// checked.
-int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G, void* stream) {
-  const hipStream_t st = static_cast<hipStream_t>(stream);
-  hipStreamCaptureStatus cap = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(st, &cap) != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: cannot query the stream");
-  }
-  if (cap != hipStreamCaptureStatusNone) return DG_OK;
-  std::vector<int32_t> idx((size_t)M_total);
-  if (hipMemcpyAsync(idx.data(), m_indices, (size_t)M_total * 4, hipMemcpyDeviceToHost, st) != hipSuccess ||
-      hipStreamSynchronize(st) != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: reading m_indices failed");
-  }
-  for (int64_t b = 0; b < M_total; b += 128) {
-    int32_t e = -1;
-    for (int64_t r = b; r < std::min(M_total, b + 128); ++r) {
-      const int32_t x = idx[(size_t)r];
-      if (x < 0 || x >= G) continue;
-      if (e >= 0 && x != e)
-        return fail(DG_ERR_INVALID_ARG,
-                    "DG_CHECK_LAYOUT: rows %lld..%lld hold experts %d and %d (segments must be padded to 128 rows)",
-                    (long long)b, (long long)std::min(M_total, b + 128) - 1, e, x);
-      e = x;
-    }
-  }
-  return DG_OK;
-}
-
 // The M-grouped contiguous form with fp32 (ue = false) or packed UE8M0 scales.
 int run_contiguous(bool ue, const uint8_t* A, const void* sfa, const uint8_t* B, const void* sfb, uint16_t* D,
                    const int32_t* m_indices, int64_t M_total, int64_t N, int64_t K, int64_t G, void* stream) {
@@ -644,7 +645,7 @@ int run_contiguous(bool ue, const uint8_t* A, const void* sfa, const uint8_t* B,
   if (chunk == 0) return fail(DG_ERR_SHAPE, "rows do not fit 32-bit offsets");
   int cus = 0;
   if ((rc = check_device(&cus))) return rc;
-  if (std::getenv("DG_CHECK_LAYOUT") && (rc = check_contiguous_layout(m_indices, M_total, G, stream))) return rc;
+  if ((rc = dg::check_contiguous_layout(m_indices, M_total, G, stream))) return rc;
   const int ecus = effective_cus(cus);
   for (int64_t r0 = 0; r0 < M_total; r0 += chunk) {
     const int64_t rows = std::min(chunk, M_total - r0);

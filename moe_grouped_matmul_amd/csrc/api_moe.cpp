@@ -182,6 +182,7 @@ int run_mx(int form, const uint8_t* A, const int32_t* sfa, const uint8_t* B, con
   if (rows * (K / 128 + 8) * 4 >= kOffLim || N * (K / 128 + 8) * 4 >= kOffLim) return fail(DG_ERR_SHAPE, "scale arrays exceed 4 GiB");
   int cus = 0;
   if ((rc = check_device(&cus))) return rc;
+  if (form == kMxContiguous && (rc = check_contiguous_layout(index, rows, G, stream))) return rc;
   cus = effective_cus(cus);
   MxPlan pl;
   if (form == kMxDense) {

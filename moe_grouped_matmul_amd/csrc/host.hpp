@@ -27,6 +27,9 @@ int effective_cus(int device_cus);
 // DG_PRINT_CONFIGS is set
 bool print_configs();
 
+// Under DG_CHECK_LAYOUT: whether every aligned 128-row block of m_indices holds rows of at most one expert.
+int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G, void* stream);
+
 // Workspace bytes and plan texts of the operations of api_moe.cpp (0 / "" for others).
 size_t moe_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus);
 int moe_describe_plan(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus, char* buf, size_t n);

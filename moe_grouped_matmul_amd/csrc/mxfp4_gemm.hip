@@ -140,10 +140,12 @@ __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p
   }
   if constexpr (FORM == kMxContiguous) {
     static_assert(128 % BM == 0, "a contiguous tile lies in one aligned block");
+    const int64_t block = row0 & ~(int64_t)127;
     int x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      x[h] = 64 * h + lane < rows ? p.index[row0 + 64 * h + lane] : -1;
+      const int64_t r = block + 64 * h + lane;
+      x[h] = r < p.rows ? p.index[r] : -1;
       if (x[h] >= p.G) x[h] = -1;
     }
     int top = x[0] > x[1] ? x[0] : x[1];
@@ -156,6 +158,10 @@ __global__ void __launch_bounds__(64 * WM * WN) mxfp4_gemm_kernel(MxGemmParams p
     if (e < 0) return;  // only padding: nothing to write
     tag[0] = __ballot(x[0] == e);
     tag[1] = __ballot(x[1] == e);
+    if (BM == 64) {
+      tag[0] = tag[(row0 >> 6) & 1];
+      if (tag[0] == 0ull) return;  // this half is padding
+    }
   }
   const int n0 = nt * BN;
   const int cols = N - n0 < BN ? N - n0 : BN;

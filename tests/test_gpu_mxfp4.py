@@ -281,6 +281,37 @@ def test_contiguous_many_experts_and_long_layout(monkeypatch):
         assert np.all(got[idx < 0] == oracle.bf16_rne_bits(np.float32(7.0)))
 
 
+@pytest.mark.parametrize("tile", TILES)
+def test_contiguous_block_of_two_experts(monkeypatch, tile):
+    """Past the layout's rule: rows of the block's one expert are right, others unwritten; refused when the check is on."""
+    rng = np.random.default_rng(3)
+    M, N, K, G = 300, 272, 384, 3
+    idx = np.repeat([0, 1, 2], [70, 130, 100]).astype(np.int32)
+    a, sa = _operand(rng, (), M, K, True)
+    b, sb = _operand(rng, (G,), N, K, True)
+    monkeypatch.setenv("DG_FORCE_CONFIG", f"mxfp4={tile}")
+    D = torch.full((M, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    args = [*map(_t, (a, sa, b, sb)), D, _t(idx)]
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*args)
+    got = _bits(D)
+    for r0 in range(0, M, 128):
+        at = np.arange(r0, min(M, r0 + 128))
+        wrote = {int(e) for e in set(idx[at]) if not np.all(got[at[idx[at] == e]] == oracle.bf16_rne_bits(np.float32(7.0)))}
+        assert len(wrote) == 1, (tile, r0, wrote)
+        e = wrote.pop()
+        r = at[idx[at] == e]
+        _check(got[r], *mxfp4.gemm_mxfp4(a[r], sa[:, r], b[e], sb[e]), K, True, (tile, r0))
+        assert np.all(got[at[idx[at] != e]] == oracle.bf16_rne_bits(np.float32(7.0)))
+    monkeypatch.setenv("DG_CHECK_LAYOUT", "1")
+    with pytest.raises(dg.DGError, match="DG_CHECK_LAYOUT"):
+        dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*args)
+    D.fill_(7.0)
+    idx[:] = np.arange(M) // 128
+    args[-1] = _t(idx)
+    dg.dg_m_grouped_mxfp4_gemm_nt_contiguous(*args)
+    _check(_bits(D)[:128], *mxfp4.gemm_mxfp4(a[:128], sa[:, :128], b[0], sb[0]), K, True, tile)
+
+
 MASKED = [(3, 16, [16, 0, 5], 144, 256), (4, 70, [70, 1, 64, 33], 272, 896), (2, 300, [300, 129], 528, 384), (5, 1, [1, 0, 1, 1, 0], 16, 128),
           (2, 40, [-3, 99], 400, 1152), (2, 600, [530, 257], 272, 640)]
 
