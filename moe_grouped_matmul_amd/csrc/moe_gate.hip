@@ -38,6 +38,7 @@
 // bf16 in 4 workgroups 7.2 us, a chain of dependent steps.  Gradient: memory,
 // 17 us for 67 MB (3.9 TB/s).
 
+#include "dg_internal.hpp"
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
 
@@ -48,7 +49,6 @@ constexpr int kGateThreads = 1024;
 constexpr int kGateWaves = kGateThreads / 64;
 constexpr int kGateFan = 16;  // workgroups per group, groups
 constexpr int kGateMaxBlocks = kGateFan * kGateFan;
-constexpr int kGateCounterBytes = 128;  // root counter, then one per group
 constexpr int kBwdThreads = 256;
 
 // ---- keys.  -inf and NaN (read as -inf) sort below every number; 0 is an
@@ -285,8 +285,9 @@ __device__ __forceinline__ bool last_arrival(unsigned int* counter, unsigned int
   return *flag != 0;
 }
 
-// workspace: counters, [blocks][2 E + 1] partials of workgroups (sums, then
-// counts), [groups][2 E + 1] of groups
+// workspace: counters (the root's, then one per group) in the bytes that every
+// operator keeps its counters in, [blocks][2 E + 1] partials of workgroups
+// (sums, then counts), [groups][2 E + 1] of groups
 template <int LPT, int VPL, int KCAP, bool BF16>
 __global__ void __launch_bounds__(kGateThreads) gate_kernel(GateParams p) {
   typedef Keys<BF16> KT;
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kGateThreads) gate_kernel(GateParams p) {
     const int items = 2 * E + 1;
     const int groups = (blocks + kGateFan - 1) / kGateFan;
     unsigned int* root = static_cast<unsigned int*>(p.ws);
-    uint32_t* part = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.ws) + kGateCounterBytes);
+    uint32_t* part = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.ws) + kWsCounterBytes);
     uint32_t* gpart = part + (int64_t)blocks * items;
     const int g = (int)blockIdx.x / kGateFan;
     const int members = blocks - g * kGateFan < kGateFan ? blocks - g * kGateFan : kGateFan;
@@ -557,7 +558,7 @@ int gate_blocks(int64_t T, int64_t E) {
 
 size_t gate_workspace_bytes(int64_t T, int64_t E) {
   const int blocks = gate_blocks(T, E);
-  return kGateCounterBytes + (size_t)(blocks + kGateFan) * (size_t)(2 * E + 1) * 4;
+  return kWsCounterBytes + (size_t)(blocks + kGateFan) * (size_t)(2 * E + 1) * 4;
 }
 
 hipError_t launch_gate(const GateParams& p, bool bf16, hipStream_t stream) {

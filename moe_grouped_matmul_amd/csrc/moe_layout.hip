@@ -24,6 +24,9 @@
 // 8 in one launch 4.3 us; 16384 x 8 of 64 experts 9.4 us (2.4 the counts);
 // 131072 x 8 of 256 experts 28 us with 128 blocks, 29 with 256, 49 with 512;
 // a million x 8 222 us, 2.1 ms with blocks of 2048.
+#include <type_traits>
+
+#include "dg_internal.hpp"
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
 
@@ -52,7 +55,13 @@ int blocks_of(int64_t n) {
   return n > 0 ? (int)((n + per - 1) / per) : 1;
 }
 
-// ws[block][g]: choices of expert g in the block
+// Counts of a block in the workspace: a block of up to kLaySingle chunks a wave has at most 2048 choices, which 16 bits hold.
+template <int C>
+using Count = std::conditional_t<C != 0, uint16_t, int32_t>;
+static_assert(kLaySingle * kLayThreads < 65536, "16-bit counts");
+
+// counts[block][g], behind the workspace's counters: choices of expert g in the block
+template <int C>
 __global__ void __launch_bounds__(kLayThreads) layout_count_kernel(LayoutParams p, int chunks) {
   __shared__ int hist[kLayThreads];
   hist[threadIdx.x] = 0;
@@ -64,7 +73,8 @@ __global__ void __launch_bounds__(kLayThreads) layout_count_kernel(LayoutParams 
     if (g >= 0) atomicAdd(&hist[g], 1);
   }
   __syncthreads();
-  if ((int)threadIdx.x < p.G) static_cast<int*>(p.ws)[(int64_t)blockIdx.x * p.G + threadIdx.x] = hist[threadIdx.x];
+  Count<C>* counts = reinterpret_cast<Count<C>*>(static_cast<uint8_t*>(p.ws) + kWsCounterBytes);
+  if ((int)threadIdx.x < p.G) counts[(int64_t)blockIdx.x * p.G + threadIdx.x] = (Count<C>)hist[threadIdx.x];
 }
 
 // workgroups [0, blocks) place their block; all share the rows that hold
@@ -107,7 +117,7 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
     const int slices = kLayThreads / slots < kLaySlices ? kLayThreads / slots : kLaySlices;
     int before = 0, total = 0;
     if (g < G && slice < slices) {
-      const int* col = static_cast<const int*>(p.ws) + g;
+      const Count<C>* col = reinterpret_cast<const Count<C>*>(static_cast<const uint8_t*>(p.ws) + kWsCounterBytes) + g;
       for (int c0 = slice; c0 < blocks; c0 += kLayBatch * slices) {
         int v[kLayBatch];
 #pragma unroll
@@ -240,14 +250,22 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
 
 }  // namespace
 
-size_t layout_workspace_bytes(int64_t n, int64_t G) { return (size_t)blocks_of(n) * (size_t)G * 4; }
+// The first kWsCounterBytes are left as they are: other operators keep counters there that have to be zero between calls.
+// A single block uses nothing of it, and no size is below 4 bytes a count.
+size_t layout_workspace_bytes(int64_t n, int64_t G) {
+  const size_t counts = (size_t)blocks_of(n) * (size_t)G;
+  if (blocks_of(n) == 1) return 4 * counts;
+  const size_t need = kWsCounterBytes + (chunks_of(n) <= kLaySingle ? sizeof(Count<1>) : sizeof(Count<0>)) * counts;
+  return need > 4 * counts ? need : 4 * counts;
+}
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {
   const int blocks = blocks_of(p.n);
   const int chunks = chunks_of(p.n);
   int slots = 1;
   while (slots < p.G) slots *= 2;
-  if (blocks > 1) hipLaunchKernelGGL(layout_count_kernel, dim3(blocks), dim3(kLayThreads), 0, stream, p, chunks);
+  auto count = chunks <= kLaySingle ? layout_count_kernel<1> : layout_count_kernel<0>;
+  if (blocks > 1) hipLaunchKernelGGL(count, dim3(blocks), dim3(kLayThreads), 0, stream, p, chunks);
   // further workgroups where the rows outnumber the choices
   const int64_t f = (p.rows + 4 * kLayThreads - 1) / (4 * kLayThreads);
   const int fill = (int)(f < 256 ? f : 256);
