@@ -169,11 +169,13 @@ __device__ __forceinline__ float group_fmax(float v) {
 }
 
 // e^x for x <= 0 (NaN stays NaN): 2^n 2^f with n the integer nearest x log2 e
-// and f = x log2 e - n rounded once, so the error does not grow with the product
+// and f = x log2 e - n, with log2 e in two parts: f is off by two roundings of
+// a number of at most a half, 2^-24, wherever x lies, and e^x by 3 x 2^-24
 __device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kHigh = 1.44269502f, kLow = 1.92596303e-8f;  // log2 e
   x = __builtin_elementwise_maximum(x, -200.f);
-  const float n = __builtin_rintf(x * 1.44269502f);
-  const float f = __builtin_fmaf(x, 1.44269502f, -n);
+  const float n = __builtin_rintf(x * kHigh);
+  const float f = __builtin_fmaf(x, kLow, __builtin_fmaf(x, kHigh, -n));
   return __builtin_ldexpf(__builtin_amdgcn_exp2f(f), (int)n);
 }
 
