@@ -84,8 +84,13 @@ def build(verbose=False, out_path=None, extra_flags=()):
     with ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         args = ex.submit(_build_args) if out_path is None else None
         results = list(ex.map(lambda s: _compile(s, build_dir, list(extra_flags)), SOURCES))
-        if args is not None:
-            args.result()
+        try:
+            if args is not None:
+                args.result()
+        except Exception as e:  # no g++, Python.h or matching torch headers: the library does without
+            if os.path.exists(ARGS_PATH):  # an older one may not fit
+                os.remove(ARGS_PATH)
+            print(f"_args.so was not built, calls that check their tensors with it will raise: {e}", file=sys.stderr)
     report = []
     for (obj, log), src in zip(results, SOURCES):
         lines = [l for l in log.splitlines() if "remark" in l or "Function Name" in l or ":" in l]

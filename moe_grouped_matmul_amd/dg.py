@@ -80,19 +80,23 @@ class DGError(RuntimeError):
 
 
 _lib = None
+_args_error = None  # why _args.so did not load
 
 
 def _pointer(*args):
-    """_args.so's function in its place from the first load of the library on."""
+    """_args.so's function is in its place from the first load of the library on, where it loads."""
     load_library()
+    if _args_error is not None:
+        raise RuntimeError("_args.so, which checks the tensors of this call, was not found or does not load with this torch: "
+                           "build it (python -m moe_grouped_matmul_amd.build)") from _args_error
     return _pointer(*args)
-
 
 
 def load_library():
     """Load (once) and return the ctypes handle of the in-tree library; raises
-    if it is missing."""
-    global _lib, _pointer
+    if it is missing.  _args.so is bound to one version of torch and only the
+    calls that use it need it."""
+    global _lib, _pointer, _args_error
     if _lib is not None:
         return _lib
     p = LIB_PATH
@@ -100,10 +104,6 @@ def load_library():
         raise RuntimeError(
             f"{p} not found: build it first (python -m moe_grouped_matmul_amd.build); "
             "there is no fallback path")
-    try:
-        from moe_grouped_matmul_amd import _args
-    except ImportError as e:
-        raise RuntimeError("_args.so not found or not loadable: build it first (python -m moe_grouped_matmul_amd.build)") from e
     lib = ctypes.CDLL(p)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     lib.dg_fp8_gemm_nt.argtypes = [P, P, P, P, P, I64, I64, I64, P, SZ, P]
@@ -150,7 +150,13 @@ def load_library():
                  "dg_moe_combine", "dg_moe_combine_bwd", "dg_set_num_cus", "dg_get_num_cus",
                  "dg_get_m_alignment_for_contiguous_layout"):
         getattr(lib, name).restype = I
-    _lib, _pointer = lib, _args.pointer
+    try:
+        from moe_grouped_matmul_amd import _args
+    except ImportError as e:
+        _args_error = e
+    else:
+        _pointer = _args.pointer
+    _lib = lib
     return lib
 
 
