@@ -46,7 +46,7 @@ constexpr int kQCols = 512;
 // first row and column of this workgroup
 template <int ROWS>
 __device__ __forceinline__ int64_t q_place(int K, int* col) {
-  const int tiles = (K + kQCols - 1) / kQCols;
+  const int tiles = (K - 1) / kQCols + 1;  // K reaches the last multiple of 128 below 2^31
   const int64_t rb = (int64_t)blockIdx.x / tiles;
   *col = (int)((int64_t)blockIdx.x - rb * tiles) * kQCols;
   return rb * ROWS;
