@@ -29,7 +29,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <vector>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -121,8 +120,9 @@ bool print_configs() { return std::getenv("DG_PRINT_CONFIGS") != nullptr; }
 
 // With DG_CHECK_LAYOUT set: every aligned 128-row block holds rows of at most one
 // expert (indices outside [0, G) are padding and free).  Reads m_indices on
-// the host, so it synchronises the stream; a stream under capture is not
-// checked.
+// the host, a run of blocks at a time into a buffer of its own (no allocation
+// that could throw through the C entries), so it synchronises the stream; a
+// stream under capture is not checked.
 int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G, void* stream) {
   if (!std::getenv("DG_CHECK_LAYOUT")) return DG_OK;
   const hipStream_t st = static_cast<hipStream_t>(stream);
@@ -132,21 +132,26 @@ int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G
     return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: cannot query the stream");
   }
   if (cap != hipStreamCaptureStatusNone) return DG_OK;
-  std::vector<int32_t> idx((size_t)M_total);
-  if (hipMemcpyAsync(idx.data(), m_indices, (size_t)M_total * 4, hipMemcpyDeviceToHost, st) != hipSuccess ||
-      hipStreamSynchronize(st) != hipSuccess) {
-    (void)hipGetLastError();
-    return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: reading m_indices failed");
-  }
-  for (int64_t b = 0; b < M_total; b += 128) {
+  constexpr int64_t kRun = 128 * 128;
+  int32_t idx[kRun];
+  for (int64_t r0 = 0; r0 < M_total; r0 += kRun) {
+    const int64_t n = std::min(M_total - r0, kRun);
+    if (hipMemcpyAsync(idx, m_indices + r0, (size_t)n * 4, hipMemcpyDeviceToHost, st) != hipSuccess ||
+        hipStreamSynchronize(st) != hipSuccess) {
+      (void)hipGetLastError();
+      return fail(DG_ERR_DEVICE, "DG_CHECK_LAYOUT: reading m_indices failed");
+    }
     int32_t e = -1;
-    for (int64_t r = b; r < std::min(M_total, b + 128); ++r) {
-      const int32_t x = idx[(size_t)r];
+    for (int64_t i = 0; i < n; ++i) {
+      if (i % 128 == 0) e = -1;
+      const int32_t x = idx[i];
       if (x < 0 || x >= G) continue;
-      if (e >= 0 && x != e)
+      if (e >= 0 && x != e) {
+        const int64_t b = r0 + i / 128 * 128;
         return fail(DG_ERR_INVALID_ARG,
                     "DG_CHECK_LAYOUT: rows %lld..%lld hold experts %d and %d (segments must be padded to 128 rows)",
                     (long long)b, (long long)std::min(M_total, b + 128) - 1, e, x);
+      }
       e = x;
     }
   }
