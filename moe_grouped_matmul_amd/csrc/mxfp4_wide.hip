@@ -23,7 +23,8 @@
 // instructions take 2850 cycles a step at 1.7 GHz and the same time: the clock
 // follows the power, and that is what bounds the kernel.
 //
-// Tiles.  Contiguous: only aligned 128-row blocks hold rows of one expert, so
+// Tiles.  Contiguous: only aligned 128-row blocks hold rows of one expert (of
+// several in a block the largest is computed, as in every other tile shape), so
 // every workgroup reads m_indices at its start and pairs the blocks of each run
 // of one expert from the run's first block on; an odd one is a tile of 128
 // rows.  Dense: a last tile of up to 128 rows.  The large tiles are walked in
@@ -49,6 +50,7 @@ constexpr int kMwRsrcWord3 = 0x00020000;  // raw (untyped) buffer
 constexpr uint32_t kMwOOB = 0xFFFFFF00u;  // an offset past every buffer range used here
 
 typedef int mwi32x4 __attribute__((ext_vector_type(4)));
+typedef int mwi32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mw_rsrc(const void* p, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, kMwRsrcWord3);
@@ -82,6 +84,13 @@ struct Scales {
 };
 
 constexpr int kNone = 0xFFFF;
+
+// maximum with the lane that DPP control C exchanges with
+template <int C>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t u) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, C, 0xf, 0xf, true);
+  return o > u ? o : u;
+}
 
 template <int FORM>
 __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
@@ -118,33 +127,43 @@ __global__ void __launch_bounds__(256, 1) mxfp4_wide_kernel(MxGemmParams p) {
   int n_large, n_small;
   if constexpr (CONTIG) {
     const int nb = (int)((M + 127) >> 7);
-    // a block's expert is that of its first row, or (padding there) of any row: a thread per block, then a wave per
-    // block for those without one, eight blocks in flight
-    for (int b = tid; b < nb; b += 64 * NW) {
-      const int x = p.index[(int64_t)b * 128];
-      expert_of[b] = (uint16_t)(x >= 0 && x < p.G ? x : kNone);
-    }
-    __syncthreads();
-    for (int b0 = wave; b0 < nb; b0 += 8 * NW) {
-      int x[8][2];
+    // a block's expert is the largest index in [0, G) among its rows; half a wave reads a block, 16 blocks of a wave in flight
+    const int sub = lane & 31;
+    for (int b1 = 2 * wave; b1 < nb; b1 += 16 * NW) {
+      const int b0 = b1 + (lane >> 5);
+      mwi32x4u x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int b = b0 + i * NW;
-        const bool open = b < nb && __builtin_amdgcn_readfirstlane((int)expert_of[b < nb ? b : 0]) == kNone;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t r = (int64_t)b * 128 + 64 * h + lane;
-          x[i][h] = open && r < M ? p.index[r] : -1;
-        }
+        const int64_t r = (int64_t)(b0 + 2 * NW * i) * 128 + 4 * sub;
+        x[i] = mwi32x4u{-1, -1, -1, -1};
+        if (r + 3 < M) x[i] = *reinterpret_cast<const mwi32x4u*>(p.index + r);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i) {
+        const int b = b0 + 2 * NW * i;
+        uint32_t top = 0;  // the index + 1
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int v = x[i][h];
-          const unsigned long long m = __ballot(v >= 0 && v < p.G);
-          if (m != 0ull && lane == __builtin_ctzll(m)) expert_of[b0 + i * NW] = (uint16_t)v;
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t v = (uint32_t)x[i][k] < (uint32_t)p.G ? (uint32_t)x[i][k] + 1u : 0u;
+          top = v > top ? v : top;
         }
+        top = dpp_max<0xB1>(top);   // pairs of lanes
+        top = dpp_max<0x4E>(top);   // pairs of pairs
+        top = dpp_max<0x141>(top);  // the quads of eight
+        top = dpp_max<0x140>(top);  // the eights of sixteen
+        const auto both = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+        top = both[0] > both[1] ? both[0] : both[1];
+        if (sub == 0 && b < nb) expert_of[b] = (uint16_t)(top ? top - 1u : kNone);
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {  // the rows past the last four whole ones
+      int e = expert_of[nb - 1] == kNone ? -1 : (int)expert_of[nb - 1];
+      for (int64_t r = M & ~(int64_t)3; r < M; ++r) {
+        const int v = p.index[r];
+        if (v < p.G && v > e) e = v;
+      }
+      expert_of[nb - 1] = (uint16_t)(e < 0 ? kNone : e);
     }
     __syncthreads();
     if (wave == 0) {
