@@ -14,9 +14,10 @@
 // Infinity Cache cannot hold from one call to the next are streamed past it,
 // and y and drows with them (non-temporal), and then the backward pass takes a
 // whole token per workgroup, which reads its dy once (4096 x 8 x 7168 279 us
-// against 291, 1024 x 8 x 4096 38 against 46).  Measured, bf16, 4096 tokens x 8
-// x 7168: forward 90 us (5.9 TB/s), backward 188 us (5.3 TB/s); 256 tokens x 8
-// x 7168, held by the Infinity Cache, 6.8 us forward.
+// against 291, 1024 x 8 x 4096 38 against 46), unless a token's rows are too
+// short for that.  Measured, bf16, 4096 tokens x 8 x 7168: forward 90 us (5.9
+// TB/s), backward 188 us (5.3 TB/s); 256 tokens x 8 x 7168, held by the
+// Infinity Cache, 6.8 us forward.
 
 #include "gemm_common.hpp"
 #include "moe_internal.hpp"
@@ -218,10 +219,19 @@ hipError_t launch_combine(const uint16_t* rows, const int32_t* row_of, const flo
   return hipGetLastError();
 }
 
+// A workgroup per token pays where a token's choices have values for all its threads.  84 MB of rows, a wave per choice
+// against a workgroup per token, us (six sets of buffers in rotation, so nothing is cached from one call to the next):
+//   k N = 2048: k = 1 54 / 66, k = 2 44 / 62, k = 4 42 / 63;  2560, k = 8: 49 / 57
+//   k N = 4096: k = 1 55 / 53, k = 2 46 / 42, k = 4 40 / 40, k = 8 41 / 41
+//   k N = 8192: k = 2 48 / 41, k = 4 43 / 38, k = 8 39 / 38
+// Narrower rows: k = 8, N = 64: 165 / 241; k = 2, N = 64: 169 / 846, N = 16: 628 / 3359.  Rows that stayed in the cache (one
+// set of buffers) are faster with a wave per choice, at k = 8, N = 2048: 84 MB 30 / 36, 130 MB 50 / 56.
+constexpr int64_t kCombTokenValues = 4096;
+
 hipError_t launch_combine_bwd(const void* dy, bool bf16_y, const uint16_t* rows, const int32_t* row_of, const float* w,
                               uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R,
                               hipStream_t stream) {
-  const bool token = streams(T, k, N, R, 48);
+  const bool token = streams(T, k, N, R, 48) && k * N >= kCombTokenValues;
   const int64_t chunk = kCombMaxGroups / k;
   for (int64_t t = 0; t < T; t += chunk) {
     const int64_t n = T - t < chunk ? T - t : chunk;
