@@ -375,8 +375,8 @@ int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t* A, const int32_t* sfa, cons
  * A masked token, or one whose logits are all -inf, has no expert and enters
  * no sum.  A row with a NaN or +inf has NaN probabilities: its weights, prob_sum
  * and the loss are NaN, its experts are still distinct and in range.
- * workspace: required, dg_get_workspace_size(DG_OP_MOE_GATE, T, E, k, 1) bytes,
- * zero-filled before its first use and left reusable, by the other operators
+ * workspace: required, dg_get_workspace_size(DG_OP_MOE_GATE, T, E, k, 1) bytes
+ * (which also serve fewer tokens of as many experts), zero-filled before its first use and left reusable, by the other operators
  * too: the first 4 KiB of any operator's workspace are counters, zero between
  * calls.  Calls that share one must be ordered on one stream.  Deterministic.
  *
@@ -408,8 +408,8 @@ int dg_moe_gate_bwd(const void* logits, int dtype, const int32_t* topk_idx, cons
  *     max_m get no row.
  *     masked_m [G] int32 (written), row_token [G,max_m], row_of [T,k] as above.
  * k in [1, 16], G in [1, 1024], T k + 128 G < 2^31.  workspace: required,
- * dg_get_workspace_size(DG_OP_MOE_LAYOUT, T, 0, k, G) bytes; it need not be
- * zero, and its first 4 KiB are left as they are, so it may be one that other
+ * dg_get_workspace_size(DG_OP_MOE_LAYOUT, T, 0, k, G) bytes, which also serve
+ * fewer tokens, choices and groups; it need not be zero, and its first 4 KiB are left as they are, so it may be one that other
  * operators use, in calls ordered on one stream.  Deterministic.
  */
 int dg_moe_layout_contiguous(const int32_t* topk_idx, int32_t* counts, int32_t* m_indices, int32_t* row_token,

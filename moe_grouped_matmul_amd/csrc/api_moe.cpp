@@ -283,7 +283,7 @@ int run_layout(const int32_t* topk_idx, int32_t* counts, int32_t* m_indices, int
     return fail(DG_ERR_INVALID_ARG, "null pointer");
   if (!aligned(topk_idx, 4) || !aligned(counts, 4) || !aligned(row_token, 4) || !aligned(row_of, 4) || !aligned(m_indices, 4))
     return fail(DG_ERR_ALIGN, "index arrays must be 4-byte aligned");
-  const size_t need = layout_workspace_bytes(T * k, G);
+  const size_t need = layout_workspace_needed(T * k, G);
   if (!ws || !aligned(ws, 16) || ws_bytes < need)
     return fail(DG_ERR_WORKSPACE, "a 16-byte aligned workspace of at least %zu bytes is needed", need);
   int cus = 0;

@@ -104,7 +104,8 @@ struct LayoutParams {
   int64_t max_m;  // 0: contiguous
   int64_t rows;
 };
-size_t layout_workspace_bytes(int64_t n, int64_t G);
+size_t layout_workspace_needed(int64_t n, int64_t G);
+size_t layout_workspace_bytes(int64_t n, int64_t G);  // asked for: enough for up to n choices
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream);
 
 // ---- combine (moe_combine.hip)

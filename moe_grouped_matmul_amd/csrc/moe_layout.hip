@@ -251,12 +251,22 @@ __global__ void __launch_bounds__(kLayThreads) layout_place_kernel(LayoutParams 
 }  // namespace
 
 // The first kWsCounterBytes are left as they are: other operators keep counters there that have to be zero between calls.
-// A single block uses nothing of it, and no size is below 4 bytes a count.
-size_t layout_workspace_bytes(int64_t n, int64_t G) {
+// A single block uses nothing of it.
+static size_t workspace_of(size_t counts, int chunks) {
+  return kWsCounterBytes + (chunks <= kLaySingle ? sizeof(Count<1>) : sizeof(Count<0>)) * counts;
+}
+size_t layout_workspace_needed(int64_t n, int64_t G) {
   const size_t counts = (size_t)blocks_of(n) * (size_t)G;
-  if (blocks_of(n) == 1) return 4 * counts;
-  const size_t need = kWsCounterBytes + (chunks_of(n) <= kLaySingle ? sizeof(Count<1>) : sizeof(Count<0>)) * counts;
-  return need > 4 * counts ? need : 4 * counts;
+  return blocks_of(n) == 1 ? 4 * counts : workspace_of(counts, chunks_of(n));
+}
+// What is asked for grows with n, so that a buffer for the most choices serves fewer (131073 choices make 65 blocks, 131072
+// make 128), and is no less than 4 bytes a count.
+size_t layout_workspace_bytes(int64_t n, int64_t G) {
+  if (blocks_of(n) == 1) return layout_workspace_needed(n, G);
+  const int64_t most = (n + kLayThreads - 1) / kLayThreads;
+  const size_t counts = (size_t)(most < kLayMaxBlocks ? most : kLayMaxBlocks) * (size_t)G;
+  const size_t bytes = workspace_of(counts, chunks_of(n));
+  return bytes > 4 * counts ? bytes : 4 * counts;
 }
 
 hipError_t launch_layout(const LayoutParams& p, hipStream_t stream) {

@@ -113,3 +113,14 @@ def test_gate_and_layout_leave_counters_alone_at_their_own_size():
         assert all(torch.equal(x, y) for x, y in zip(first, again)), n
         assert bool((guard[size:] == 0xA5).all()), n
         assert not bool(ws[: min(size, 4096)].any()), n
+
+
+def test_row_order_in_a_buffer_for_more_choices():
+    G = 64
+    size = dg.dg_get_workspace_size(dg.DG_OP_MOE_LAYOUT, 400000, 0, 1, G)
+    guard = torch.full((size + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    for T, k in ((400000, 1), (16384, 8), (131073, 1), (2049, 1), (32768, 8), (300, 2)):
+        call, own = _layout(T, k, G)
+        alone = call(torch.zeros(own, dtype=torch.uint8, device=DEV))
+        assert all(torch.equal(x, y) for x, y in zip(call(guard[:size]), alone)), (T, k)
+        assert bool((guard[size:] == 0xA5).all()) and bool((guard[:4096] == 0xA5).all())
