@@ -318,7 +318,7 @@ int dg_m_grouped_fp8_gemm_nt_masked_ue8m0(const uint8_t* A, const int32_t* sfa, 
  * gets 255 and zero elements.  Elements are x * 2^(127 - c), an exact scaling,
  * rounded to nearest, ties to the even mantissa, the sign of zero kept.
  * Bit-exact and deterministic.  T is ignored when row_token is null.
- * Limits: G <= 65535, R < 2^31, ceil(R / 4) * ceil(K / 512) < 2^24; x, q 16-byte
+ * Limits: G <= 65535, R and K < 2^31, ceil(R / 4) * ceil(K / 512) < 2^24; x, q 16-byte
  * aligned, sf and row_token 4-byte aligned.
  *
  * dg_dequant_mxfp4: the values back, y [G,R,K] of `dtype` (exact in both, past
@@ -338,9 +338,10 @@ int dg_dequant_mxfp4(const uint8_t* q, const int32_t* sf, void* y, int dtype, in
  *   [G][K/128][max_m]): both operands scaled per row and 32 elements
  * The matrix cores apply the scales; sums are fp32, rounded once to bf16.
  * A row or column with a NaN code (255) gives NaN.  K is a positive multiple
- * of 128 up to 2^24, N of 16, and the scale words of one operand (masked: of one
- * expert) take less than 4 GiB; larger codes and outputs are addressed in 64
- * bits.  Deterministic.
+ * of 128 up to 2^24, N of 16, and (K / 128 + 8) words of 4 bytes for each row of
+ * one operand (masked: of one expert) take less than 4 GiB; codes and outputs
+ * are addressed in 64 bits.  Plans of about 2^23 tiles (of 64 x 64 or 128 x 256)
+ * and more are refused.  Sums that fit 24 bits are exact.  Deterministic.
  * workspace (dense only): as for dg_fp8_gemm_nt: optional, zero-filled before
  * its first use and left reusable, full size
  * dg_get_workspace_size(DG_OP_MXFP4_GEMM_NT, M, N, K, 1).
@@ -366,7 +367,7 @@ int dg_m_grouped_mxfp4_gemm_nt_masked(const uint8_t* A, const int32_t* sfa, cons
  *            never chosen; -1 where nothing is left to choose
  *   topk_w   [T,k] fp32 (written): with p = softmax(logits of the row),
  *            w_scale * p_j / (sum of the chosen p) if renorm, else w_scale * p_j;
- *            0 where topk_idx is -1
+ *            0 where topk_idx is -1 (NaN in a row whose probabilities are NaN)
  *   counts   [E+1] int32 (written): choices c_e of each expert, then the number n
  *            of tokens with a choice
  *   prob_sum [E] fp32 (written): P_e = sum of p_te over the tokens
@@ -398,7 +399,8 @@ int dg_moe_gate_bwd(const void* logits, int dtype, const int32_t* topk_idx, cons
  * entries (another GPU's experts, -1) are skipped.  A group's choices take its
  * rows in (token, choice) order.
  *   contiguous: group g's rows start at a multiple of 128, groups in order.
- *     counts    [G] int32 (written)
+ *     counts    [G] int32 (written): all of the group's choices, also those
+ *               that got no row
  *     m_indices [M_total] int32 (written): group of each row, -1 on padding
  *     row_token [M_total] int32 (written): token of each row, -1 on padding
  *     row_of    [T,k] int32 (written): row of each choice, -1 if it has none
@@ -406,7 +408,8 @@ int dg_moe_gate_bwd(const void* logits, int dtype, const int32_t* topk_idx, cons
  *     M_total get no row.
  *   masked: group g's rows are [g max_m, g max_m + masked_m[g]); choices past
  *     max_m get no row.
- *     masked_m [G] int32 (written), row_token [G,max_m], row_of [T,k] as above.
+ *     masked_m [G] int32 (written): the rows taken, at most max_m;
+ *     row_token [G,max_m], row_of [T,k] as above.
  * k in [1, 16], G in [1, 1024], T k + 128 G < 2^31.  workspace: required,
  * dg_get_workspace_size(DG_OP_MOE_LAYOUT, T, 0, k, G) bytes, which also serve
  * fewer tokens, choices and groups; it need not be zero, and its first 4 KiB are left as they are, so it may be one that other

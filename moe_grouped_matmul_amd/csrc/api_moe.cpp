@@ -125,11 +125,12 @@ MxPlan plan_mx_dense(int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) 
 }
 
 // Contiguous: the tile shape of least estimated time. Every other expert's number of 128-row blocks is taken to be odd,
-// the persistent kernel reads m_indices first (4 us), and the weights of all experts and the output pass at 2.8, 3.5 or
-// 4.3 TB/s at most (experts of few rows, whose weights no other row tile repeats: 64 experts, 256 rows, 4096 x 7168 in
-// 313, 217 and 214 us). Over 18 layouts of 8-8192 rows and 2-64 experts the choice was the fastest of the three or
-// within 10% of it: 2000 rows of 16 experts, 512 x 7168, 16, 31 and 25 us; 1000 of 4, 4096 x 2048, 20, 15 and 20; 8192
-// of 16, 4096 x 1024, 96, 59 and 50.
+// the persistent kernel is charged 4 us for reading m_indices first, and the weights of all experts and the output pass
+// at 2.8, 3.5 or 4.3 TB/s at most (experts of few rows, whose weights no other row tile repeats: 64 experts, 256 rows,
+// 4096 x 7168 in 314, 220 and 214 us). Of 18 layouts of 8-8192 rows and 2-64 experts the choice was the fastest of the
+// three or within 3% of it on 16 (2000 rows of 16 experts, 512 x 7168, 16, 31 and 24 us; 1000 of 4, 4096 x 2048, 20, 16
+// and 19; 8192 of 16, 4096 x 1024, 96, 58 and 47), and slower on two: 1500 of 8, 4096 x 1024, 25, 22 (chosen) and 18;
+// 8192 of 64, 512 x 2048, 26, 17 and 23 (chosen).
 int mx_contiguous_tile(int64_t rows, int64_t N, int64_t K, int64_t G, int cus) {
   const int64_t blocks = ceil_div(rows, 128);
   const int64_t odd = std::min(blocks, (G + 1) / 2);

@@ -30,13 +30,16 @@
 // last workgroup to arrive (agent-scope counters, coherent partials) and in a
 // fixed order, so results do not depend on scheduling.
 //
-// Bounds.  Forward: the vector units (sorting and k rounds over 16 values per
-// lane), then the tail over workgroups: 32768 x 256 fp32, k = 8, 22 us, of
-// which the logits' bytes at the copy rate are 7 and the tail about 6 (131 us
+// Bounds.  Forward, 32768 x 256 fp32, k = 8: 23 us, of which the logits' bytes
+// at the copy rate are 7 and the tail over workgroups about 6.  The vector units
+// (sorting and k rounds over 16 values per lane) are busy 0.67 of the cycles; a
+// CU holds one workgroup of 16 waves in phase, so a pass's loads and the tail
+// have no other work under them, and a wave waits 0.60 of its cycles (131 us
 // with a wave per token and no sorted keys, 26 with 16 lanes; 22-bit keys in 32
 // bits with the expert in the low ones and a second comparison 29).  64 x 256
-// bf16 in 4 workgroups 7.2 us, a chain of dependent steps.  Gradient: memory,
-// 17 us for 67 MB (3.9 TB/s).
+// bf16: 7.3 us, all 64 tokens in one workgroup, four waves a SIMD one after
+// another through a chain of dependent steps.  Gradient: memory, 17 us for 67
+// MB (3.9 TB/s).
 
 #include "dg_internal.hpp"
 #include "gemm_common.hpp"

@@ -8,10 +8,11 @@
 // v_mfma_scale_f32_16x16x128_f8f6f4 takes 32 elements (16 bytes) of one row
 // from each lane and that block's exponent byte beside them, so a lane's
 // operand is one aligned 16-byte chunk and its scale one byte, and products
-// are accumulated in fp32 over the whole K range (a product of two e2m1
-// values has at most 6 significant bits, so a block's 32 products add without
-// loss; rounding happens where blocks of different scale meet, in the fp32
-// accumulator).
+// are accumulated in fp32 over the whole K range.  A product of two e2m1 values
+// has at most 6 significant bits, so a block's 32 products add without loss.
+// Where blocks of different scale meet, and with the accumulator, 24 bits are
+// kept: a 1 beside 2^23 survives, inside one instruction and across two, a 1
+// beside 2^24 does not, so sums that fit 24 bits are exact in any order.
 //
 // Organisation: a workgroup computes one BM x BN tile.  K advances in steps
 // of 256 elements, 128 bytes per operand row, through a ring of P LDS slots

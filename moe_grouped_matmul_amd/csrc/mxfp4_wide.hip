@@ -36,7 +36,10 @@
 // (rows 128 on are the same rows further along K) and it meets a barrier every
 // other one.  Measured, 8 experts x 16384 rows, 4096 x 7168: 276 us without
 // quarters, 270 with quarters of one step a slot, 267 us (3.6 PFLOP/s); 8192
-// rows 163, 156, 148; one expert of 4352 rows 78, 74.5, 67.
+// rows 163, 156, 148; one expert of 4352 rows 78, 74.5, 67.  Reading all of
+// m_indices with half a wave a block against a thread's first row of each and a
+// wave for the rest: 16384 rows 251 -> 248 us in even segments, 262144 rows of
+// 8 experts, 512 x 256, 214 -> 141.
 #include <utility>
 
 #include "dg_internal.hpp"
@@ -47,7 +50,6 @@ namespace dg {
 namespace {
 
 constexpr int kMwRsrcWord3 = 0x00020000;  // raw (untyped) buffer
-constexpr uint32_t kMwOOB = 0xFFFFFF00u;  // an offset past every buffer range used here
 
 typedef int mwi32x4 __attribute__((ext_vector_type(4)));
 typedef int mwi32x4u __attribute__((ext_vector_type(4), aligned(4)));
