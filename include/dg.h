@@ -79,8 +79,18 @@ enum {
   DG_OP_K_GROUPED = 5, /* dg_k_grouped_fp8_gemm_nt_contiguous (plan description only) */
   DG_OP_MXFP4_GEMM_NT = 6,
   DG_OP_MOE_GATE = 7,  /* workspace only: rows = T, N = E */
-  DG_OP_MOE_LAYOUT = 8 /* workspace only: rows = T, K = k */
+  DG_OP_MOE_LAYOUT = 8, /* workspace only: rows = T, K = k */
+  DG_OP_MOE_EXPERTS = 9,    /* workspace only: rows = T k, N = H, K = I */
+  DG_OP_RMS_NORM_BWD = 10,  /* workspace only: rows = M, K */
+  DG_OP_EPILOGUE_BWD = 11   /* workspace only: rows = M, N */
 };
+
+/* Activations of dg_fp8_gemm_nt_epilogue: z, max(z, 0), z / (1 + e^-z), z Phi(z)
+ * (the normal distribution's), and z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum { DG_ACT_NONE = 0, DG_ACT_RELU = 1, DG_ACT_SILU = 2, DG_ACT_GELU = 3, DG_ACT_GELU_TANH = 4 };
+
+/* Scales of a quantised output: one fp32 or one UE8M0 code (packed) per 1x128. */
+enum { DG_SCALE_F32 = 0, DG_SCALE_UE8M0 = 1 };
 
 /* Element types of the operators that take more than one. */
 enum { DG_F32 = 0, DG_BF16 = 1 };
@@ -184,6 +194,69 @@ int dg_m_grouped_fp8_gemm_nt_masked(const uint8_t* A, const float* sfa, const ui
 int dg_fp8_gemm_nt_acc(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb,
                        const float* C, float* D, int64_t M, int64_t N, int64_t K, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/*
+ * Dense GEMM with bias, activation and residual: z = A . B^T + bias,
+ * D = act(z) + residual, all in fp32 and rounded once to bf16.
+ *   A, sfa, B, sfb, workspace as for dg_fp8_gemm_nt (same size query)
+ *   bias     [N] fp32 or NULL      act  one of DG_ACT_*
+ *   residual [M,N] bf16 or NULL; may equal D (in place)
+ *   pre      [M,N] bf16 or NULL (written): z, what dg_epilogue_bwd reads
+ * bias, residual and pre are 16-byte aligned; apart from residual = D no two
+ * arrays overlap.
+ */
+int dg_fp8_gemm_nt_epilogue(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, const float* bias,
+                            int act, const uint16_t* residual, uint16_t* pre, uint16_t* D, int64_t M, int64_t N,
+                            int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of that epilogue: dz = dy act'(pre) (the residual's gradient is dy,
+ * the operands' are products of dz).
+ *   dy [M,N] bf16        pre [M,N] bf16, unused (may be NULL) for DG_ACT_NONE
+ *   dz [M,N] bf16 or NULL (written); may equal dy or pre
+ *   q  [M,N] e4m3 and sf [N/128][M] fp32, both or neither (written): the 1x128
+ *      quantisation of dz before its rounding (rules of dg_quant_1x128), the
+ *      left operand of the product that gives A's gradient; N a multiple of 128
+ *   dbias [N] fp32 or NULL (written): the sum of dz over the rows (zeros for M = 0)
+ * N is a multiple of 16.  workspace: required with dbias,
+ * dg_get_workspace_size(DG_OP_EPILOGUE_BWD, M, N, 0, 1) bytes; it need not be
+ * zero, and its first 4 KiB are left as they are.  Deterministic.
+ */
+int dg_epilogue_bwd(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* dz, uint8_t* q, float* sf, float* dbias,
+                    int64_t M, int64_t N, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it and the
+ * next product's quantisation after it:
+ *   h = x + residual, rounded to `dtype` (x itself without a residual)
+ *   r = 1 / sqrt(mean(h^2) + eps),  v = (h r) weight
+ *   x, residual [M,K] of `dtype` (DG_F32 or DG_BF16), residual may be NULL
+ *   weight [K] of `weight_dtype`
+ *   h    [M,K] of `dtype` (written), may be NULL without a residual; may equal x or residual
+ *   y    [M,K] of `dtype` or NULL (written): v rounded; may equal x or residual, not h
+ *   q    [M,K] e4m3 or NULL (written) with sf: the 1x128 quantisation of v in
+ *        fp32, scales and rules of dg_quant_1x128 (DG_SCALE_F32: sf [K/128][M]
+ *        fp32) or dg_quant_1x128_ue8m0 (DG_SCALE_UE8M0: sf [ceil(K/512)][M] int32)
+ *   rstd [M] fp32 or NULL (written): r
+ * At least one of y and q is given.  K is a multiple of 8 (with q: of 128) up to
+ * 16384, eps positive; sums are fp32, so a row whose sum of squares passes
+ * 3.4e38 has r = 0.  Non-finite rows give NaN in y and unspecified codes.
+ * Deterministic.
+ *
+ * dg_rms_norm_bwd: with n = h r,
+ *   dx [M,K] of `dtype` (written) = dh + r (weight dy - n mean(weight dy n))
+ *   dw [K] fp32 (written) = sum over the rows of dy n (zeros for M = 0)
+ * dy [M,K] and dh [M,K] (the gradient that reaches h by other ways, or NULL) of
+ * `dtype`; h and rstd are dg_rms_norm's (x without a residual).  dx is the
+ * gradient of x and of the residual; it may equal dy, h or dh.  workspace:
+ * required, dg_get_workspace_size(DG_OP_RMS_NORM_BWD, M, 0, K, 1) bytes; it need
+ * not be zero, and its first 4 KiB are left as they are.  Deterministic.
+ */
+int dg_rms_norm(const void* x, const void* residual, const void* weight, int dtype, int weight_dtype, void* h, void* y,
+                uint8_t* q, void* sf, int scale_kind, float* rstd, int64_t M, int64_t K, float eps, void* stream);
+int dg_rms_norm_bwd(const void* dy, const void* h, const void* weight, const float* rstd, int dtype, int weight_dtype,
+                    const void* dh, void* dx, float* dw, int64_t M, int64_t K, void* workspace, size_t workspace_bytes,
+                    void* stream);
 
 /*
  * K-grouped contiguous GEMM (MoE weight gradient), D[g] = C[g] + A_g . B_g^T

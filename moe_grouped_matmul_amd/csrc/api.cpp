@@ -483,7 +483,15 @@ void plan_skinny(DensePlan& pl, int64_t M, int64_t N, int64_t K, int cus, size_t
 // 256 x 128 tiles with a K-split tail.  kBf16: 256 x 256 tiles where they fill whole rounds, else 256 x 128
 // tiles.  DG_FORCE_CONFIG=kernel=... overrides the wide / 256 x 128 choice
 // for M > 128 (and for the BF16 form at any M >= 1).
-enum DenseKind { kFp8 = 0, kAcc = 1, kUe8m0 = 2, kBf16 = 3 };
+enum DenseKind { kFp8 = 0, kAcc = 1, kUe8m0 = 2, kBf16 = 3, kEpi = 4 };
+
+// Operands of the epilogue form (kEpi, planned as kFp8).
+struct Epilogue {
+  const float* bias;
+  int act;
+  const uint16_t* residual;
+  uint16_t* pre;
+};
 
 DensePlan plan_dense(DenseKind kind, int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) {
   DensePlan pl;
@@ -522,13 +530,14 @@ DensePlan plan_dense(DenseKind kind, int64_t M, int64_t N, int64_t K, int cus, s
 }
 
 const char* kind_name(DenseKind k) {
-  return k == kFp8 ? "gemm_nt" : k == kAcc ? "gemm_nt_acc" : k == kUe8m0 ? "gemm_nt_ue8m0" : "bf16_gemm_nt";
+  return k == kFp8 ? "gemm_nt" : k == kAcc ? "gemm_nt_acc" : k == kUe8m0 ? "gemm_nt_ue8m0" : k == kEpi ? "gemm_nt_epilogue" : "bf16_gemm_nt";
 }
 
 // Validation shared by the dense forms past their pointer checks, then one
 // launch per row chunk.
 int run_dense(DenseKind kind, const uint8_t* A, const void* sfa, const uint8_t* B, const void* sfb, const float* C,
-              void* D, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+              void* D, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream,
+              const Epilogue* epi = nullptr) {
   const int64_t kbytes = kind == kBf16 ? 2 * K : K;
   const int64_t out_bytes = (kind == kAcc ? 4 : 2) * N;
   int rc = check_weights_and_scales(N, kbytes, kind == kBf16 ? 0 : M, kind == kUe8m0 ? ceil_div(K / 128, 4) : K / 128);
@@ -553,6 +562,11 @@ int run_dense(DenseKind kind, const uint8_t* A, const void* sfa, const uint8_t* 
       p.Dacc = static_cast<float*>(D) + r0 * N;
     } else {
       p.D = static_cast<uint16_t*>(D) + r0 * N;
+    }
+    if (epi) {
+      p.bias = epi->bias;
+      p.residual = epi->residual ? epi->residual + r0 * N : nullptr;
+      p.pre = epi->pre ? epi->pre + r0 * N : nullptr;
     }
     p.ws = static_cast<float*>(workspace);
     p.index = nullptr;
@@ -583,10 +597,10 @@ int run_dense(DenseKind kind, const uint8_t* A, const void* sfa, const uint8_t* 
                      pl.wide ? "wide" : "persistent", pl.grid, pl.m_tiles * pl.n_tiles, pl.dp_tiles, pl.sk_tiles,
                      pl.sk_pieces, pl.sk_kb);
     }
-    const int mode = kind == kFp8 ? dg::kDense : kind == kAcc ? dg::kDenseAcc : kind == kUe8m0 ? dg::kDenseUe8m0
+    const int mode = epi ? dg::kDenseEpi + epi->act : kind == kFp8 ? dg::kDense : kind == kAcc ? dg::kDenseAcc : kind == kUe8m0 ? dg::kDenseUe8m0
                                                                                                  : dg::kDenseBf16;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const hipError_t e = pl.skinny ? dg::launch_gemm_skinny(pl.cfg, pl.wn, pl.depth, kind == kUe8m0, p, st)
+    const hipError_t e = pl.skinny ? dg::launch_gemm_skinny(pl.cfg, pl.wn, pl.depth, kind == kUe8m0, epi ? epi->act : -1, p, st)
                          : pl.wide ? dg::launch_gemm_wide(mode, pl.grid, p, st)
                                    : dg::launch_gemm_persistent(mode, pl.grid, p, st);
     if (e != hipSuccess) return fail(DG_ERR_LAUNCH, "launch failed: %s", hipGetErrorString(e));
@@ -797,6 +811,23 @@ int dg_fp8_gemm_nt_acc(const uint8_t* A, const float* sfa, const uint8_t* B, con
   return run_dense(kAcc, A, sfa, B, sfb, C, D, M, N, K, workspace, workspace_bytes, stream);
 }
 
+int dg_fp8_gemm_nt_epilogue(const uint8_t* A, const float* sfa, const uint8_t* B, const float* sfb, const float* bias,
+                            int act, const uint16_t* residual, uint16_t* pre, uint16_t* D, int64_t M, int64_t N,
+                            int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_nk(N, K);
+  if (rc) return rc;
+  if ((rc = check_rows(M, "M"))) return rc;
+  if ((rc = check_activation(act))) return rc;
+  if (M == 0) return ok();
+  if ((rc = check_operands(A, sfa, B, sfb, D))) return rc;
+  if (pre == D) return fail(DG_ERR_INVALID_ARG, "pre and D must be different arrays");
+  if (!aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16))
+    return fail(DG_ERR_ALIGN, "bias, residual and pre must be 16-byte aligned");
+  if ((rc = check_workspace(workspace, workspace_bytes))) return rc;
+  const Epilogue e{bias, act, residual, pre};
+  return run_dense(kEpi, A, sfa, B, sfb, nullptr, D, M, N, K, workspace, workspace_bytes, stream, &e);
+}
+
 int dg_fp8_gemm_nt_ue8m0(const uint8_t* A, const int32_t* sfa, const uint8_t* B, const int32_t* sfb, uint16_t* D,
                          int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
   int rc = check_nk(N, K);
@@ -996,6 +1027,7 @@ int dg_quant_128x128_ue8m0(const float* x, uint8_t* q, int32_t* sfb, int64_t G, 
 }
 
 size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t G) {
+  if (op >= DG_OP_MOE_EXPERTS) return block_workspace_size(op, rows, N, K, effective_cus(query_cus()));
   if (op >= DG_OP_MXFP4_GEMM_NT) return moe_workspace_size(op, rows, N, K, G, effective_cus(query_cus()));
   if (op != DG_OP_GEMM_NT && op != DG_OP_BF16_GEMM_NT && op != DG_OP_GEMM_NT_UE8M0) return 0;
   if (rows <= 0 || N <= 0 || K <= 0 || K % (op == DG_OP_BF16_GEMM_NT ? 64 : 128)) return 0;

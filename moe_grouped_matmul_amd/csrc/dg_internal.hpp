@@ -15,6 +15,9 @@ struct GemmParams {
   uint16_t* D;           // bf16 output
   const float* Cacc;     // accumulating forms: fp32 C [G][rows][N] (null: zero), fp32 D below
   float* Dacc;           // accumulating forms: fp32 output D = C + A . B^T (may equal Cacc)
+  const float* bias;         // epilogue form: [N] or null
+  const uint16_t* residual;  // epilogue form: bf16 [rows][N] or null (may equal D)
+  uint16_t* pre;             // epilogue form: bf16 [rows][N], A . B^T + bias, or null
   float* ws;             // split-K partials [splits][rows][N] (dense only)
   const int32_t* index;  // m_indices (contiguous), masked_m (masked) or ks (K-grouped); unused when dense
   int64_t rows;          // dense: M; contiguous: M_total; masked: max_m (rows per group)
@@ -49,6 +52,8 @@ struct GemmParams {
 // by the matrix cores' block scaling; kContiguousUe8m0 / kMaskedUe8m0: the
 // M-grouped forms with those scales (sfb per expert; masked sfa
 // [G][ceil(KB/4)][max_m]).
+// kDenseEpi + an Activation: the dense fp8 schedule, D = act(A . B^T + bias) +
+// residual.
 enum GemmMode {
   kDense = 0,
   kContiguous = 1,
@@ -58,8 +63,10 @@ enum GemmMode {
   kKGrouped = 5,
   kDenseUe8m0 = 6,
   kContiguousUe8m0 = 7,
-  kMaskedUe8m0 = 8
+  kMaskedUe8m0 = 8,
+  kDenseEpi = 9  // .. 13
 };
+constexpr int kActivations = 5;
 
 // Split-K workspace layout shared by the skinny and persistent kernels: the
 // first kWsCounterBytes hold one uint32 completion counter per split tile
@@ -77,9 +84,10 @@ constexpr size_t kWsCounterBytes = 4 * kWsMaxCounters;
 // tiles), p.ws must hold skinny_workspace_bytes(...) bytes laid out as above.
 // ue: UE8M0 scales packed four per int32 along K (sfa [ceil(KB/4)][rows],
 // sfb [ceil(N/128)][ceil(KB/4)]); p.Dacc selects the fp32 accumulating
-// epilogue (fp32 scales only).
+// epilogue (fp32 scales only).  act: an Activation for the epilogue form (fp32
+// scales, the default depth of the tile), -1 for the others.
 size_t skinny_workspace_bytes(int bm, int m_tiles, int n_tiles, int wn, int splits);
-hipError_t launch_gemm_skinny(int bm, int wn, int depth, bool ue, const GemmParams& p, hipStream_t stream);
+hipError_t launch_gemm_skinny(int bm, int wn, int depth, bool ue, int act, const GemmParams& p, hipStream_t stream);
 // K blocks in flight per wave (ring depth; LDS per slot is (bm + 4 wn) * 128 B
 // plus 1 KB); a split's block count is padded to a multiple of it (padding
 // blocks read as zeros), so splits should be multiples.  Four slots for 64-row

@@ -72,6 +72,7 @@
 // promotion are shared with the wide-tile kernel (gemm_wide.hip).
 
 #include "dg_internal.hpp"
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 
 namespace dg {
@@ -103,7 +104,8 @@ struct Seg {
   int zero;          // K-grouped tile of a group without K blocks: one iteration over zeros
 };
 
-// HASC (fp32-output modes): C is given and read; without it nothing is loaded.
+// HASC (fp32-output modes): C is given and read; without it nothing is loaded
+// (epilogue form: the residual).
 // NT (masked forms with max_m <= 128, one row tile per expert): every weight
 // line is read by exactly one task, and the weight loads carry the
 // non-temporal cache policy (where two row tiles of an expert share the
@@ -115,6 +117,8 @@ __global__ void __launch_bounds__(512) fp8_gemm_persistent_kernel(GemmParams p) 
   constexpr bool ACC = MODE == kDenseAcc;    // fp32 output D = C + A . B^T
   constexpr bool KG = MODE == kKGrouped;     // groups along K, per-column beta, fp32 D[g] = C[g] + ...
   constexpr bool F32OUT = ACC || KG;
+  constexpr bool EPI = MODE >= kDenseEpi;    // bf16 D = act(A . B^T + bias) + residual
+  constexpr int ACT = EPI ? MODE - kDenseEpi : 0;
   // UE8M0 codes, applied by the matrix cores' block scaling (dense and the M-grouped forms)
   constexpr bool UE = MODE == kDenseUe8m0 || MODE == kContiguousUe8m0 || MODE == kMaskedUe8m0;
   // the schedule: dense, contiguous or masked (the UE8M0 grouped modes take those of their form)
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_persistent_kernel(GemmParams p) 
   const int dp_tiles = FORM == kMasked || KG ? T : p.dp_tiles;  // tasks run as whole tiles
   const int P = p.sk_pieces;                               // pieces per tail tile (dense)
   const int n_dp = b < dp_tiles ? (dp_tiles - b + G - 1) / G : 0;
-  const bool has_tail = (MODE == kDense || BF16 || ACC || MODE == kDenseUe8m0) && b < p.sk_tiles * P;
+  const bool has_tail = (MODE == kDense || BF16 || ACC || EPI || MODE == kDenseUe8m0) && b < p.sk_tiles * P;
   const int nseg = n_dp + (has_tail ? 1 : 0);
   if (nseg == 0) return;  // uniform over the workgroup
 
@@ -347,6 +351,11 @@ __global__ void __launch_bounds__(512) fp8_gemm_persistent_kernel(GemmParams p) 
                                         : make_rsrc(p.D, (uint32_t)rows * (uint32_t)N * 2u);
   // accumulating form: C (a null C reads as zeros through a zero-length range)
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.Cacc, ACC && p.Cacc ? (uint32_t)rows * (uint32_t)N * 4u : 0u);
+
+  // epilogue form: bias, residual and the kept product (null: zero-length, read as zeros and never written)
+  const __amdgpu_buffer_rsrc_t rb_epi = make_rsrc(p.bias, EPI && p.bias ? (uint32_t)N * 4u : 0u);
+  const __amdgpu_buffer_rsrc_t rr_epi = make_rsrc(p.residual, EPI && HASC ? (uint32_t)rows * (uint32_t)N * 2u : 0u);
+  const __amdgpu_buffer_rsrc_t rp_epi = make_rsrc(p.pre, EPI && p.pre ? (uint32_t)rows * (uint32_t)N * 2u : 0u);
 
   // DMA lanes: instruction i of this wave fills LDS rows 64 i + 8 wave + lane / 8;
   // lane chunk (lane % 8) of row r holds K chunk (lane % 8) ^ (r % 8).  B rows
@@ -542,6 +551,39 @@ __global__ void __launch_bounds__(512) fp8_gemm_persistent_kernel(GemmParams p) 
         _Pragma("unroll") for (int j_ = 0; j_ < TN; ++j_)                                                  \
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, u[i_][j_] + c_[i_][j_]), rd_,   \
                                                  o_[i_] + 16u * j_, 0, 0);                                 \
+    } else if constexpr (EPI) {                                                                            \
+      /* every load of the tile first; null operands read zeros through zero-length ranges */              \
+      const uint32_t c0_ = (uint32_t)(st_col0 + wn * 64 + q * 16);                                         \
+      uint32_t o_[TM];                                                                                     \
+      u32x4 r_[TM][2];                                                                                     \
+      f32x4 b_[TN];                                                                                        \
+      _Pragma("unroll") for (int j_ = 0; j_ < TN; ++j_) b_[j_] = bias4(rb_epi, c0_ + 4u * j_);             \
+      _Pragma("unroll") for (int i_ = 0; i_ < TM; ++i_) {                                                  \
+        o_[i_] = PS_OUT_OFF(i_);                                                                           \
+        _Pragma("unroll") for (int h_ = 0; h_ < 2; ++h_)                                                   \
+          r_[i_][h_] = HASC ? __builtin_amdgcn_raw_buffer_load_b128(rr_epi, o_[i_] == kOOB ? kOOB : o_[i_] + 16u * h_, 0, 0) \
+                            : u32x4{0u, 0u, 0u, 0u};                                                       \
+      }                                                                                                    \
+      _Pragma("unroll") for (int i_ = 0; i_ < TM; ++i_) {                                                  \
+        _Pragma("unroll") for (int j_ = 0; j_ < TN; ++j_) u[i_][j_] += b_[j_];                             \
+        if (p.pre) {                                                                                       \
+          _Pragma("unroll") for (int h_ = 0; h_ < 2; ++h_)                                                 \
+            __builtin_amdgcn_raw_buffer_store_b128(                                                        \
+                u32x4{pack_bf16x2(u[i_][2 * h_][0], u[i_][2 * h_][1]), pack_bf16x2(u[i_][2 * h_][2], u[i_][2 * h_][3]), \
+                      pack_bf16x2(u[i_][2 * h_ + 1][0], u[i_][2 * h_ + 1][1]),                              \
+                      pack_bf16x2(u[i_][2 * h_ + 1][2], u[i_][2 * h_ + 1][3])},                             \
+                rp_epi, o_[i_] == kOOB ? kOOB : o_[i_] + 16u * h_, 0, 0);                                  \
+        }                                                                                                  \
+        _Pragma("unroll") for (int h_ = 0; h_ < 2; ++h_) {                                                 \
+          u32x4 w_;                                                                                        \
+          _Pragma("unroll") for (int e_ = 0; e_ < 4; ++e_) {                                               \
+            const float x_ = activate<ACT>(u[i_][2 * h_ + (e_ >> 1)][2 * (e_ & 1)]);                       \
+            const float y_ = activate<ACT>(u[i_][2 * h_ + (e_ >> 1)][2 * (e_ & 1) + 1]);                   \
+            w_[e_] = HASC ? add_pack(r_[i_][h_][e_], x_, y_) : pack_bf16x2(x_, y_);                        \
+          }                                                                                                \
+          __builtin_amdgcn_raw_buffer_store_b128(w_, rd, o_[i_] == kOOB ? kOOB : o_[i_] + 16u * h_, 0, 0); \
+        }                                                                                                  \
+      }                                                                                                    \
     } else {                                                                                               \
       const __amdgpu_buffer_rsrc_t rdm_ =                                                                  \
           FORM == kMasked ? make_rsrc(p.D + (size_t)st_grp * (size_t)rows * (size_t)N, (uint32_t)rows * (uint32_t)N * 2u) : rd; \
@@ -839,6 +881,19 @@ size_t persistent_workspace_bytes(int sk_tiles, int sk_pieces) {
   return kWsCounterBytes + (size_t)sk_tiles * sk_pieces * 256 * 128 * 4;
 }
 
+// the epilogue form of each activation, with a residual and without
+template <int ACT>
+static void launch_epilogue(int act, dim3 g, const GemmParams& p, hipStream_t stream) {
+  if (act == ACT) {
+    if (p.residual)
+      hipLaunchKernelGGL((fp8_gemm_persistent_kernel<kDenseEpi + ACT, true, false>), g, dim3(512), 0, stream, p);
+    else
+      hipLaunchKernelGGL((fp8_gemm_persistent_kernel<kDenseEpi + ACT, false, false>), g, dim3(512), 0, stream, p);
+  } else if constexpr (ACT > 0) {
+    launch_epilogue<ACT - 1>(act, g, p, stream);
+  }
+}
+
 hipError_t launch_gemm_persistent(int mode, int grid, const GemmParams& p, hipStream_t stream) {
   if (grid <= 0) return hipSuccess;
   const dim3 g((unsigned)grid), t(512);
@@ -868,6 +923,8 @@ hipError_t launch_gemm_persistent(int mode, int grid, const GemmParams& p, hipSt
     hipLaunchKernelGGL((fp8_gemm_persistent_kernel<kMaskedUe8m0, false, true>), g, t, 0, stream, p);
   else if (mode == kMaskedUe8m0)
     hipLaunchKernelGGL((fp8_gemm_persistent_kernel<kMaskedUe8m0, false, false>), g, t, 0, stream, p);
+  else if (mode >= kDenseEpi)
+    launch_epilogue<kActivations - 1>(mode - kDenseEpi, g, p, stream);
   else
     hipLaunchKernelGGL((fp8_gemm_persistent_kernel<kDense, false, false>), g, t, 0, stream, p);
   return hipGetLastError();

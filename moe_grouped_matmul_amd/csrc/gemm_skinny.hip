@@ -47,6 +47,7 @@
 //     therefore independent of the order in which splits finish.
 
 #include "dg_internal.hpp"
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 
 namespace dg {
@@ -67,9 +68,16 @@ constexpr int kStream = 2;
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-template <int BM, int WN, int P, bool ACC, bool UE, bool NT>
+// What a launch writes: bf16 D, fp32 D = C + A . B^T, or (from kOutEpi on, one
+// per activation) bf16 D = act(A . B^T + bias) + residual.
+enum SkinnyOut { kOutBf16 = 0, kOutAcc = 1, kOutEpi = 2 };
+
+template <int BM, int WN, int P, int OUT, bool UE, bool NT>
 __global__ void __launch_bounds__(256) fp8_gemm_skinny_kernel(GemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool ACC = OUT == kOutAcc;
+  constexpr bool EPI = OUT >= kOutEpi;
+  constexpr int ACT = EPI ? OUT - kOutEpi : 0;
   constexpr int NW = 4;
   constexpr int TM = BM / 16;
   constexpr int TN = WN / 16;
@@ -82,7 +90,7 @@ __global__ void __launch_bounds__(256) fp8_gemm_skinny_kernel(GemmParams p) {
   static_assert(WN == 16 || WN == 32, "WN");
   static_assert(P == 4 || P == 6 || P == 8, "ring depth");
   static_assert((P - 1) * L_STEP < 64, "vmcnt range");
-  static_assert(!(ACC && UE), "the accumulating form has fp32 scales");
+  static_assert(!(OUT != kOutBf16 && UE), "the accumulating and epilogue forms have fp32 scales");
 
   // ring slots are separate arrays so the compiler can tell DMA targets from
   // the slots being read; slots 4..7 exist only for deeper rings
@@ -402,6 +410,38 @@ __global__ void __launch_bounds__(256) fp8_gemm_skinny_kernel(GemmParams p) {
     }
     return;
   }
+  if constexpr (EPI) {
+    // bias of the lane's columns, the residual of all row tiles in flight at
+    // once (the residual may be D: each lane reads what it writes)
+    if (c0 >= N) return;
+    f32x4 bv[TN];
+    uint2 rv[TM][TN];
+#pragma unroll
+    for (int jj = 0; jj < TN; ++jj)
+      bv[jj] = p.bias ? *reinterpret_cast<const f32x4*>(p.bias + c0 + 4 * jj) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = m0 + i * 16 + (lane & 15);
+#pragma unroll
+      for (int jj = 0; jj < TN; ++jj)
+        rv[i][jj] = r < M && p.residual ? *reinterpret_cast<const uint2*>(p.residual + (int64_t)r * N + c0 + 4 * jj) : uint2{0u, 0u};
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = m0 + i * 16 + (lane & 15);
+      if (r >= M) continue;
+      const int64_t at = (int64_t)r * N + c0;
+#pragma unroll
+      for (int jj = 0; jj < TN; ++jj) {
+        const f32x4 z = acc[i][jj] + bv[jj];
+        if (p.pre) *reinterpret_cast<uint2*>(p.pre + at + 4 * jj) = uint2{pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3])};
+        *reinterpret_cast<uint2*>(p.D + at + 4 * jj) =
+            uint2{add_pack(rv[i][jj].x, activate<ACT>(z[0]), activate<ACT>(z[1])),
+                  add_pack(rv[i][jj].y, activate<ACT>(z[2]), activate<ACT>(z[3]))};
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int r = m0 + i * 16 + (lane & 15);
@@ -430,18 +470,28 @@ __global__ void __launch_bounds__(256) fp8_gemm_skinny_kernel(GemmParams p) {
 #endif  // __HIP_DEVICE_COMPILE__
 }
 
+template <int BM, int WN, int P, bool NT, int ACT>
+void launch_skinny_epilogue(int act, const GemmParams& p, int64_t grid, hipStream_t stream) {
+  if (act == ACT)
+    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, kOutEpi + ACT, false, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+  else if constexpr (ACT > 0)
+    launch_skinny_epilogue<BM, WN, P, NT, ACT - 1>(act, p, grid, stream);
+}
+
 template <int BM, int WN, int P, bool NT>
-void launch_skinny_form(bool ue, const GemmParams& p, int64_t grid, hipStream_t stream) {
+void launch_skinny_form(bool ue, int act, const GemmParams& p, int64_t grid, hipStream_t stream) {
+  if constexpr (P == skinny_depth(BM, WN))
+    if (act >= 0) return launch_skinny_epilogue<BM, WN, P, NT, kActivations - 1>(act, p, grid, stream);
   if (ue)
-    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, false, true, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, kOutBf16, true, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   else if (p.Dacc)
-    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, true, false, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, kOutAcc, false, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, false, false, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((fp8_gemm_skinny_kernel<BM, WN, P, kOutBf16, false, NT>), dim3((unsigned)grid), dim3(256), 0, stream, p);
 }
 
 template <int BM, int WN, int P>
-hipError_t launch_skinny_cfg(bool ue, const GemmParams& p, hipStream_t stream) {
+hipError_t launch_skinny_cfg(bool ue, int act, const GemmParams& p, hipStream_t stream) {
   const int64_t units = (int64_t)p.n_tiles * p.splits;
   const int64_t grid = (units + 7) / 8 * 8 * p.m_tiles;
   if (grid <= 0) return hipSuccess;
@@ -450,11 +500,11 @@ hipError_t launch_skinny_cfg(bool ue, const GemmParams& p, hipStream_t stream) {
   // 128-row tile reads them, the default policy measured faster.
   if constexpr (BM == 64) {
     if (p.m_tiles == 1) {
-      launch_skinny_form<BM, WN, P, true>(ue, p, grid, stream);
+      launch_skinny_form<BM, WN, P, true>(ue, act, p, grid, stream);
       return hipGetLastError();
     }
   }
-  launch_skinny_form<BM, WN, P, false>(ue, p, grid, stream);
+  launch_skinny_form<BM, WN, P, false>(ue, act, p, grid, stream);
   return hipGetLastError();
 }
 
@@ -466,12 +516,13 @@ size_t skinny_workspace_bytes(int bm, int m_tiles, int n_tiles, int wn, int spli
   return kWsCounterBytes + (size_t)splits * m_tiles * n_tiles * bm * 4 * wn * 4;
 }
 
-hipError_t launch_gemm_skinny(int bm, int wn, int depth, bool ue, const GemmParams& p, hipStream_t stream) {
+hipError_t launch_gemm_skinny(int bm, int wn, int depth, bool ue, int act, const GemmParams& p, hipStream_t stream) {
+  const bool deep = act < 0 && depth != skinny_depth(bm, wn);  // the epilogue form has the default depths only
   if (bm == 64 && wn == 16)
-    return depth == 8 ? launch_skinny_cfg<64, 16, 8>(ue, p, stream) : launch_skinny_cfg<64, 16, 4>(ue, p, stream);
+    return deep ? launch_skinny_cfg<64, 16, 8>(ue, act, p, stream) : launch_skinny_cfg<64, 16, 4>(ue, act, p, stream);
   if (bm == 64)
-    return depth == 6 ? launch_skinny_cfg<64, 32, 6>(ue, p, stream) : launch_skinny_cfg<64, 32, 4>(ue, p, stream);
-  return wn == 16 ? launch_skinny_cfg<128, 16, 6>(ue, p, stream) : launch_skinny_cfg<128, 32, 4>(ue, p, stream);
+    return deep ? launch_skinny_cfg<64, 32, 6>(ue, act, p, stream) : launch_skinny_cfg<64, 32, 4>(ue, act, p, stream);
+  return wn == 16 ? launch_skinny_cfg<128, 16, 6>(ue, act, p, stream) : launch_skinny_cfg<128, 32, 4>(ue, act, p, stream);
 }
 
 }  // namespace dg

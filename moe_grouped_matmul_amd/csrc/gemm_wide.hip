@@ -73,6 +73,7 @@
 // loads the A rows tagged with its expert only.
 
 #include "dg_internal.hpp"
+#include "epilogue.hpp"
 #include "gemm_common.hpp"
 
 namespace dg {
@@ -94,7 +95,7 @@ template <int MODE, bool HASC>
 __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   static_assert(MODE == kDense || MODE == kContiguous || MODE == kDenseUe8m0 || MODE == kContiguousUe8m0 ||
-                    MODE == kDenseBf16 || MODE == kDenseAcc || MODE == kKGrouped,
+                    MODE == kDenseBf16 || MODE == kDenseAcc || MODE == kKGrouped || MODE >= kDenseEpi,
                 "modes of the wide kernel");
   constexpr bool KG = MODE == kKGrouped;     // groups along K, per-column beta, fp32 D[g] = C[g] + ...
   constexpr bool ACC = MODE == kDenseAcc || KG;  // fp32 output D = C + A . B^T
@@ -102,6 +103,8 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
   // UE8M0 codes, applied by the matrix cores' block scaling (dense and contiguous)
   constexpr bool UE = MODE == kDenseUe8m0 || MODE == kContiguousUe8m0;
   constexpr bool BF16 = MODE == kDenseBf16;  // bf16 operands, no scales, no promotion
+  constexpr bool EPI = MODE >= kDenseEpi;    // bf16 D = act(A . B^T + bias) + residual
+  constexpr int ACT = EPI ? MODE - kDenseEpi : 0;
   constexpr int MAXT = kWideMaxContigTiles;  // tiles per workgroup the contiguous pass table holds
   constexpr int WGN = 2;
   constexpr int TM = 4;
@@ -266,7 +269,11 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
   const uint32_t s_bytes = ((uint32_t)p.sfa_ld * (uint32_t)((UE ? KW : KB) - 1) + (uint32_t)rows) * 4u;
   const __amdgpu_buffer_rsrc_t rd = ACC ? wide_rsrc(p.Dacc, (uint32_t)rows * (uint32_t)N * 4u)
                                         : wide_rsrc(p.D, (uint32_t)rows * (uint32_t)N * 2u);
-  const __amdgpu_buffer_rsrc_t rc = wide_rsrc(p.Cacc, HASC ? (uint32_t)rows * (uint32_t)N * 4u : 0u);
+  const __amdgpu_buffer_rsrc_t rc = wide_rsrc(p.Cacc, ACC && HASC ? (uint32_t)rows * (uint32_t)N * 4u : 0u);
+  // epilogue form: bias, residual and the kept product (null: zero-length, read as zeros and never written)
+  const __amdgpu_buffer_rsrc_t rb_epi = wide_rsrc(p.bias, EPI && p.bias ? (uint32_t)N * 4u : 0u);
+  const __amdgpu_buffer_rsrc_t rr_epi = wide_rsrc(p.residual, EPI && HASC ? (uint32_t)rows * (uint32_t)N * 2u : 0u);
+  const __amdgpu_buffer_rsrc_t rp_epi = wide_rsrc(p.pre, EPI && p.pre ? (uint32_t)rows * (uint32_t)N * 2u : 0u);
 
   // DMA lanes (as gemm_persist.hip): instruction i of this wave fills LDS rows
   // 64 i + 8 wave + lane / 8, lane chunk (lane % 8) of row r holding K chunk
@@ -441,6 +448,21 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
                                     rcg_, o_ == kWideOOB ? kWideOOB : o_ + 16u * j_, 0, 0))                \
                               : f32x4{0.f, 0.f, 0.f, 0.f};                                                 \
   }
+#define WD_PUT(i_, h_, w_, rsrc_) /* eight packed words of the lane's run, through this wave's 2 KB of LDS */   \
+  do {                                                                                                     \
+    const int ra_ = st_row0 + wm * 64 + (i_) * 16 + sr_;                                                   \
+    *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q) ^ (q16 & 7)) << 4)) =                           \
+        uint4{w_[0], w_[1], w_[2], w_[3]};                                                                 \
+    *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q + 1) ^ (q16 & 7)) << 4)) =                       \
+        uint4{w_[4], w_[5], w_[6], w_[7]};                                                                 \
+    const uint4 va_ = *reinterpret_cast<const uint4*>(stg_ + sr_ * 128 + ((sc_ ^ sr_) << 4));              \
+    const uint4 vb_ = *reinterpret_cast<const uint4*>(stg_ + (8 + sr_) * 128 + ((sc_ ^ sr_) << 4));        \
+    const int c_ = st_col0 + wn * 128 + (h_) * 64 + sc_ * 8;                                               \
+    const uint32_t offa_ = (ra_ < rows && c_ < N) ? ((uint32_t)ra_ * (uint32_t)N + (uint32_t)c_) * 2u : kWideOOB; \
+    const uint32_t offb_ = (ra_ + 8 < rows && c_ < N) ? ((uint32_t)(ra_ + 8) * (uint32_t)N + (uint32_t)c_) * 2u : kWideOOB; \
+    __builtin_amdgcn_raw_buffer_store_b128(wu32x4{va_.x, va_.y, va_.z, va_.w}, rsrc_, offa_, 0, 0);        \
+    __builtin_amdgcn_raw_buffer_store_b128(wu32x4{vb_.x, vb_.y, vb_.z, vb_.w}, rsrc_, offb_, 0, 0);        \
+  } while (0)
 #define WD_STORE_U()                                                                                       \
   do {                                                                                                     \
     if constexpr (ACC) {                                                                                   \
@@ -462,6 +484,44 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
                                                    rdg_, o_ == kWideOOB ? kWideOOB : o_ + 16u * j_, 0, 0); \
         }                                                                                                  \
       }                                                                                                    \
+    } else if constexpr (EPI) {                                                                            \
+      /* the residual of a 64-column half is loaded first, in the layout of the accumulators (it may be D:  \
+         a run's loads precede its stores); null operands read zeros through zero-length ranges */         \
+      uint8_t* stg_ = stage + wave * 2048;                                                                 \
+      const int sr_ = lane >> 3;                                                                           \
+      const int sc_ = lane & 7;                                                                            \
+      _Pragma("unroll") for (int h_ = 0; h_ < 2; ++h_) {                                                   \
+        wu32x4 r_[HASC ? TM : 1][2];                                                                       \
+        if constexpr (HASC)                                                                                \
+          _Pragma("unroll") for (int i_ = 0; i_ < TM; ++i_) {                                              \
+            const int rr_ = st_row0 + wm * 64 + i_ * 16 + q16, c_ = st_col0 + wn * 128 + h_ * 64 + q * 16; \
+            const uint32_t o_ = rr_ < rows && c_ < N ? ((uint32_t)rr_ * (uint32_t)N + (uint32_t)c_) * 2u : kWideOOB; \
+            _Pragma("unroll") for (int t_ = 0; t_ < 2; ++t_)                                               \
+              r_[i_][t_] =                                                                                 \
+                  __builtin_amdgcn_raw_buffer_load_b128(rr_epi, o_ == kWideOOB ? kWideOOB : o_ + 16u * t_, 0, 0); \
+          }                                                                                                \
+        f32x4 b_[4];                                                                                       \
+        _Pragma("unroll") for (int j_ = 0; j_ < 4; ++j_)                                                   \
+          b_[j_] = bias4(rb_epi, (uint32_t)(st_col0 + wn * 128 + h_ * 64 + q * 16 + 4 * j_));              \
+        _Pragma("unroll") for (int i_ = 0; i_ < TM; ++i_) {                                                \
+          uint32_t w_[8];                                                                                  \
+          _Pragma("unroll") for (int j_ = 0; j_ < 4; ++j_) {                                               \
+            f32x4& z_ = u[i_][4 * h_ + j_];                                                                \
+            z_ += b_[j_];                                                                                  \
+            w_[2 * j_] = pack_bf16x2(z_[0], z_[1]);                                                        \
+            w_[2 * j_ + 1] = pack_bf16x2(z_[2], z_[3]);                                                    \
+          }                                                                                                \
+          if (p.pre) WD_PUT(i_, h_, w_, rp_epi);                                                           \
+          if constexpr (ACT != kActNone || HASC)                                                           \
+            _Pragma("unroll") for (int e_ = 0; e_ < 8; ++e_) {                                             \
+              const f32x4 z_ = u[i_][4 * h_ + (e_ >> 1)];                                                  \
+              const float x_ = activate<ACT>(z_[2 * (e_ & 1)]), y_ = activate<ACT>(z_[2 * (e_ & 1) + 1]);  \
+              if constexpr (HASC) w_[e_] = add_pack(r_[i_][e_ >> 2][e_ & 3], x_, y_);           \
+              else w_[e_] = pack_bf16x2(x_, y_);                                                           \
+            }                                                                                              \
+          WD_PUT(i_, h_, w_, rd);                                                                          \
+        }                                                                                                  \
+      }                                                                                                    \
     } else if constexpr (!CONTIG) {                                                                        \
       /* through this wave's 2 KB of LDS, one 16-row x 64-column block at a time: lane (q, r) writes its     \
          32 bytes of row r, then lane l reads 16 bytes of row l / 8 (and 8 + l / 8) at chunk l % 8, so      \
@@ -471,24 +531,13 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
       const int sr_ = lane >> 3;                                                                           \
       const int sc_ = lane & 7;                                                                            \
       _Pragma("unroll") for (int i_ = 0; i_ < TM; ++i_) {                                                  \
-        const int ra_ = st_row0 + wm * 64 + i_ * 16 + sr_;                                                 \
         _Pragma("unroll") for (int h_ = 0; h_ < 2; ++h_) {                                                 \
           uint32_t w_[8];                                                                                  \
           _Pragma("unroll") for (int j_ = 0; j_ < 4; ++j_) {                                               \
             w_[2 * j_] = pack_bf16x2(u[i_][4 * h_ + j_][0], u[i_][4 * h_ + j_][1]);                        \
             w_[2 * j_ + 1] = pack_bf16x2(u[i_][4 * h_ + j_][2], u[i_][4 * h_ + j_][3]);                    \
           }                                                                                                \
-          *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q) ^ (q16 & 7)) << 4)) =                     \
-              uint4{w_[0], w_[1], w_[2], w_[3]};                                                           \
-          *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q + 1) ^ (q16 & 7)) << 4)) =                 \
-              uint4{w_[4], w_[5], w_[6], w_[7]};                                                           \
-          const uint4 va_ = *reinterpret_cast<const uint4*>(stg_ + sr_ * 128 + ((sc_ ^ sr_) << 4));        \
-          const uint4 vb_ = *reinterpret_cast<const uint4*>(stg_ + (8 + sr_) * 128 + ((sc_ ^ sr_) << 4));  \
-          const int c_ = st_col0 + wn * 128 + h_ * 64 + sc_ * 8;                                           \
-          const uint32_t offa_ = (ra_ < rows && c_ < N) ? ((uint32_t)ra_ * (uint32_t)N + (uint32_t)c_) * 2u : kWideOOB; \
-          const uint32_t offb_ = (ra_ + 8 < rows && c_ < N) ? ((uint32_t)(ra_ + 8) * (uint32_t)N + (uint32_t)c_) * 2u : kWideOOB; \
-          __builtin_amdgcn_raw_buffer_store_b128(wu32x4{va_.x, va_.y, va_.z, va_.w}, rd, offa_, 0, 0);   \
-          __builtin_amdgcn_raw_buffer_store_b128(wu32x4{vb_.x, vb_.y, vb_.z, vb_.w}, rd, offb_, 0, 0);   \
+          WD_PUT(i_, h_, w_, rd);                                                                          \
         }                                                                                                  \
       }                                                                                                    \
     } else                                                                                                 \
@@ -654,6 +703,7 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
 #undef WD_STEP
 #undef WD_FRAG
 #undef WD_STORE_U
+#undef WD_PUT
 #undef WD_LOAD_C
 #undef WD_OUT_OFF
 #undef WD_ISSUE_BEGIN
@@ -665,6 +715,19 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
 }
 
 }  // namespace
+
+// the epilogue form of each activation, with a residual and without
+template <int ACT>
+static void launch_wide_epilogue(int act, int grid, const GemmParams& p, hipStream_t stream) {
+  if (act == ACT) {
+    if (p.residual)
+      hipLaunchKernelGGL((fp8_gemm_wide_kernel<kDenseEpi + ACT, true>), dim3((unsigned)grid), dim3(512), 0, stream, p);
+    else
+      hipLaunchKernelGGL((fp8_gemm_wide_kernel<kDenseEpi + ACT, false>), dim3((unsigned)grid), dim3(512), 0, stream, p);
+  } else if constexpr (ACT > 0) {
+    launch_wide_epilogue<ACT - 1>(act, grid, p, stream);
+  }
+}
 
 hipError_t launch_gemm_wide(int mode, int grid, const GemmParams& p, hipStream_t stream) {
   if (grid <= 0) return hipSuccess;
@@ -684,6 +747,8 @@ hipError_t launch_gemm_wide(int mode, int grid, const GemmParams& p, hipStream_t
     hipLaunchKernelGGL((fp8_gemm_wide_kernel<kDenseAcc, true>), dim3((unsigned)grid), dim3(512), 0, stream, p);
   else if (mode == kDenseAcc)
     hipLaunchKernelGGL((fp8_gemm_wide_kernel<kDenseAcc, false>), dim3((unsigned)grid), dim3(512), 0, stream, p);
+  else if (mode >= kDenseEpi)
+    launch_wide_epilogue<kActivations - 1>(mode - kDenseEpi, grid, p, stream);
   else
     hipLaunchKernelGGL((fp8_gemm_wide_kernel<kDense, false>), dim3((unsigned)grid), dim3(512), 0, stream, p);
   return hipGetLastError();

@@ -34,4 +34,9 @@ int check_contiguous_layout(const int32_t* m_indices, int64_t M_total, int64_t G
 size_t moe_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus);
 int moe_describe_plan(int op, int64_t rows, int64_t N, int64_t K, int64_t G, int cus, char* buf, size_t n);
 
+// Workspace bytes of the operations of api_block.cpp (0 for others).
+size_t block_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int cus);
+// DG_ERR_INVALID_ARG unless `act` is one of the DG_ACT_* values
+int check_activation(int act);
+
 }  // namespace dg

@@ -33,9 +33,21 @@ DG_OP_K_GROUPED = 5
 DG_OP_MXFP4_GEMM_NT = 6
 DG_OP_MOE_GATE = 7
 DG_OP_MOE_LAYOUT = 8
+DG_OP_MOE_EXPERTS = 9
+DG_OP_RMS_NORM_BWD = 10
+DG_OP_EPILOGUE_BWD = 11
 
 DG_F32 = 0
 DG_BF16 = 1
+
+DG_ACT_NONE = 0
+DG_ACT_RELU = 1
+DG_ACT_SILU = 2
+DG_ACT_GELU = 3
+DG_ACT_GELU_TANH = 4
+
+DG_SCALE_F32 = 0
+DG_SCALE_UE8M0 = 1
 
 EXPORTED = (
     "dg_fp8_gemm_nt",
@@ -63,6 +75,10 @@ EXPORTED = (
     "dg_moe_layout_masked",
     "dg_moe_combine",
     "dg_moe_combine_bwd",
+    "dg_fp8_gemm_nt_epilogue",
+    "dg_epilogue_bwd",
+    "dg_rms_norm",
+    "dg_rms_norm_bwd",
     "dg_get_workspace_size",
     "dg_describe_plan",
     "dg_get_m_alignment_for_contiguous_layout",
@@ -132,6 +148,10 @@ def load_library():
     lib.dg_moe_layout_masked.argtypes = [P, P, P, P, I64, I64, I64, I64, I64, P, SZ, P]
     lib.dg_moe_combine.argtypes = [P, P, P, P, I, I64, I64, I64, I64, P]
     lib.dg_moe_combine_bwd.argtypes = [P, I, P, P, P, P, P, I64, I64, I64, I64, P]
+    lib.dg_fp8_gemm_nt_epilogue.argtypes = [P, P, P, P, P, I, P, P, P, I64, I64, I64, P, SZ, P]
+    lib.dg_epilogue_bwd.argtypes = [P, P, I, P, P, P, P, I64, I64, P, SZ, P]
+    lib.dg_rms_norm.argtypes = [P, P, P, I, I, P, P, P, P, I, P, I64, I64, F, P]
+    lib.dg_rms_norm_bwd.argtypes = [P, P, P, P, I, I, P, P, P, I64, I64, P, SZ, P]
     lib.dg_get_workspace_size.argtypes = [I, I64, I64, I64, I64]
     lib.dg_get_workspace_size.restype = SZ
     lib.dg_describe_plan.argtypes = [I, I64, I64, I64, I64]
@@ -147,7 +167,8 @@ def load_library():
                  "dg_m_grouped_fp8_gemm_nt_masked_ue8m0", "dg_quant_128x128", "dg_quant_mxfp4", "dg_dequant_mxfp4",
                  "dg_mxfp4_gemm_nt", "dg_m_grouped_mxfp4_gemm_nt_contiguous", "dg_m_grouped_mxfp4_gemm_nt_masked",
                  "dg_moe_gate", "dg_moe_gate_bwd", "dg_moe_layout_contiguous", "dg_moe_layout_masked",
-                 "dg_moe_combine", "dg_moe_combine_bwd", "dg_set_num_cus", "dg_get_num_cus",
+                 "dg_moe_combine", "dg_moe_combine_bwd", "dg_fp8_gemm_nt_epilogue", "dg_epilogue_bwd", "dg_rms_norm",
+                 "dg_rms_norm_bwd", "dg_set_num_cus", "dg_get_num_cus",
                  "dg_get_m_alignment_for_contiguous_layout"):
         getattr(lib, name).restype = I
     try:
@@ -750,4 +771,98 @@ def dg_moe_combine_bwd(dy, rows, row_of, w, drows, dw, stream=None):
         _arg(dy, "dy", dy.dtype, (T, N), dev), dt, _arg(rows, "rows", torch.bfloat16, (R, N), dev),
         _arg(row_of, "row_of", torch.int32, (T, k), dev), _arg(w, "w", torch.float32, (T, k), dev),
         _arg(drows, "drows", torch.bfloat16, (R, N), dev), _arg(dw, "dw", torch.float32, (T, k), dev), T, k, N, R,
+        _raw_stream(stream, dev)))
+
+
+# ---- operators that join the products of a block
+
+_ACTS = {"none": DG_ACT_NONE, "relu": DG_ACT_RELU, "silu": DG_ACT_SILU, "gelu": DG_ACT_GELU, "gelu_tanh": DG_ACT_GELU_TANH}
+
+
+def _act_arg(act):
+    """A DG_ACT_* value, or its name in lower case."""
+    if act.__class__ is int:
+        return act
+    a = _ACTS.get(act)
+    if a is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)} or a DG_ACT_* value (got {act!r})")
+    return a
+
+
+def _codes(t):
+    # e4m3 codes as torch's own type or as bytes
+    return t.view(torch.uint8) if t.dtype is torch.float8_e4m3fn else t
+
+
+def dg_fp8_gemm_nt_epilogue(A, sfa, B, sfb, D, bias=None, act="none", residual=None, pre=None, workspace=None, stream=None):
+    """z = A[M,K] . B[N,K]^T + bias, D[M,N] (bf16, written) = act(z) + residual; sfa [K/128,M], sfb [ceil(N/128),K/128].
+    bias [N] fp32, residual [M,N] bf16 (may be D), pre [M,N] bf16 (written: z), act a name ("none", "relu", "silu",
+    "gelu", "gelu_tanh") or DG_ACT_*.  workspace as for dg_fp8_gemm_nt."""
+    dev = torch.cuda.current_device()
+    A, B = _codes(A), _codes(B)
+    M, K = _dims(A, "A", 2)
+    N = _dims(B, "B", 2)[0]
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    bf = torch.bfloat16
+    _check(load_library().dg_fp8_gemm_nt_epilogue(
+        _arg(A, "A", torch.uint8, (M, K), dev), _arg(sfa, "sfa", torch.float32, (K // 128, M), dev),
+        _arg(B, "B", torch.uint8, (N, K), dev), _arg(sfb, "sfb", torch.float32, ((N + 127) // 128, K // 128), dev),
+        None if bias is None else _arg(bias, "bias", torch.float32, (N,), dev), _act_arg(act),
+        None if residual is None else _arg(residual, "residual", bf, (M, N), dev),
+        None if pre is None else _arg(pre, "pre", bf, (M, N), dev), _arg(D, "D", bf, (M, N), dev), M, N, K, ws, ws_bytes,
+        _raw_stream(stream, dev)))
+
+
+def dg_epilogue_bwd(dy, dz=None, pre=None, act="none", q=None, sf=None, dbias=None, workspace=None, stream=None):
+    """Gradient of dg_fp8_gemm_nt_epilogue's epilogue: dz = dy * act'(pre) from dy and pre [M,N] bf16 -> dz [M,N] bf16,
+    q [M,N] e4m3 with sf [N/128,M] fp32, dbias [N] fp32, each optional.  workspace (with dbias):
+    dg_get_workspace_size(DG_OP_EPILOGUE_BWD, M, N, 0) bytes."""
+    dev = torch.cuda.current_device()
+    M, N = _dims(dy, "dy", 2)
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    bf = torch.bfloat16
+    _check(load_library().dg_epilogue_bwd(
+        _arg(dy, "dy", bf, (M, N), dev), None if pre is None else _arg(pre, "pre", bf, (M, N), dev), _act_arg(act),
+        None if dz is None else _arg(dz, "dz", bf, (M, N), dev),
+        None if q is None else _arg(_codes(q), "q", torch.uint8, (M, N), dev),
+        None if sf is None else _arg(sf, "sf", torch.float32, (N // 128, M), dev),
+        None if dbias is None else _arg(dbias, "dbias", torch.float32, (N,), dev), M, N, ws, ws_bytes,
+        _raw_stream(stream, dev)))
+
+
+def dg_rms_norm(x, weight, residual=None, h=None, y=None, q=None, sf=None, rstd=None, eps=1e-6, stream=None):
+    """h = x + residual, then v = h / sqrt(mean(h^2) + eps) * weight: x, residual, h, y [M,K] fp32 or bf16, weight [K]
+    fp32 or bf16; y receives v, q [M,K] and sf its 1x128 e4m3 quantisation (sf fp32 [K/128,M], or int32 [ceil(K/512),M]
+    for UE8M0 codes), rstd [M] fp32 the factor.  h is written (needed with a residual); y or q is needed."""
+    dev = torch.cuda.current_device()
+    dt, wt = _float_arg(x, "x"), _float_arg(weight, "weight")
+    M, K = _dims(x, "x", 2)
+    t = x.dtype
+    kind, sp = DG_SCALE_F32, None
+    if sf is not None:
+        if sf.dtype is torch.int32:
+            kind, sp = DG_SCALE_UE8M0, _arg(sf, "sf", torch.int32, (_kw(K), M), dev)
+        else:
+            sp = _arg(sf, "sf", torch.float32, (K // 128, M), dev)
+    _check(load_library().dg_rms_norm(
+        _arg(x, "x", t, (M, K), dev), None if residual is None else _arg(residual, "residual", t, (M, K), dev),
+        _arg(weight, "weight", weight.dtype, (K,), dev), dt, wt, None if h is None else _arg(h, "h", t, (M, K), dev),
+        None if y is None else _arg(y, "y", t, (M, K), dev),
+        None if q is None else _arg(_codes(q), "q", torch.uint8, (M, K), dev), sp, kind,
+        None if rstd is None else _arg(rstd, "rstd", torch.float32, (M,), dev), M, K, eps, _raw_stream(stream, dev)))
+
+
+def dg_rms_norm_bwd(dy, h, weight, rstd, dx, dw, dh=None, workspace=None, stream=None):
+    """Gradients of dg_rms_norm: dx [M,K] (of x and of the residual; plus dh, the gradient that reaches h otherwise) and dw
+    [K] fp32 from dy, h [M,K] of one type, weight [K], rstd [M] fp32.  workspace:
+    dg_get_workspace_size(DG_OP_RMS_NORM_BWD, M, 0, K) bytes."""
+    dev = torch.cuda.current_device()
+    dt, wt = _float_arg(h, "h"), _float_arg(weight, "weight")
+    M, K = _dims(h, "h", 2)
+    t = h.dtype
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    _check(load_library().dg_rms_norm_bwd(
+        _arg(dy, "dy", t, (M, K), dev), _arg(h, "h", t, (M, K), dev), _arg(weight, "weight", weight.dtype, (K,), dev),
+        _arg(rstd, "rstd", torch.float32, (M,), dev), dt, wt, None if dh is None else _arg(dh, "dh", t, (M, K), dev),
+        _arg(dx, "dx", t, (M, K), dev), _arg(dw, "dw", torch.float32, (K,), dev), M, K, ws, ws_bytes,
         _raw_stream(stream, dev)))
