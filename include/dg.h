@@ -509,6 +509,33 @@ int dg_moe_combine(const uint16_t* rows, const int32_t* row_of, const float* w, 
 int dg_moe_combine_bwd(const void* dy, int dtype, const uint16_t* rows, const int32_t* row_of, const float* w,
                        uint16_t* drows, float* dw, int64_t T, int64_t k, int64_t N, int64_t R, void* stream);
 
+/*
+ * The experts of a mixture-of-experts layer for a few tokens, in two kernels:
+ *   y[t] = sum_j topk_w[t,j] W2_e (silu(W1g_e x[t]) * (W1u_e x[t])),  e = topk_idx[t,j] - first_expert in [0, G)
+ * (other choices, -1 among them, add nothing; a token without one gets zeros).
+ *   x [T,H] bf16            topk_idx [T,k] int32, topk_w [T,k] fp32 (as from dg_moe_gate)
+ *   y [T,H] bf16 (written); may equal x
+ *   w1 [G,2 I,H]: rows [0, I) the gate projection, [I, 2 I) the up projection;  w2 [G,H,I]
+ *   fp8:   e4m3, s1 [G][2 I / 128][H/128] and s2 [G][H / 128][I/128] fp32 (dg_quant_128x128)
+ *   mxfp4: packed e2m1 ([G,2 I,H/2] and [G,H,I/2] bytes), s1 [G][H/128][2 I] and s2 [G][I/128][H] int32 (dg_quant_mxfp4)
+ * Activations stay bf16: the weights are widened exactly, products are summed in
+ * fp32, the inner activations are rounded to bf16 once and y once; a token's
+ * experts are added in the order of their numbers (an e2m1 element past bf16's range, scale
+ * codes 253 and above, is infinite).  The weights of the chosen experts are read once for up to 32
+ * of their tokens.  A choice named twice counts twice.
+ * T in [0, 64], k in [1, 16], G in [1, 1024], H and I multiples of 128 up to
+ * 32768.  workspace: required, dg_get_workspace_size(DG_OP_MOE_EXPERTS, T k, H,
+ * I, 1) bytes, which also serve fewer tokens and choices; as for
+ * dg_fp8_gemm_nt it is zero-filled before its first use and left reusable, by
+ * the other operators too, in calls ordered on one stream.  Deterministic.
+ */
+int dg_moe_experts_fp8(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint8_t* w1, const float* s1,
+                       const uint8_t* w2, const float* s2, uint16_t* y, int64_t T, int64_t k, int64_t first_expert, int64_t G,
+                       int64_t H, int64_t I, void* workspace, size_t workspace_bytes, void* stream);
+int dg_moe_experts_mxfp4(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint8_t* w1, const int32_t* s1,
+                         const uint8_t* w2, const int32_t* s2, uint16_t* y, int64_t T, int64_t k, int64_t first_expert, int64_t G,
+                         int64_t H, int64_t I, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes that let `op` use its full K split for this shape with the
  * current CU cap (0 = none used); a call split into row chunks reuses it for
  * every chunk. */

@@ -25,7 +25,7 @@ ARGS_PATH = os.path.join(HERE, "_args.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "gemm_skinny.hip", "gemm_persist.hip", "gemm_wide.hip", "noalloc.hip", "mxfp4_quant.hip", "mxfp4_gemm.hip", "mxfp4_wide.hip",
-           "moe_gate.hip", "moe_layout.hip", "moe_combine.hip", "rms_norm.hip", "epilogue_bwd.hip", "api.cpp", "api_moe.cpp", "api_block.cpp"]
+           "moe_gate.hip", "moe_layout.hip", "moe_combine.hip", "rms_norm.hip", "epilogue_bwd.hip", "moe_experts.hip", "api.cpp", "api_moe.cpp", "api_block.cpp"]
 # per-source flags: the persistent kernels need the iterative ILP scheduler to
 # stay within 256 VGPRs (two waves per SIMD) without spilling
 SOURCE_FLAGS = {"gemm_persist.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],

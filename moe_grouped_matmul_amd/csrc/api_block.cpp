@@ -1,6 +1,7 @@
 // C ABI of the operators that join the products of a block: the root-mean-square
-// norm and the gradient of a product's epilogue.  As in api.cpp, no call
-// allocates, synchronises or reads device data on the host, and no call throws.
+// norm, the gradient of a product's epilogue, and the experts of a layer for a
+// few tokens.  As in api.cpp, no call allocates, synchronises or reads device
+// data on the host, and no call throws.
 
 #include <cmath>
 
@@ -40,6 +41,58 @@ int check_partials(const void* ws, size_t ws_bytes, size_t need) {
   return DG_OK;
 }
 
+size_t experts_bytes(int64_t choices, int64_t T, int64_t H, int64_t I, int splits) {
+  return kBlockWsCounterBytes + experts_h_bytes(choices, I) + (splits > 1 ? (size_t)splits * (size_t)H * (size_t)T * 4 : 0);
+}
+
+bool experts_dim(int64_t d) { return d > 0 && d % 128 == 0 && d <= kExpertsMaxDim; }
+
+int run_experts(bool fp4, const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint8_t* w1, const void* s1,
+                const uint8_t* w2, const void* s2, uint16_t* y, int64_t T, int64_t k, int64_t first_expert, int64_t G, int64_t H,
+                int64_t I, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 0 || T > kExpertsMaxTokens) return fail(DG_ERR_SHAPE, "T must be in [0, %d] (got %lld)", kExpertsMaxTokens, (long long)T);
+  if (k < 1 || k > kExpertsMaxTopK) return fail(DG_ERR_SHAPE, "k must be in [1, %d] (got %lld)", kExpertsMaxTopK, (long long)k);
+  if (G < 1 || G > kExpertsMaxGroups) return fail(DG_ERR_SHAPE, "G must be in [1, %d] (got %lld)", kExpertsMaxGroups, (long long)G);
+  if (first_expert < 0 || first_expert > kIntMax - G) return fail(DG_ERR_SHAPE, "first_expert out of range");
+  if (!experts_dim(H) || !experts_dim(I))
+    return fail(DG_ERR_SHAPE, "H and I must be positive multiples of 128 up to %d (got %lld and %lld)", kExpertsMaxDim, (long long)H, (long long)I);
+  if (T == 0) return ok();
+  if (!x || !topk_idx || !topk_w || !w1 || !s1 || !w2 || !s2 || !y) return fail(DG_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16))
+    return fail(DG_ERR_ALIGN, "x, w1, w2 and y must be 16-byte aligned");
+  if (!aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(s1, 4) || !aligned(s2, 4))
+    return fail(DG_ERR_ALIGN, "topk_idx, topk_w and scales must be 4-byte aligned");
+  int cus = 0, rc = check_device(&cus);
+  if (rc) return rc;
+  const int splits = experts_splits(T * k, H, I, G, effective_cus(cus));
+  const size_t need = experts_bytes(T * k, T, H, I, splits);
+  if (!ws || !aligned(ws, 16) || ws_bytes < need)
+    return fail(DG_ERR_WORKSPACE, "a 16-byte aligned workspace of at least %zu bytes is needed", need);
+  uint8_t* base = static_cast<uint8_t*>(ws) + kBlockWsCounterBytes;
+  ExpertsParams p{};
+  p.x = x;
+  p.idx = topk_idx;
+  p.w = topk_w;
+  p.w1 = w1;
+  p.s1 = s1;
+  p.w2 = w2;
+  p.s2 = s2;
+  p.y = y;
+  p.h = reinterpret_cast<uint16_t*>(base);
+  p.partials = reinterpret_cast<float*>(base + experts_h_bytes(T * k, I));
+  p.counters = static_cast<unsigned int*>(ws);
+  p.T = (int)T;
+  p.k = (int)k;
+  p.first = (int)first_expert;
+  p.G = (int)G;
+  p.H = (int)H;
+  p.I = (int)I;
+  p.splits = splits;
+  // weights that the 256 MB Infinity Cache cannot hold from one call to the next are streamed past it
+  const bool stream_weights = G * 3 * H * I / (fp4 ? 2 : 1) >= (int64_t)256 << 20;
+  return launched(launch_moe_experts(p, fp4, stream_weights, hs(stream)));
+}
+
 float* partials_of(void* ws) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kBlockWsCounterBytes); }
 
 }  // namespace
@@ -59,6 +112,10 @@ size_t block_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int cus)
   } else if (op == DG_OP_EPILOGUE_BWD) {
     if (N <= 0 || N % 16 || N > (int64_t)1 << 30) return 0;
     need = partials_bytes(epilogue_bwd_partials(rows, N, cus), N);
+  } else if (op == DG_OP_MOE_EXPERTS) {
+    if (rows > kExpertsMaxChoices || !experts_dim(N) || !experts_dim(K)) return 0;
+    const int64_t tokens = rows < kExpertsMaxTokens ? rows : kExpertsMaxTokens;  // k may be 1
+    need = experts_bytes(rows, tokens, N, K, experts_splits(rows, N, K, kExpertsMaxGroups, cus));
   }
   return (need + 15) / 16 * 16;
 }
@@ -124,6 +181,18 @@ int dg_epilogue_bwd(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* 
   if (dbias && (rc = check_partials(workspace, workspace_bytes, partials_bytes(ceil_div(M, rows), N)))) return rc;
   const EpilogueBwdParams p{dy, pre, dz, q, sf, dbias, dbias ? partials_of(workspace) : nullptr, M, rows, (int)N};
   return launched(launch_epilogue_bwd(p, act, hs(stream)));
+}
+
+int dg_moe_experts_fp8(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint8_t* w1, const float* s1,
+                       const uint8_t* w2, const float* s2, uint16_t* y, int64_t T, int64_t k, int64_t first_expert, int64_t G,
+                       int64_t H, int64_t I, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_experts(false, x, topk_idx, topk_w, w1, s1, w2, s2, y, T, k, first_expert, G, H, I, workspace, workspace_bytes, stream);
+}
+
+int dg_moe_experts_mxfp4(const uint16_t* x, const int32_t* topk_idx, const float* topk_w, const uint8_t* w1, const int32_t* s1,
+                         const uint8_t* w2, const int32_t* s2, uint16_t* y, int64_t T, int64_t k, int64_t first_expert, int64_t G,
+                         int64_t H, int64_t I, void* workspace, size_t workspace_bytes, void* stream) {
+  return run_experts(true, x, topk_idx, topk_w, w1, s1, w2, s2, y, T, k, first_expert, G, H, I, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -64,4 +64,30 @@ int64_t epilogue_bwd_rows(int64_t M, int64_t N, int cus);
 int64_t epilogue_bwd_partials(int64_t M, int64_t N, int cus);  // rows of partials that serve up to M rows
 hipError_t launch_epilogue_bwd(const EpilogueBwdParams& p, int act, hipStream_t stream);
 
+
+// ---- experts of a mixture-of-experts layer for a few tokens (moe_experts.hip)
+constexpr int kExpertsMaxTokens = 64;
+constexpr int kExpertsMaxTopK = 16;
+constexpr int kExpertsMaxChoices = kExpertsMaxTokens * kExpertsMaxTopK;
+constexpr int kExpertsMaxGroups = 1024;
+constexpr int kExpertsMaxDim = 32768;  // H and I: a wave's quarter of a row is at most 64 steps of 128
+struct ExpertsParams {
+  const uint16_t* x;     // [T][H] bf16
+  const int32_t* idx;    // [T][k]
+  const float* w;        // [T][k]
+  const uint8_t* w1;     // [G][2 I][H], gate rows first
+  const void* s1;
+  const uint8_t* w2;     // [G][H][I]
+  const void* s2;
+  uint16_t* y;           // [T][H] bf16
+  uint16_t* h;           // [T k][I] bf16
+  float* partials;       // [H / 16][splits][T][16], splits > 1
+  unsigned int* counters;
+  int T, k, first, G, H, I;
+  int splits;
+};
+int experts_splits(int64_t choices, int64_t H, int64_t I, int64_t G, int cus);
+size_t experts_h_bytes(int64_t choices, int64_t I);
+hipError_t launch_moe_experts(const ExpertsParams& p, bool fp4, bool stream_weights, hipStream_t stream);
+
 }  // namespace dg

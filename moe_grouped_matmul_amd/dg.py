@@ -79,6 +79,8 @@ EXPORTED = (
     "dg_epilogue_bwd",
     "dg_rms_norm",
     "dg_rms_norm_bwd",
+    "dg_moe_experts_fp8",
+    "dg_moe_experts_mxfp4",
     "dg_get_workspace_size",
     "dg_describe_plan",
     "dg_get_m_alignment_for_contiguous_layout",
@@ -152,6 +154,8 @@ def load_library():
     lib.dg_epilogue_bwd.argtypes = [P, P, I, P, P, P, P, I64, I64, P, SZ, P]
     lib.dg_rms_norm.argtypes = [P, P, P, I, I, P, P, P, P, I, P, I64, I64, F, P]
     lib.dg_rms_norm_bwd.argtypes = [P, P, P, P, I, I, P, P, P, I64, I64, P, SZ, P]
+    lib.dg_moe_experts_fp8.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I64, P, SZ, P]
+    lib.dg_moe_experts_mxfp4.argtypes = lib.dg_moe_experts_fp8.argtypes
     lib.dg_get_workspace_size.argtypes = [I, I64, I64, I64, I64]
     lib.dg_get_workspace_size.restype = SZ
     lib.dg_describe_plan.argtypes = [I, I64, I64, I64, I64]
@@ -168,7 +172,7 @@ def load_library():
                  "dg_mxfp4_gemm_nt", "dg_m_grouped_mxfp4_gemm_nt_contiguous", "dg_m_grouped_mxfp4_gemm_nt_masked",
                  "dg_moe_gate", "dg_moe_gate_bwd", "dg_moe_layout_contiguous", "dg_moe_layout_masked",
                  "dg_moe_combine", "dg_moe_combine_bwd", "dg_fp8_gemm_nt_epilogue", "dg_epilogue_bwd", "dg_rms_norm",
-                 "dg_rms_norm_bwd", "dg_set_num_cus", "dg_get_num_cus",
+                 "dg_rms_norm_bwd", "dg_moe_experts_fp8", "dg_moe_experts_mxfp4", "dg_set_num_cus", "dg_get_num_cus",
                  "dg_get_m_alignment_for_contiguous_layout"):
         getattr(lib, name).restype = I
     try:
@@ -866,3 +870,40 @@ def dg_rms_norm_bwd(dy, h, weight, rstd, dx, dw, dh=None, workspace=None, stream
         _arg(rstd, "rstd", torch.float32, (M,), dev), dt, wt, None if dh is None else _arg(dh, "dh", t, (M, K), dev),
         _arg(dx, "dx", t, (M, K), dev), _arg(dw, "dw", torch.float32, (K,), dev), M, K, ws, ws_bytes,
         _raw_stream(stream, dev)))
+
+
+def dg_moe_experts_fp8(x, topk_idx, topk_w, w1, s1, w2, s2, y, first_expert=0, workspace=None, stream=None):
+    """Experts first_expert + [0, G) of a mixture-of-experts layer for up to 64 tokens: x [T,H] bf16, topk_idx [T,k] int32 and
+    topk_w [T,k] fp32 -> y [T,H] bf16 (may be x), y[t] = sum_j topk_w[t,j] w2_e (silu(gate) * up) of w1_e x[t].  w1 [G,2I,H]
+    (gate rows, then up rows) and w2 [G,H,I] e4m3, s1 [G,2I/128,H/128] and s2 [G,H/128,I/128] fp32.  workspace:
+    dg_get_workspace_size(DG_OP_MOE_EXPERTS, T * k, H, I) bytes."""
+    dev = torch.cuda.current_device()
+    w1, w2 = _codes(w1), _codes(w2)
+    T, H = _dims(x, "x", 2)
+    k = _dims(topk_idx, "topk_idx", 2)[1]
+    G, n, _ = _dims(w1, "w1", 3)
+    inner = n // 2
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    u8, f32, bf = torch.uint8, torch.float32, torch.bfloat16
+    _check(load_library().dg_moe_experts_fp8(
+        _arg(x, "x", bf, (T, H), dev), _arg(topk_idx, "topk_idx", torch.int32, (T, k), dev), _arg(topk_w, "topk_w", f32, (T, k), dev),
+        _arg(w1, "w1", u8, (G, 2 * inner, H), dev), _arg(s1, "s1", f32, (G, 2 * inner // 128, H // 128), dev),
+        _arg(w2, "w2", u8, (G, H, inner), dev), _arg(s2, "s2", f32, (G, H // 128, inner // 128), dev), _arg(y, "y", bf, (T, H), dev), T, k,
+        first_expert, G, H, inner, ws, ws_bytes, _raw_stream(stream, dev)))
+
+
+def dg_moe_experts_mxfp4(x, topk_idx, topk_w, w1, s1, w2, s2, y, first_expert=0, workspace=None, stream=None):
+    """dg_moe_experts_fp8 with weights in microscaled 4-bit floats: w1 [G,2I,H/2] and w2 [G,H,I/2] packed e2m1 (uint8), s1
+    [G,H/128,2I] and s2 [G,I/128,H] int32 (dg_quant_mxfp4)."""
+    dev = torch.cuda.current_device()
+    T, H = _dims(x, "x", 2)
+    k = _dims(topk_idx, "topk_idx", 2)[1]
+    G, n, _ = _dims(w1, "w1", 3)
+    inner = n // 2
+    ws, ws_bytes = _ws_arg(workspace, dev)
+    u8, i32, bf = torch.uint8, torch.int32, torch.bfloat16
+    _check(load_library().dg_moe_experts_mxfp4(
+        _arg(x, "x", bf, (T, H), dev), _arg(topk_idx, "topk_idx", i32, (T, k), dev), _arg(topk_w, "topk_w", torch.float32, (T, k), dev),
+        _arg(w1, "w1", u8, (G, 2 * inner, H // 2), dev), _arg(s1, "s1", i32, (G, H // 128, 2 * inner), dev),
+        _arg(w2, "w2", u8, (G, H, inner // 2), dev), _arg(s2, "s2", i32, (G, inner // 128, H), dev), _arg(y, "y", bf, (T, H), dev), T, k,
+        first_expert, G, H, inner, ws, ws_bytes, _raw_stream(stream, dev)))

@@ -108,3 +108,30 @@ def test_activation_names():
     assert [dg._act_arg(a) for a in ("none", "relu", "silu", "gelu", "gelu_tanh")] == [0, 1, 2, 3, 4] and dg._act_arg(dg.DG_ACT_GELU) == 3
     with pytest.raises(ValueError, match="gelu_tanh"):
         dg._act_arg("swish")
+
+
+def _experts(lib, name, x=P, idx=P, w=P, w1=P, s1=P, w2=P, s2=P, y=P, T=4, k=2, first=0, G=8, H=256, I=128, ws=None, n=0):
+    return getattr(lib, name)(x, idx, w, w1, s1, w2, s2, y, T, k, first, G, H, I, ws, n, NULL)
+
+
+@pytest.mark.parametrize("name", ["dg_moe_experts_fp8", "dg_moe_experts_mxfp4"])
+def test_experts(lib, name):
+    for kw, want, text in [
+        (dict(T=65), S, "T"), (dict(T=-1), S, "T"), (dict(k=0), S, "k"), (dict(k=17), S, "k"), (dict(G=0), S, "G"), (dict(G=1025), S, "G"),
+        (dict(first=-1), S, "first_expert"), (dict(first=(1 << 31) - 4), S, "first_expert"), (dict(H=192), S, "H"), (dict(H=0), S, "H"),
+        (dict(I=64), S, "I"), (dict(I=32896), S, "I"), (dict(x=None), V, "null"), (dict(idx=None), V, "null"), (dict(w=None), V, "null"),
+        (dict(w1=None), V, "null"), (dict(s1=None), V, "null"), (dict(w2=None), V, "null"), (dict(s2=None), V, "null"), (dict(y=None), V, "null"),
+        (dict(x=P + 8), A, "16"), (dict(w1=P + 4), A, "16"), (dict(w2=P + 8), A, "16"), (dict(y=P + 2), A, "16"), (dict(idx=P + 2), A, "4"),
+        (dict(w=P + 1), A, "4"), (dict(s1=P + 2), A, "4"), (dict(s2=P + 2), A, "4"),
+    ]:
+        _expect(lib, _experts(lib, name, **kw), want, text)
+    _expect(lib, _experts(lib, name, T=0, x=None, y=None), OK)
+
+
+def test_experts_workspace(lib):
+    size = dg.dg_get_workspace_size
+    for H, inner in ((256, 128), (1024, 512), (7168, 2048), (32768, 128)):
+        got = [size(dg.DG_OP_MOE_EXPERTS, n, H, inner) for n in (1, 2, 8, 64, 512, 1024)]
+        assert got == sorted(got) and got[0] >= 4096 + 2 * inner and got[-1] >= 4096 + 2048 * inner
+    for bad in ((1025, 256, 128), (-1, 256, 128), (8, 200, 128), (8, 256, 0)):
+        assert size(dg.DG_OP_MOE_EXPERTS, *bad) == 0
