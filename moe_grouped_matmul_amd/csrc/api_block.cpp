@@ -41,8 +41,10 @@ int check_partials(const void* ws, size_t ws_bytes, size_t need) {
   return DG_OK;
 }
 
+constexpr size_t kTableBytes = (sizeof(ExpertsTable) + 255) / 256 * 256;
+
 size_t experts_bytes(int64_t choices, int64_t T, int64_t H, int64_t I, int splits) {
-  return kBlockWsCounterBytes + experts_h_bytes(choices, I) + (splits > 1 ? (size_t)splits * (size_t)H * (size_t)T * 4 : 0);
+  return kBlockWsCounterBytes + kTableBytes + experts_h_bytes(choices, I) + (splits > 1 ? (size_t)splits * (size_t)H * (size_t)T * 4 : 0);
 }
 
 bool experts_dim(int64_t d) { return d > 0 && d % 128 == 0 && d <= kExpertsMaxDim; }
@@ -64,7 +66,7 @@ int run_experts(bool fp4, const uint16_t* x, const int32_t* topk_idx, const floa
     return fail(DG_ERR_ALIGN, "topk_idx, topk_w and scales must be 4-byte aligned");
   int cus = 0, rc = check_device(&cus);
   if (rc) return rc;
-  const int splits = experts_splits(T * k, H, I, G, effective_cus(cus));
+  const int splits = experts_splits(T, T * k, H, I, G, effective_cus(cus));
   const size_t need = experts_bytes(T * k, T, H, I, splits);
   if (!ws || !aligned(ws, 16) || ws_bytes < need)
     return fail(DG_ERR_WORKSPACE, "a 16-byte aligned workspace of at least %zu bytes is needed", need);
@@ -78,8 +80,9 @@ int run_experts(bool fp4, const uint16_t* x, const int32_t* topk_idx, const floa
   p.w2 = w2;
   p.s2 = s2;
   p.y = y;
-  p.h = reinterpret_cast<uint16_t*>(base);
-  p.partials = reinterpret_cast<float*>(base + experts_h_bytes(T * k, I));
+  p.table = reinterpret_cast<ExpertsTable*>(base);
+  p.h = reinterpret_cast<uint16_t*>(base + kTableBytes);
+  p.partials = reinterpret_cast<float*>(base + kTableBytes + experts_h_bytes(T * k, I));
   p.counters = static_cast<unsigned int*>(ws);
   p.T = (int)T;
   p.k = (int)k;
@@ -90,7 +93,7 @@ int run_experts(bool fp4, const uint16_t* x, const int32_t* topk_idx, const floa
   p.splits = splits;
   // weights that the 256 MB Infinity Cache cannot hold from one call to the next are streamed past it
   const bool stream_weights = G * 3 * H * I / (fp4 ? 2 : 1) >= (int64_t)256 << 20;
-  return launched(launch_moe_experts(p, fp4, stream_weights, hs(stream)));
+  return launched(launch_moe_experts(p, fp4, stream_weights, effective_cus(cus), hs(stream)));
 }
 
 float* partials_of(void* ws) { return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kBlockWsCounterBytes); }
@@ -115,7 +118,8 @@ size_t block_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int cus)
   } else if (op == DG_OP_MOE_EXPERTS) {
     if (rows > kExpertsMaxChoices || !experts_dim(N) || !experts_dim(K)) return 0;
     const int64_t tokens = rows < kExpertsMaxTokens ? rows : kExpertsMaxTokens;  // k may be 1
-    need = experts_bytes(rows, tokens, N, K, experts_splits(rows, N, K, kExpertsMaxGroups, cus));
+    // (as many tokens as choices, whose workgroups are the smaller and so the more)
+    need = experts_bytes(rows, tokens, N, K, experts_splits(kExpertsMaxTokens, rows, N, K, kExpertsMaxGroups, cus));
   }
   return (need + 15) / 16 * 16;
 }

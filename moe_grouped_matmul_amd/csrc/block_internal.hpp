@@ -71,6 +71,13 @@ constexpr int kExpertsMaxTopK = 16;
 constexpr int kExpertsMaxChoices = kExpertsMaxTokens * kExpertsMaxTopK;
 constexpr int kExpertsMaxGroups = 1024;
 constexpr int kExpertsMaxDim = 32768;  // H and I: a wave's quarter of a row is at most 64 steps of 128
+// The choices by expert, as the first kernel leaves them for the second in the workspace
+struct ExpertsTable {
+  int n;                                // chosen experts
+  uint32_t run[kExpertsMaxChoices];     // of each: number, tokens and first entry
+  uint32_t entry[kExpertsMaxChoices];   // token << 16 | choice whose row of h is the token's
+  float weight[kExpertsMaxChoices];
+};
 struct ExpertsParams {
   const uint16_t* x;     // [T][H] bf16
   const int32_t* idx;    // [T][k]
@@ -81,13 +88,14 @@ struct ExpertsParams {
   const void* s2;
   uint16_t* y;           // [T][H] bf16
   uint16_t* h;           // [T k][I] bf16
+  ExpertsTable* table;
   float* partials;       // [H / 16][splits][T][16], splits > 1
   unsigned int* counters;
   int T, k, first, G, H, I;
   int splits;
 };
-int experts_splits(int64_t choices, int64_t H, int64_t I, int64_t G, int cus);
+int experts_splits(int64_t T, int64_t choices, int64_t H, int64_t I, int64_t G, int cus);
 size_t experts_h_bytes(int64_t choices, int64_t I);
-hipError_t launch_moe_experts(const ExpertsParams& p, bool fp4, bool stream_weights, hipStream_t stream);
+hipError_t launch_moe_experts(const ExpertsParams& p, bool fp4, bool stream_weights, int cus, hipStream_t stream);
 
 }  // namespace dg

@@ -9,8 +9,14 @@
 //
 // Bound by the weights of the experts that were chosen, which are read once,
 // straight into registers: no two waves share a weight, so staging them in LDS
-// would only add a hop.  16 weight rows are the matrix cores' row operand and up
-// to 16 tokens the column operand, so one token costs what sixteen do.
+// would only add a hop.  An instruction loads whole cache lines, 8 rows of 128
+// bytes, streamed past the caches (8 rows x 128 bytes 6.3 TB/s of 224 MB,
+// 16 rows x 64 bytes, where a line is taken in two halves, 5.1).  So a lane has
+// 16 bytes (a chunk) of one of 8 rows, row lane % 8, chunk lane / 16 + 4 (lane /
+// 8 % 2), and the matrix cores' 16 x 16 product takes the 8 rows twice, in its
+// upper and lower half with different chunks; 8 tokens are its columns, twice
+// too.  The products of unlike halves are of no use, those of like halves are
+// two sums over K that meet at the end: one token costs what eight do.
 
 #include "activation.hpp"
 #include "block_internal.hpp"
@@ -20,6 +26,7 @@ namespace dg {
 namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr uint32_t kOOB = 0xFFFFFF00u;  // an offset past every buffer range used here
@@ -32,40 +39,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* p, uint3
 
 enum Format { kFp8 = 0, kFp4 = 1 };
 
-// A lane's 32 consecutive weights of one row (a quarter of a 128-deep step)
+// The t-th 8 weights of a lane's chunk as bf16: of 16 e4m3 as they are (t < 2), of 32 e2m1 times the power of two `scale` (t < 4)
 template <int FMT>
-struct Weights {
-  u32x4 v[FMT == kFp8 ? 2 : 1];
-};
-
-template <int FMT, bool NT>
-__device__ __forceinline__ Weights<FMT> load_weights(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t step) {
-  Weights<FMT> w;
-  if constexpr (FMT == kFp8) {
-    w.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r, off, step * 128u, NT ? kStream : 0);
-    w.v[1] = __builtin_amdgcn_raw_buffer_load_b128(r, off + 16u, step * 128u, NT ? kStream : 0);
-  } else {
-    w.v[0] = __builtin_amdgcn_raw_buffer_load_b128(r, off, step * 64u, NT ? kStream : 0);
-  }
-  return w;
-}
-
-// The i-th 8 of them as bf16.  e4m3 as it is; e2m1 times the power of two in byte 0 of `code`.
-template <int FMT>
-__device__ __forceinline__ bf16x8 widened(const Weights<FMT>& w, int i, float scale) {
+__device__ __forceinline__ bf16x8 widened(u32x4 w, int t, float scale) {
   typedef __bf16 bf16x2_ __attribute__((ext_vector_type(2)));
   union {
     bf16x8 v;
     bf16x2_ p[4];
   } r;
   if constexpr (FMT == kFp8) {
-    const int a = (int)w.v[i >> 1][2 * (i & 1)], b = (int)w.v[i >> 1][2 * (i & 1) + 1];
+    const int a = (int)w[2 * t], b = (int)w[2 * t + 1];
     r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false);
     r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true);
     r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false);
     r.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true);
   } else {
-    const uint32_t a = w.v[0][i];
+    const uint32_t a = w[t];
     r.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 0);
     r.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 1);
     r.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, scale, 2);
@@ -73,257 +62,69 @@ __device__ __forceinline__ bf16x8 widened(const Weights<FMT>& w, int i, float sc
   }
   return r.v;
 }
+template <int FMT>
+constexpr int kParts = FMT == kFp8 ? 2 : 4;  // 8-deep parts of a chunk: products of a step, and 16-byte loads of its activations
+template <int FMT>
+constexpr uint32_t kStepDepth = FMT == kFp8 ? 128 : 256;  // weights of a row in a step's 128 bytes
 
 // fp32 whose exponent is byte q of a scale word (the conversion reads the exponent alone: 255 gives NaN, 0 2^-127)
 __device__ __forceinline__ float exponent_of(uint32_t word, int q) { return __uint_as_float(((word >> (8 * q)) & 0xffu) << 23); }
+
+// 16 bytes of each lane to where the products want them: loaded so that four neighbouring lanes have 64 consecutive bytes (row
+// lane / 8, chunk lane % 8, which the address unit takes as one access and not as four), used by the lane of row lane % 8 and
+// chunk lane / 16 + 4 (lane / 8 % 2)
+__device__ __forceinline__ u32x4 spread(int from, u32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
+  return v;
+}
+
+// the sum of both like halves of a product, in both
+__device__ __forceinline__ f32x4 halves(f32x4 v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += __shfl_xor(v[i], 40);
+  return v;
+}
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// ---- gate and up projection.  A workgroup takes 16 columns of h of one chosen expert (16 rows of the gate and of the up
-// weights), its four waves a quarter of H each.  The expert's choices share a pass over the weights, up to 32 of them (most
-// experts have few: 16 keep four steps in flight, 32 two).
-
-// the chosen experts of [first, first + G) as bits, and each choice's (-1: not here), in LDS
-struct Chosen {
-  uint32_t bits[kExpertsMaxGroups / 32];
-  int before[kExpertsMaxGroups / 32 + 1];  // experts before each word's
-  int16_t expert[kExpertsMaxChoices];
-};
-
-__device__ __forceinline__ void read_choices(const ExpertsParams& p, Chosen& s) {
-  const int n = p.T * p.k;
-  if (threadIdx.x < 32) s.bits[threadIdx.x] = 0;
-  __syncthreads();
-  for (int c = threadIdx.x; c < n; c += 256) {
-    const int64_t e = (int64_t)p.idx[c] - p.first;
-    const bool here = e >= 0 && e < p.G;
-    s.expert[c] = here ? (int16_t)e : -1;
-    if (here) atomicOr(&s.bits[e >> 5], 1u << (e & 31));
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {  // one wave
-    const int lane = threadIdx.x;
-    int v = lane < 32 ? __popc(s.bits[lane]) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up(v, o);
-      if (lane >= o) v += u;
-    }
-    if (lane == 0) s.before[0] = 0;
-    if (lane < 32) s.before[lane + 1] = v;
-  }
-  __syncthreads();
-}
-
-// the a-th chosen expert (a < s.before[32])
-__device__ __forceinline__ int nth_expert(const Chosen& s, int a) {
-  int lo = 0, hi = 31;  // the last word with before[] <= a
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.before[mid] <= a) lo = mid;
-    else hi = mid - 1;
-  }
-  uint32_t b = s.bits[lo];
-  for (int i = a - s.before[lo]; i > 0; --i) b &= b - 1;
-  return __builtin_amdgcn_readfirstlane(lo * 32 + __ffs(b) - 1);
-}
-
-// what the passes of a wave share
-struct UpWave {
-  const uint8_t* wbase;
-  const void* sbase;
-  uint32_t w_bytes, s_bytes;
-  uint32_t g_off, u_off;    // of the lane's gate and up row
-  float beta_g, beta_u;     // e4m3: block scales of the wave's steps, one to a lane
-  int lo, hi;               // steps
-  int i0, lane, wave, q, n16;
-};
-
-// rows [m0, m0 + 16 MG) of the expert's choices
-template <int FMT, int MG, bool NT>
-__device__ __forceinline__ void up_pass(const ExpertsParams& p, const UpWave& s, const int16_t* rows, int m, int m0,
-                                        f32x4 (*part)[4][64]) {
-  constexpr int D = MG == 1 ? 4 : 2;  // steps in flight
-  const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, (uint32_t)p.T * (uint32_t)p.H * 2u);
-  const uint32_t two_i = 2u * (uint32_t)p.I;
-  uint32_t x_off[MG];
-#pragma unroll
-  for (int g = 0; g < MG; ++g) {
-    const int r = m0 + 16 * g + s.n16;
-    x_off[g] = r < m ? (uint32_t)(rows[r] / p.k) * (uint32_t)p.H * 2u + 64u * s.q : kOOB;
-  }
-  Weights<FMT> wg[D], wu[D];
-  uint32_t sg[D], su[D];
-  u32x4 xr[D][MG][4];
-  f32x4 cg[MG], cu[MG];
-#pragma unroll
-  for (int g = 0; g < MG; ++g) cg[g] = cu[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // past the wave's last step the ranges are empty: zeros, and no traffic
-  auto load = [&](int d, int kb) {
-    const bool in = kb < s.hi;
-    const uint32_t k = in ? (uint32_t)kb : 0u;
-    const __amdgpu_buffer_rsrc_t rw = make_rsrc(s.wbase, in ? s.w_bytes : 0u);
-    const __amdgpu_buffer_rsrc_t ry = in ? rx : make_rsrc(p.x, 0u);
-    wg[d] = load_weights<FMT, NT>(rw, s.g_off, k);
-    wu[d] = load_weights<FMT, NT>(rw, s.u_off, k);
-    if constexpr (FMT == kFp4) {  // a word of four codes a row and step
-      const __amdgpu_buffer_rsrc_t rs = make_rsrc(s.sbase, in ? s.s_bytes : 0u);
-      sg[d] = __builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(s.i0 + s.n16) * 4u, k * 4u * two_i, 0);
-      su[d] = __builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(p.I + s.i0 + s.n16) * 4u, k * 4u * two_i, 0);
-    }
-#pragma unroll
-    for (int g = 0; g < MG; ++g)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        xr[d][g][t] = __builtin_amdgcn_raw_buffer_load_b128(ry, x_off[g] == kOOB ? kOOB : x_off[g] + 16u * t, k * 256u, 0);
-  };
-#pragma unroll
-  for (int d = 0; d < D; ++d) load(d, s.lo + d);
-  for (int k0 = s.lo; k0 < s.hi; k0 += D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
-      __builtin_amdgcn_sched_barrier(0);
-      const float eg = FMT == kFp4 ? exponent_of(sg[d], s.q) : 1.f, eu = FMT == kFp4 ? exponent_of(su[d], s.q) : 1.f;
-      bf16x8 ag[4], au[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        ag[t] = widened<FMT>(wg[d], t, eg);
-        au[t] = widened<FMT>(wu[d], t, eu);
-      }
-      const int i = k0 + d - s.lo;  // a lane's: a quarter of a row is at most 64 steps, and lanes past it hold zeros
-      const float bg = FMT == kFp8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s.beta_g), i)) : 1.f;
-      const float bu = FMT == kFp8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(s.beta_u), i)) : 1.f;
-#pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
-        f32x4 pg = FMT == kFp8 ? zero : cg[g], pu = FMT == kFp8 ? zero : cu[g];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          pg = mfma(ag[t], xr[d][g][t], pg);
-          pu = mfma(au[t], xr[d][g][t], pu);
-        }
-        if constexpr (FMT == kFp8) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            cg[g][v] = __builtin_fmaf(pg[v], bg, cg[g][v]);
-            cu[g][v] = __builtin_fmaf(pu[v], bu, cu[g][v]);
-          }
-        } else {
-          cg[g] = pg;
-          cu[g] = pu;
-        }
-      }
-      load(d, k0 + d + D);
-    }
-  }
-  // the waves' sums, in order
-  __syncthreads();  // (the last pass' reads of part are done)
-  if (s.wave > 0) {
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      part[s.wave - 1][2 * g][s.lane] = cg[g];
-      part[s.wave - 1][2 * g + 1][s.lane] = cu[g];
-    }
-  }
-  __syncthreads();
-  if (s.wave > 0) return;
-#pragma unroll
-  for (int g = 0; g < MG; ++g) {
-#pragma unroll
-    for (int o = 0; o < 3; ++o) {
-      cg[g] += part[o][2 * g][s.lane];
-      cu[g] += part[o][2 * g + 1][s.lane];
-    }
-    float v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = activate<kActSilu>(cg[g][j]) * cu[g][j];
-    const int r = m0 + 16 * g + s.n16;
-    if (r < m)
-      *reinterpret_cast<uint2*>(p.h + (int64_t)rows[r] * p.I + s.i0 + 4 * s.q) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  }
-}
-
-template <int FMT, bool NT>
-__global__ void __launch_bounds__(256) experts_up_kernel(ExpertsParams p) {
-  __shared__ Chosen s;
-  __shared__ int16_t rows[kExpertsMaxChoices];
-  __shared__ int n_rows;
-  __shared__ __attribute__((aligned(16))) f32x4 part[3][4][64];
-  const int H = p.H, I = p.I;
-  const int tiles = I >> 4;
-  const int a = (int)blockIdx.x / tiles;
-  UpWave u;
-  u.i0 = ((int)blockIdx.x - a * tiles) * 16;
-  u.lane = threadIdx.x & 63;
-  u.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  u.q = u.lane >> 4;
-  u.n16 = u.lane & 15;
-  if (threadIdx.x == 0) n_rows = 0;
-  read_choices(p, s);
-  if (a >= s.before[kExpertsMaxGroups / 32]) return;  // fewer experts were chosen than could be
-  const int e = nth_expert(s, a);
-  for (int c = threadIdx.x; c < p.T * p.k; c += 256)  // (which column of the products a choice takes does not matter)
-    if (s.expert[c] == e) rows[atomicAdd(&n_rows, 1)] = (int16_t)c;
-  __syncthreads();
-  const int m = __builtin_amdgcn_readfirstlane(n_rows);
-
-  const int KB = H >> 7;
-  const int per = (KB + 3) >> 2;
-  u.lo = u.wave * per < KB ? u.wave * per : KB;
-  u.hi = u.lo + per < KB ? u.lo + per : KB;
-  const uint32_t row_bytes = FMT == kFp8 ? (uint32_t)H : (uint32_t)H / 2;
-  u.w_bytes = 2u * (uint32_t)I * row_bytes;
-  u.wbase = p.w1 + (int64_t)e * u.w_bytes;
-  u.g_off = (uint32_t)(u.i0 + u.n16) * row_bytes + (FMT == kFp8 ? 32u * u.q : 16u * u.q);
-  u.u_off = u.g_off + (uint32_t)I * row_bytes;
-  u.beta_g = u.beta_u = 0.f;
-  u.s_bytes = FMT == kFp8 ? 0u : (uint32_t)KB * 2u * (uint32_t)I * 4u;
-  u.sbase = FMT == kFp8 ? p.s1 : static_cast<const int32_t*>(p.s1) + (int64_t)e * KB * 2 * I;
-  if constexpr (FMT == kFp8) {
-    const float* b = static_cast<const float*>(p.s1) + (int64_t)e * (I >> 6) * KB;  // [2 I / 128][KB]
-    if (u.lo + u.lane < u.hi) {
-      u.beta_g = b[(int64_t)(u.i0 >> 7) * KB + u.lo + u.lane];
-      u.beta_u = b[(int64_t)((I + u.i0) >> 7) * KB + u.lo + u.lane];
-    }
-  }
-  int m0 = 0;
-  for (; m - m0 > 16; m0 += 32) up_pass<FMT, 2, NT>(p, u, rows, m, m0, part);
-  if (m0 < m) up_pass<FMT, 1, NT>(p, u, rows, m, m0, part);
-}
-
-// ---- down projection and weighted sum.  A workgroup takes 16 columns of y for all tokens; its eight waves, and those of all
-// p.splits workgroups of the columns, take equal runs of the 128-deep steps of all chosen experts, one expert after the other,
-// with the next steps' loads in flight across experts.  The tokens of an expert share its steps, 16 at a time; a product goes
-// into the accumulator times its block scale and the token's weight, and from there, when the expert (or its 16 tokens) change,
-// into the wave's sums of the tokens in LDS, so that a token's experts are added in the order of their numbers.
+// ---- who chose what.  Every workgroup of the first kernel sorts the choices by expert; its first leaves the result for the second.
 struct Members {
-  int16_t expert[kExpertsMaxChoices];   // of each choice, -1: not here
-  int count[kExpertsMaxGroups];         // tokens of each expert
-  int16_t rank[kExpertsMaxGroups];      // of a chosen expert among the chosen
-  int16_t list[kExpertsMaxGroups];      // chosen experts
-  int16_t start[kExpertsMaxGroups + 1]; // first of its entries below
-  int16_t group[kExpertsMaxGroups + 1]; // groups of 16 tokens before it
-  int16_t choice[kExpertsMaxChoices];   // entries: a choice whose row of h is the token's, and its weight
+  int16_t expert[kExpertsMaxChoices];  // of each choice, -1: not here
   float weight[kExpertsMaxChoices];
-  int n;                                // chosen experts
+  int count[kExpertsMaxGroups];        // tokens of each expert
+  int start[kExpertsMaxGroups];        // its first entry
+  ExpertsTable table;
 };
+// a chosen expert's number, tokens and first entry in one word
+__device__ __forceinline__ uint32_t run_word(int expert, int count, int start) {
+  return (uint32_t)expert | (uint32_t)(count - 1) << 10 | (uint32_t)start << 16;
+}
+__device__ __forceinline__ int expert_of(uint32_t r) { return (int)(r & 1023u); }
+__device__ __forceinline__ int count_of(uint32_t r) { return (int)((r >> 10) & 63u) + 1; }
+__device__ __forceinline__ int start_of(uint32_t r) { return (int)(r >> 16); }
+static_assert(kExpertsMaxGroups <= 1024 && kExpertsMaxTokens <= 64 && kExpertsMaxChoices <= 65536, "the words of the table");
+
+constexpr int kUpThreads = 256;
 
 __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s) {
+  constexpr int EACH = kExpertsMaxChoices / kUpThreads;
   const int n = p.T * p.k;
-  for (int e = threadIdx.x; e < p.G; e += 512) s.count[e] = 0;
-  for (int c = threadIdx.x; c < n; c += 512) {
+  for (int e = threadIdx.x; e < p.G; e += kUpThreads) s.count[e] = 0;
+  for (int c = threadIdx.x; c < n; c += kUpThreads) {
     const int64_t e = (int64_t)p.idx[c] - p.first;
     s.expert[c] = e >= 0 && e < p.G ? (int16_t)e : -1;
+    s.weight[c] = p.w[c];
   }
   __syncthreads();
   // a token that names an expert twice is one entry, of the first of the choices, with the sum of their weights
-  int mine[kExpertsMaxChoices / 512], place[kExpertsMaxChoices / 512];
-  float w[kExpertsMaxChoices / 512];
+  int mine[EACH], place[EACH];
+  float w[EACH];
 #pragma unroll
-  for (int i = 0; i < kExpertsMaxChoices / 512; ++i) {
-    const int c = threadIdx.x + 512 * i;
+  for (int i = 0; i < EACH; ++i) {
+    const int c = threadIdx.x + kUpThreads * i;
     mine[i] = -1;
     place[i] = 0;
     w[i] = 0.f;
@@ -335,20 +136,20 @@ __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s)
     for (int j = t0; j < t0 + p.k; ++j)
       if (s.expert[j] == e) {
         if (j < c) first = false;
-        else w[i] += p.w[j];
+        else w[i] += s.weight[j];
       }
     if (!first) continue;
     mine[i] = e;
-    place[i] = atomicAdd(&s.count[e], 1);  // (which column a token takes does not matter)
+    place[i] = atomicAdd(&s.count[e], 1);  // (which column of the products a token takes does not matter)
   }
   __syncthreads();
-  if (threadIdx.x < 64) {  // one wave: ranks, and sums over the chosen experts of their tokens and groups
+  if (threadIdx.x < 64) {  // one wave: the chosen experts in order
     const int lane = threadIdx.x;
-    int chosen = 0, tokens = 0, groups = 0;
+    int chosen = 0, tokens = 0;
     for (int e0 = 0; e0 < p.G; e0 += 64) {
       const int e = e0 + lane;
       const int m = e < p.G ? s.count[e] : 0;
-      int v = m | (((m + 15) >> 4) << 16);  // both sums at once: at most 1024 tokens and 1024 groups
+      int v = m;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int u = __shfl_up(v, o);
@@ -356,176 +157,526 @@ __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s)
       }
       const unsigned long long mask = __ballot(m > 0);
       if (m > 0) {
-        const int a = chosen + __popcll(mask & ((1ull << lane) - 1));
-        s.rank[e] = (int16_t)a;
-        s.list[a] = (int16_t)e;
-        s.start[a] = (int16_t)(tokens + (v & 0xffff) - m);
-        s.group[a] = (int16_t)(groups + (v >> 16) - ((m + 15) >> 4));
+        s.start[e] = tokens + v - m;
+        s.table.run[chosen + __popcll(mask & ((1ull << lane) - 1))] = run_word(e, m, tokens + v - m);
       }
       chosen += __popcll(mask);
-      const int all = __shfl(v, 63);
-      tokens += all & 0xffff;
-      groups += all >> 16;
+      tokens += __shfl(v, 63);
     }
-    if (lane == 0) {
-      s.n = chosen;
-      s.start[chosen] = (int16_t)tokens;
-      s.group[chosen] = (int16_t)groups;
-    }
+    if (lane == 0) s.table.n = chosen;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kExpertsMaxChoices / 512; ++i)
+  for (int i = 0; i < EACH; ++i)
     if (mine[i] >= 0) {
-      const int at = s.start[s.rank[mine[i]]] + place[i];
-      s.choice[at] = (int16_t)(threadIdx.x + 512 * i);
-      s.weight[at] = w[i];
+      const int c = threadIdx.x + kUpThreads * i, at = s.start[mine[i]] + place[i];
+      s.table.entry[at] = (uint32_t)c | (uint32_t)(c / p.k) << 16;
+      s.table.weight[at] = w[i];
     }
   __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < n; i += kUpThreads) {  // (what lies past the experts and entries is not looked at)
+      p.table->run[i] = s.table.run[i];
+      p.table->entry[i] = s.table.entry[i];
+      p.table->weight[i] = s.table.weight[i];
+    }
+    if (threadIdx.x == 0) p.table->n = s.table.n;
+  }
 }
 
-template <int FMT, bool NT>
-__global__ void __launch_bounds__(512) experts_down_kernel(ExpertsParams p) {
-  constexpr int D = 3;  // steps in flight
-  constexpr int W = 8;
-  __shared__ Members s;
-  __shared__ __attribute__((aligned(16))) f32x4 sums[W][kExpertsMaxTokens * 4];  // [token][quarter of the columns]
-  __shared__ int last;
+// ---- gate and up projection.  A unit is 16 columns of h of one chosen expert (16 rows of the gate and of the up weights); a
+// workgroup takes every so-manyth unit, its four waves a quarter of H each, and the next unit's first steps are in flight while
+// the current one ends.  An expert's tokens share a pass over the weights, up to 8 MAXMG of them.
+
+// steps in flight: (weights and activations of) a step take 16 + 8 registers for every 8 tokens of e4m3, 20 + 16 of e2m1, and the
+// accumulators 16 for every 8 tokens
+template <int FMT>
+constexpr int up_depth(int mg, int maxmg) {
+  if (FMT == kFp8) return maxmg == 2 ? 2 : mg == 1 ? 4 : mg == 2 ? 3 : 2;
+  return maxmg == 2 ? (mg == 1 ? 3 : 1) : (mg == 1 ? 2 : 1);
+}
+
+struct UpShared {
+  Members members;
+  __attribute__((aligned(16))) f32x4 part[2][3][16][16];  // [turn][wave - 1][accumulator][lane]
+};
+
+// A pass of 8 MG tokens, from m0 on, of unit u (all uniform)
+struct UpItem {
+  int u, m0;
+  int expert, start, m, i0;
+};
+__device__ __forceinline__ UpItem up_item(const Members& s, int u, int m0, int tiles) {
+  UpItem r;
+  const int a = u / tiles;
+  const uint32_t w = __builtin_amdgcn_readfirstlane(s.table.run[a]);
+  r.u = u;
+  r.m0 = m0;
+  r.expert = expert_of(w);
+  r.start = start_of(w);
+  r.m = count_of(w);
+  r.i0 = (u - a * tiles) * 16;
+  return r;
+}
+// groups of 8 that share the pass: 1, 2 or 4
+template <int MAXMG>
+__device__ __forceinline__ int up_groups(const UpItem& it) {
+  const int left = it.m - it.m0;
+  return left > 8 * 2 && MAXMG > 2 ? 4 : left > 8 ? 2 : 1;
+}
+
+// the passes of this workgroup from `it` on, as long as they are of MG groups; returns whether one is left, which is in `it`
+template <int FMT, int MG, int MAXMG, bool NT>
+__device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared& sh, UpItem& it, int units, int stride, int& turn) {
+  constexpr int D = up_depth<FMT>(MG, MAXMG);
+  constexpr int P = kParts<FMT>;
+  const Members& s = sh.members;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int q = lane >> 4, n16 = lane & 15;
-  const int H = p.H, I = p.I;
-  const int tile = (int)blockIdx.x / p.splits, split = (int)blockIdx.x - tile * p.splits;
-  const int c0 = tile * 16;
-  for (int i = lane; i < p.T * 4; i += 64) sums[wave][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  read_members(p, s);
-  const int KB = I >> 7;
-  const int chosen = __builtin_amdgcn_readfirstlane(s.n);
-  const int steps = chosen * KB;  // (a step of all of an expert's groups: which of them a token is in changes no sum)
-  const int slots = W * p.splits;
+  const int r8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
+  const uint32_t H = (uint32_t)p.H, I = (uint32_t)p.I;
+  const int tiles = p.I >> 4;
+  const uint32_t row_bytes = FMT == kFp8 ? H : H / 2;
+  const uint32_t w_bytes = 2u * I * row_bytes;
+  const int KB = p.H >> 7;
+  const uint32_t s_bytes = FMT == kFp8 ? (I >> 6) * (uint32_t)KB * 4u : (uint32_t)KB * 2u * I * 4u;
+  // this wave's steps [lo, lo + n) of a row, `per` a wave, padded to whole turns of the stages with empty ones
+  const int steps = (int)((row_bytes + 127) >> 7);
+  const int per = (steps + 3) >> 2;
+  const int lo = wave * per;
+  const int n = lo >= steps ? 0 : steps - lo < per ? steps - lo : per;
+  const int padded = (per + D - 1) / D * D;
+  // loads: row (or token) lane / 8, chunk lane % 8; weight rows 2 (lane / 8) + a: neighbours, whose scale words are loaded together
+  const int l8 = lane >> 3, ch = lane & 7;
+  const int from = 4 * (8 * r8 + q + 4 * half);
+  uint32_t w_off[2];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(2 * l8 + a) * row_bytes + 16u * ch;
+  const uint32_t s_off = (half * 2 * I + 2 * r8) * 4u;
+
+  // a pass' own: where its weights and tokens are, and the block scales of the wave's steps, one to a lane (e4m3)
+  struct Own {
+    bool there;
+    int expert, i0;
+    uint32_t x_off[MG];
+    float beta[2];
+  };
+  auto own_of = [&](const UpItem& t, bool there) {
+    Own o;
+    o.there = there;
+    o.expert = there ? t.expert : 0;
+    o.i0 = t.i0;
+#pragma unroll
+    for (int g = 0; g < MG; ++g) {
+      const int r = t.m0 + 8 * g + l8;
+      o.x_off[g] = there && r < t.m ? (s.table.entry[t.start + r] >> 16) * H * 2u + 16u * P * ch : kOOB;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      o.beta[b] = 0.f;
+      if constexpr (FMT == kFp8) {  // [2 I / 128][KB] fp32
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(static_cast<const uint8_t*>(p.s1) + (int64_t)o.expert * s_bytes, there ? s_bytes : 0u);
+        o.beta[b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            r, lane < n ? (uint32_t)(lo + lane) * 4u : kOOB, (uint32_t)((b * p.I + o.i0) >> 7) * (uint32_t)KB * 4u, 0));
+      }
+    }
+    return o;
+  };
+
+  u32x4 w[D][2][2];
+  u32x2 sc[D][2];
+  u32x4 xr[D][MG][P];
+  // step i of a pass into stage d; empty ranges past its last step: zeros, and no traffic; so are the upper chunks of a last
+  // half step of e2m1
+  auto load = [&](int d, const Own& o, int i) {
+    const bool in = o.there && i < n;
+    const uint32_t k = in ? (uint32_t)(lo + i) : 0u;
+    const bool over = FMT == kFp4 && (k + 1) * 256u > H;
+    const bool cut = over && ch >= 4;
+    const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w1 + (int64_t)o.expert * w_bytes, in ? w_bytes : 0u);
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, in ? (uint32_t)p.T * H * 2u : 0u);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+        w[d][b][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], (b * I + (uint32_t)o.i0) * row_bytes + k * 128u, NT ? kStream : 0);
+    if constexpr (FMT == kFp4) {  // the words of step k are 2 k and 2 k + 1 of a row
+      const __amdgpu_buffer_rsrc_t rs = make_rsrc(static_cast<const uint8_t*>(p.s1) + (int64_t)o.expert * s_bytes, in ? s_bytes : 0u);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        sc[d][b] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
+    }
+#pragma unroll
+    for (int g = 0; g < MG; ++g)
+#pragma unroll
+      for (int t = 0; t < P; ++t)
+        xr[d][g][t] = __builtin_amdgcn_raw_buffer_load_b128(rx, cut || o.x_off[g] == kOOB ? kOOB : o.x_off[g] + 16u * t, k * 2u * kStepDepth<FMT>, 0);
+  };
+
+  Own cur = own_of(it, true);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, cur, d);
+  for (;;) {
+    UpItem next = it;
+    bool left = true;
+    if (it.m0 + 8 * MG < it.m) next.m0 += 8 * MG;
+    else if (it.u + stride < units) next = up_item(s, it.u + stride, 0, tiles);
+    else left = false;
+    const bool on = left && up_groups<MAXMG>(next) == MG;
+    const Own then = own_of(next, on);
+    f32x4 c[2][2][MG];
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int g = 0; g < MG; ++g) c[b][a][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < padded; k0 += D) {
+      const bool ahead = k0 + D >= padded;  // the loads of this turn are the next pass'
+      Own o = cur;
+      if (ahead) o = then;
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        __builtin_amdgcn_sched_barrier(0);
+        // a lane's: a wave has at most 64 steps, and past them lanes hold zero, or the step's products are zero
+        const int i = k0 + d < 63 ? k0 + d : 63;
+        u32x4 y[MG][P];
+#pragma unroll
+        for (int g = 0; g < MG; ++g)
+#pragma unroll
+          for (int t = 0; t < P; ++t) y[g][t] = spread(from, xr[d][g][t]);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const float beta = FMT == kFp8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cur.beta[b]), i)) : 1.f;
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            const float ex = FMT == kFp4 ? exponent_of(sc[d][b][a], q) : 1.f;
+            const u32x4 chunk = spread(from, w[d][b][a]);
+            bf16x8 v[P];
+#pragma unroll
+            for (int t = 0; t < P; ++t) v[t] = widened<FMT>(chunk, t, ex);
+#pragma unroll
+            for (int g = 0; g < MG; ++g) {
+              f32x4 z = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a][g];
+#pragma unroll
+              for (int t = 0; t < P; ++t) z = mfma(v[t], y[g][t], z);
+              if constexpr (FMT == kFp8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[b][a][g][e] = __builtin_fmaf(z[e], beta, c[b][a][g][e]);
+              } else {
+                c[b][a][g] = z;
+              }
+            }
+          }
+        }
+        load(d, o, ahead ? d : k0 + D + d);
+      }
+    }
+    // the waves' sums, in order; lanes (token r8, q < 2) of the lower half have weight rows 8 q + 2 e + a
+    const int at = r8 | (q << 3);
+    const bool mine = !half && q < 2;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int g = 0; g < MG; ++g) {
+          c[b][a][g] = halves(c[b][a][g]);
+          if (wave > 0 && mine) sh.part[turn][wave - 1][(g * 2 + b) * 2 + a][at] = c[b][a][g];
+        }
+    __syncthreads();  // (the other half of `part` is what the next pass writes)
+    if (wave == 0 && mine) {
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+        const int r = it.m0 + 8 * g + r8;
+        float v[8];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          f32x4 z[2] = {c[0][a][g], c[1][a][g]};
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int u = 0; u < 3; ++u) z[b] += sh.part[turn][u][(g * 2 + b) * 2 + a][at];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[2 * e + a] = activate<kActSilu>(z[0][e]) * z[1][e];
+        }
+        if (r < it.m)
+          *reinterpret_cast<uint4*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 8 * q) =
+              uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+      }
+    }
+    turn ^= 1;
+    it = next;
+    if (!on) return left;
+    cur = then;
+  }
+}
+
+template <int FMT, int MAXMG, bool NT>
+__global__ void __launch_bounds__(kUpThreads) experts_up_kernel(ExpertsParams p) {
+  __shared__ UpShared sh;
+  read_members(p, sh.members);
+  // as many workgroups as give each the same number of units, or one less
+  const int tiles = p.I >> 4;
+  const int units = __builtin_amdgcn_readfirstlane(sh.members.table.n) * tiles;
+  if (units == 0) return;
+  const int rounds = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int stride = (units + rounds - 1) / rounds;
+  if ((int)blockIdx.x >= stride) return;
+  UpItem it = up_item(sh.members, (int)blockIdx.x, 0, tiles);
+  int turn = 0;
+  for (bool left = true; left;) {
+    const int g = up_groups<MAXMG>(it);
+    if (g == 1) left = up_passes<FMT, 1, MAXMG, NT>(p, sh, it, units, stride, turn);
+    else if (g == 2) left = up_passes<FMT, 2, MAXMG, NT>(p, sh, it, units, stride, turn);
+    else if constexpr (MAXMG > 2) left = up_passes<FMT, 4, MAXMG, NT>(p, sh, it, units, stride, turn);
+  }
+}
+
+// ---- down projection and weighted sum.  A workgroup takes 16 columns of y for all tokens; its waves, and those of all
+// p.splits workgroups of the columns, take equal runs of the steps of all chosen experts, one expert after the other, with the
+// next steps' loads in flight across experts.  The tokens of an expert share its steps, 8 MG at a time (one group).  When the
+// group changes, the accumulators times the tokens' weights are added to the wave's sums of the tokens in LDS, so that a
+// token's experts are added in the order of their numbers.
+constexpr int kDownCols = 16;
+// waves of a workgroup: eight, two workgroups to a CU, where 8 tokens at most leave the registers for it; else four of twice the
+// registers
+template <bool FEW>
+constexpr int kDownWaves = FEW ? 8 : 4;
+
+// Steps in flight.  128 registers leave room for two workgroups of eight waves a CU, 256 for two of four.
+template <int FMT, bool FEW>
+constexpr int down_depth(int mg) {
+  if (FMT == kFp8) return FEW ? 4 : mg == 1 ? 5 : mg == 2 ? 3 : 2;
+  return FEW ? 2 : mg == 1 ? 3 : mg == 2 ? 2 : 1;
+}
+
+// the wave's part: its run of the steps, into its sums
+template <int FMT, int MG, bool FEW, bool NT>
+__device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTable& s, f32x4* sums, int c0, int slot, int slots) {
+  constexpr int D = down_depth<FMT, FEW>(MG);
+  constexpr int P = kParts<FMT>;
+  const int lane = threadIdx.x & 63;
+  const int r8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
+  const uint32_t H = (uint32_t)p.H, I = (uint32_t)p.I;
+  const uint32_t row_bytes = FMT == kFp8 ? I : I / 2;
+  const int KS = (int)((row_bytes + 127) >> 7);  // steps of an expert
+  const int steps = __builtin_amdgcn_readfirstlane(s.n) * KS;  // (a step of all of an expert's groups: which of them a token is in changes no sum)
   const int per = (steps + slots - 1) / slots;
-  const int lo = (split * W + wave) * per < steps ? (split * W + wave) * per : steps;
+  const int lo = slot * per < steps ? slot * per : steps;
   const int hi = lo + per < steps ? lo + per : steps;
 
-  const uint32_t row_bytes = FMT == kFp8 ? (uint32_t)I : (uint32_t)I / 2;
-  const uint32_t w_bytes = (uint32_t)H * row_bytes;
-  const uint32_t w_off = (uint32_t)(c0 + n16) * row_bytes + (FMT == kFp8 ? 32u * q : 16u * q);
-  // scales: e4m3 [ceil(H / 128)][KB] fp32, e2m1 words [KB][H]
-  const uint32_t s_bytes = FMT == kFp8 ? (uint32_t)((H + 127) >> 7) * (uint32_t)KB * 4u : (uint32_t)KB * (uint32_t)H * 4u;
-  const uint32_t s_off = FMT == kFp8 ? (uint32_t)(c0 >> 7) * (uint32_t)KB * 4u : (uint32_t)(c0 + n16) * 4u;
-  const uint32_t s_step = FMT == kFp8 ? 4u : 4u * (uint32_t)H;
-  const uint32_t h_bytes = (uint32_t)p.T * (uint32_t)p.k * (uint32_t)I * 2u;
-
   if (lo < hi) {
-    // what is being loaded: expert ld_a of the list, step ld_k, group ld_g of its ld_n; the lane's row of h, weight and token
-    int ld_a = lo / KB, ld_k = lo - ld_a * KB;
+    const int KB = p.I >> 7;
+    const uint32_t w_bytes = H * row_bytes;
+    // loads: row (or token) lane / 8, chunk lane % 8; weight rows c0 + 2 (lane / 8) + a
+    const int l8 = lane >> 3, ch = lane & 7;
+    const int from = 4 * (8 * r8 + q + 4 * half);
+    uint32_t w_off[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(c0 + 2 * l8 + a) * row_bytes + 16u * ch;
+    // scales: e4m3 [ceil(H / 128)][KB] fp32, e2m1 words [KB][H]
+    const uint32_t s_bytes = FMT == kFp8 ? ((H + 127) >> 7) * (uint32_t)KB * 4u : (uint32_t)KB * H * 4u;
+    const uint32_t s_off = FMT == kFp8 ? (uint32_t)(c0 >> 7) * (uint32_t)KB * 4u : (half * H + (uint32_t)(c0 + 2 * r8)) * 4u;
+    const uint32_t s_step = FMT == kFp8 ? 4u : 8u * H;
+    const uint32_t h_bytes = (uint32_t)p.T * (uint32_t)p.k * I * 2u;
+
+    // what is loaded next: step ld_u of the run, step ld_k of expert ld_a of the list, group ld_g of its ld_n; the lane's rows
+    // of h, weights and tokens
+    int ld_u = lo, ld_a = lo / KS, ld_k = lo - ld_a * KS;
     int ld_g = 0, ld_n = 1, first = 0, members = 0;
-    // loads of the run: a step's groups one after the other
-    auto loads_before = [&](int step) {
-      const int a = step / KB;
-      const int g = __builtin_amdgcn_readfirstlane((int)s.group[a]);
-      const int n = a < chosen ? __builtin_amdgcn_readfirstlane((int)s.group[a + 1]) - g : 0;
-      return g * KB + (step - a * KB) * n;
-    };
-    const int loads = loads_before(hi) - loads_before(lo);
     const uint8_t* wbase = p.w2;
     const uint8_t* sbase = static_cast<const uint8_t*>(p.s2);
-    uint32_t h_off = kOOB;
-    float fac = 0.f;
-    int token = -1;
+    uint32_t h_off[MG];
+    float fac[MG];
+    int token[MG];
     auto enter_expert = [&]() {
-      const int e = __builtin_amdgcn_readfirstlane((int)s.list[ld_a]);
+      const uint32_t r = __builtin_amdgcn_readfirstlane(s.run[ld_a]);
+      const int e = expert_of(r);
       wbase = p.w2 + (int64_t)e * w_bytes;
       sbase = static_cast<const uint8_t*>(p.s2) + (int64_t)e * s_bytes;
-      first = __builtin_amdgcn_readfirstlane((int)s.start[ld_a]);
-      members = __builtin_amdgcn_readfirstlane((int)s.start[ld_a + 1]) - first;
-      ld_n = (members + 15) >> 4;
+      first = start_of(r);
+      members = count_of(r);
+      ld_n = (members + 8 * MG - 1) / (8 * MG);
     };
     auto enter_group = [&]() {
-      const int r = 16 * ld_g + n16;
-      h_off = kOOB;
-      fac = 0.f;
-      token = -1;
-      if (r < members) {
-        const int c = s.choice[first + r];
-        h_off = (uint32_t)c * (uint32_t)I * 2u + 64u * q;
-        fac = s.weight[first + r];
-        token = c / p.k;
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+        const int r = 8 * (MG * ld_g + g);
+        h_off[g] = r + l8 < members ? (s.entry[first + r + l8] & 0xffffu) * I * 2u + 16u * P * ch : kOOB;
+        fac[g] = r + r8 < members ? s.weight[first + r + r8] : 0.f;
+        token[g] = r + r8 < members ? (int)(s.entry[first + r + r8] >> 16) : -1;
       }
     };
     enter_expert();
     enter_group();
     bool fresh = true;  // the next load begins a group of tokens
 
-    Weights<FMT> wr[D];
-    uint32_t sr[D];
-    u32x4 hr[D][4];
-    float fr[D];
-    int tr[D];
-    bool nr[D];
-    auto load = [&](int d, int j) {
-      const bool in = j < loads;
-      if (in && ld_k == KB) {
+    u32x4 w[D][2];
+    u32x2 sc[D];
+    u32x4 hr[D][MG][P];
+    float fr[D][MG];
+    int tr[D][MG];
+    bool nr[D], vr[D];
+    int gr[D];  // groups of 8 that hold a token
+    auto load = [&](int d) {
+      const bool in = ld_u < hi;
+      if (in && ld_k == KS) {
         ++ld_a;
-        ld_k = ld_g = 0;
+        ld_k = 0;
         enter_expert();
         enter_group();
         fresh = true;
       }
+      // past the run's last step the ranges are empty: zeros, and no traffic
       const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, in ? w_bytes : 0u);
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(sbase, in ? s_bytes : 0u);
       const __amdgpu_buffer_rsrc_t rh = make_rsrc(p.h, in ? h_bytes : 0u);
       const uint32_t k = in ? (uint32_t)ld_k : 0u;
-      wr[d] = load_weights<FMT, NT>(rw, w_off, k);
-      sr[d] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
+      const bool over = FMT == kFp4 && (k + 1) * 256u > I;  // a last half step has no upper chunks
+      const bool cut = over && ch >= 4;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) hr[d][t] = __builtin_amdgcn_raw_buffer_load_b128(rh, h_off == kOOB ? kOOB : h_off + 16u * t, k * 256u, 0);
-      fr[d] = in ? fac : 0.f;  // (an infinite weight times the padding's zero would be NaN)
-      tr[d] = token;
-      nr[d] = in && fresh;
+      for (int a = 0; a < 2; ++a) w[d][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], k * 128u, NT ? kStream : 0);
+      if constexpr (FMT == kFp8) sc[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
+      else sc[d] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, k * s_step, 0);
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+#pragma unroll
+        for (int t = 0; t < P; ++t)
+          hr[d][g][t] = __builtin_amdgcn_raw_buffer_load_b128(rh, cut || h_off[g] == kOOB ? kOOB : h_off[g] + 16u * t, k * 2u * kStepDepth<FMT>, 0);
+        fr[d][g] = fac[g];
+        tr[d][g] = token[g];
+      }
+      nr[d] = fresh;
+      vr[d] = in;
+      gr[d] = (members - 8 * MG * ld_g + 7) >> 3;
       fresh = false;
       if (in) {
         if (ld_n == 1) {
           ++ld_k;
+          ++ld_u;
         } else {
           if (++ld_g == ld_n) {
             ld_g = 0;
             ++ld_k;
+            ++ld_u;
           }
           enter_group();
           fresh = true;
         }
       }
     };
-    f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-    int to = -1;
+    f32x4 acc[MG][2];
+    int to[MG];
+    float by[MG];
+    // the accumulators into the sums: lanes (token r8, q < 2) of the lower half have columns 8 q + 2 e + a
+    auto flush = [&]() {
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(d, d);
-    for (int j0 = 0; j0 < loads; j0 += D) {
+      for (int g = 0; g < MG; ++g) {
+        const f32x4 x = halves(acc[g][0]), y = halves(acc[g][1]);
+        if (to[g] >= 0 && !half && q < 2) {
+          f32x4* at = &sums[to[g] * (kDownCols / 4) + 2 * q];
+          at[0] += f32x4{x[0], y[0], x[1], y[1]} * by[g];
+          at[1] += f32x4{x[2], y[2], x[3], y[3]} * by[g];
+        }
+      }
+    };
+#pragma unroll
+    for (int g = 0; g < MG; ++g) {
+      to[g] = -1;
+      by[g] = 0.f;
+      acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) load(d);
+    bool any = false, more = true;
+    while (more) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         __builtin_amdgcn_sched_barrier(0);
-        if (nr[d]) {  // uniform
-          if (to >= 0) sums[wave][to * 4 + q] += acc;
-          acc = f32x4{0.f, 0.f, 0.f, 0.f};
-          to = tr[d];
+        if (nr[d] && vr[d]) {  // uniform
+          if (any) flush();
+          any = true;
+#pragma unroll
+          for (int g = 0; g < MG; ++g) {
+            to[g] = tr[d][g];
+            by[g] = fr[d][g];
+            acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+          }
         }
-        const float ex = FMT == kFp4 ? exponent_of(sr[d], q) : 1.f;
-        f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+        bf16x8 v[2][P];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) o = mfma(widened<FMT>(wr[d], t, ex), hr[d][t], o);
-        const float f = FMT == kFp8 ? fr[d] * __uint_as_float(sr[d]) : fr[d];
+        for (int a = 0; a < 2; ++a) {
+          const float ex = FMT == kFp4 ? exponent_of(sc[d][a], q) : 1.f;
+          const u32x4 chunk = spread(from, w[d][a]);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(o[v], f, acc[v]);
-        load(d, j0 + d + D);
+          for (int t = 0; t < P; ++t) v[a][t] = widened<FMT>(chunk, t, ex);
+        }
+#pragma unroll
+        for (int g = 0; g < MG; ++g) {
+          if (g > 0 && g >= gr[d]) break;  // uniform
+          u32x4 x[P];
+#pragma unroll
+          for (int t = 0; t < P; ++t) x[t] = spread(from, hr[d][g][t]);
+#pragma unroll
+          for (int a = 0; a < 2; ++a) {
+            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[g][a];
+#pragma unroll
+            for (int t = 0; t < P; ++t) o = mfma(v[a][t], x[t], o);
+            if constexpr (FMT == kFp8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[g][a][e] = __builtin_fmaf(o[e], __uint_as_float(sc[d][0]), acc[g][a][e]);
+            } else {
+              acc[g][a] = o;
+            }
+          }
+        }
+        load(d);
       }
+      more = vr[0];
     }
-    if (to >= 0) sums[wave][to * 4 + q] += acc;
+    flush();
+  }
+}
+
+template <int FMT, bool FEW, bool NT>
+__global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_down_kernel(ExpertsParams p) {
+  constexpr int W = kDownWaves<FEW>;
+  constexpr int THREADS = 64 * W;
+  __shared__ ExpertsTable s;
+  __shared__ __attribute__((aligned(16))) f32x4 sums[W][(FEW ? 8 : kExpertsMaxTokens) * (kDownCols / 4)];  // [token][four columns]
+  __shared__ int last;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = (int)blockIdx.x / p.splits, split = (int)blockIdx.x - tile * p.splits;
+  const int c0 = tile * kDownCols;
+  {
+    const int n = p.T * p.k;
+    for (int i = threadIdx.x; i < n; i += THREADS) {
+      s.run[i] = p.table->run[i];
+      s.entry[i] = p.table->entry[i];
+      s.weight[i] = p.table->weight[i];
+    }
+    if (threadIdx.x == 0) s.n = p.table->n;
+  }
+  for (int i = lane; i < p.T * (kDownCols / 4); i += 64) sums[wave][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  const int slot = split * W + wave, slots = W * p.splits;
+  if constexpr (FEW) {
+    down_run<FMT, 1, FEW, NT>(p, s, sums[wave], c0, slot, slots);
+  } else {
+    // tokens of an expert on average: an expert of more takes its steps group by group
+    const int chosen = __builtin_amdgcn_readfirstlane(s.n);
+    const uint32_t end = chosen > 0 ? __builtin_amdgcn_readfirstlane(s.run[chosen - 1]) : 0u;
+    const int entries = chosen > 0 ? start_of(end) + count_of(end) : 0;
+    if (entries <= 6 * chosen) down_run<FMT, 1, FEW, NT>(p, s, sums[wave], c0, slot, slots);
+    else if (entries <= 12 * chosen) down_run<FMT, 2, FEW, NT>(p, s, sums[wave], c0, slot, slots);
+    else down_run<FMT, 4, FEW, NT>(p, s, sums[wave], c0, slot, slots);
   }
   __syncthreads();
   // the waves' sums in order: a thread takes four columns of a token
   const int u = threadIdx.x;
-  const bool live = u < p.T * 4;
+  const bool live = u < p.T * (kDownCols / 4);
   f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
   if (live)
 #pragma unroll
@@ -534,8 +685,8 @@ __global__ void __launch_bounds__(512) experts_down_kernel(ExpertsParams p) {
     // The workgroups' sums meet in the workspace: sc1 stores and loads are coherent across the XCDs' L2 caches; every wave's
     // stores are acknowledged (vmcnt 0) before the barrier that precedes the relaxed counter increment, and the last
     // workgroup loads only after its own increment has returned.  It adds them in order and leaves the counter at zero.
-    const uint32_t one = (uint32_t)p.T * 64u;
-    const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.partials, (uint32_t)(p.splits * (H >> 4)) * one);
+    const uint32_t one = (uint32_t)p.T * 4u * kDownCols;
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.partials, (uint32_t)p.splits * (uint32_t)p.H * (uint32_t)p.T * 4u);
     const uint32_t off = live ? (uint32_t)tile * (uint32_t)p.splits * one + (uint32_t)u * 16u : kOOB;
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, off, (uint32_t)split * one, kCoherent);
     wait_vmcnt<0>();
@@ -544,42 +695,55 @@ __global__ void __launch_bounds__(512) experts_down_kernel(ExpertsParams p) {
       last = __hip_atomic_fetch_add(&p.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned int)(p.splits - 1);
     __syncthreads();
     if (!last) return;
-    y = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < p.splits; ++i)
-      y += __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, off, (uint32_t)i * one, kCoherent));
     if (threadIdx.x == 0) __hip_atomic_store(&p.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    y = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < p.splits; i0 += 4) {  // four in flight; past the last, an empty place
+      f32x4 t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        t[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, i0 + i < p.splits ? off : kOOB, (uint32_t)(i0 + i < p.splits ? i0 + i : 0) * one, kCoherent));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y += t[i];
+    }
   }
   if (live)
-    *reinterpret_cast<uint2*>(p.y + (int64_t)(u >> 2) * H + c0 + 4 * (u & 3)) = uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+    *reinterpret_cast<uint2*>(p.y + (int64_t)(u / (kDownCols / 4)) * p.H + c0 + 4 * (u % (kDownCols / 4))) =
+        uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
 }
 
 template <int FMT, bool NT>
-hipError_t launch_format(const ExpertsParams& p, hipStream_t stream) {
-  const int most = p.G < p.T * p.k ? p.G : p.T * p.k;  // experts that can have been chosen
-  hipLaunchKernelGGL((experts_up_kernel<FMT, NT>), dim3((unsigned)(most * (p.I / 16))), dim3(256), 0, stream, p);
+hipError_t launch_format(const ExpertsParams& p, int cus, hipStream_t stream) {
+  const int64_t most = (int64_t)(p.G < p.T * p.k ? p.G : p.T * p.k) * (p.I / 16);  // units, where every choice names another expert
+  const int64_t room = (int64_t)(p.T <= 16 ? 3 : 2) * cus;
+  const dim3 up((unsigned)(most < room ? most : room));
+  if (p.T <= 16) hipLaunchKernelGGL((experts_up_kernel<FMT, 2, NT>), up, dim3(kUpThreads), 0, stream, p);
+  else hipLaunchKernelGGL((experts_up_kernel<FMT, 4, NT>), up, dim3(kUpThreads), 0, stream, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((experts_down_kernel<FMT, NT>), dim3((unsigned)(p.H / 16 * p.splits)), dim3(512), 0, stream, p);
+  const dim3 grid((unsigned)(p.H / kDownCols * p.splits));
+  if (p.T <= 8) hipLaunchKernelGGL((experts_down_kernel<FMT, true, NT>), grid, dim3(64 * kDownWaves<true>), 0, stream, p);
+  else hipLaunchKernelGGL((experts_down_kernel<FMT, false, NT>), grid, dim3(64 * kDownWaves<false>), 0, stream, p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Workgroups that share 16 columns of the down projection: as many as give the chip sixteen waves a CU, with two steps a wave
-int experts_splits(int64_t choices, int64_t H, int64_t I, int64_t G, int cus) {
-  const int64_t tiles = H / 16;
+// Workgroups that share 16 columns of the down projection: as many as give the chip eight waves a CU, with two steps a wave
+int experts_splits(int64_t T, int64_t choices, int64_t H, int64_t I, int64_t G, int cus) {
+  const int64_t tiles = H / kDownCols;
   if (tiles > 1024) return 1;  // counters
+  const int waves = T <= 8 ? kDownWaves<true> : kDownWaves<false>;
   const int64_t steps = (G < choices ? G : choices) * (I / 128);
-  int64_t s = 2 * (int64_t)cus / tiles;
-  if (s > steps / 16) s = steps / 16;
+  int64_t s = 8 * (int64_t)cus / waves / tiles;
+  if (s > steps / (2 * waves)) s = steps / (2 * waves);
   return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
 size_t experts_h_bytes(int64_t choices, int64_t I) { return ((size_t)choices * (size_t)I * 2 + 255) / 256 * 256; }
 
-hipError_t launch_moe_experts(const ExpertsParams& p, bool fp4, bool stream_weights, hipStream_t stream) {
-  if (fp4) return stream_weights ? launch_format<kFp4, true>(p, stream) : launch_format<kFp4, false>(p, stream);
-  return stream_weights ? launch_format<kFp8, true>(p, stream) : launch_format<kFp8, false>(p, stream);
+hipError_t launch_moe_experts(const ExpertsParams& p, bool fp4, bool stream_weights, int cus, hipStream_t stream) {
+  if (fp4) return stream_weights ? launch_format<kFp4, true>(p, cus, stream) : launch_format<kFp4, false>(p, cus, stream);
+  return stream_weights ? launch_format<kFp8, true>(p, cus, stream) : launch_format<kFp8, false>(p, cus, stream);
 }
 
 }  // namespace dg
