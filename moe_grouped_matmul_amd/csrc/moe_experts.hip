@@ -481,10 +481,11 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     const uint32_t s_step = FMT == kFp8 ? 4u : 8u * H;
     const uint32_t h_bytes = (uint32_t)p.T * (uint32_t)p.k * I * 2u;
 
-    // what is loaded next: step ld_u of the run, step ld_k of expert ld_a of the list, group ld_g of its ld_n; the lane's rows
-    // of h, weights and tokens
-    int ld_u = lo, ld_a = lo / KS, ld_k = lo - ld_a * KS;
-    int ld_g = 0, ld_n = 1, first = 0, members = 0;
+    // what is loaded next: step ld_k of [k_lo, k_hi) of expert ld_a of the list, group ld_g of its ld_n; the lane's rows of h,
+    // weights and tokens.  An expert's groups take its steps one after the other (32 tokens of one group are common, more rare).
+    int ld_a = lo / KS;
+    int k_lo = lo - ld_a * KS, k_hi = 0, left = hi - lo;  // steps of the run past k_hi
+    int ld_k = k_lo, ld_g = 0, ld_n = 1, first = 0, members = 0;
     const uint8_t* wbase = p.w2;
     const uint8_t* sbase = static_cast<const uint8_t*>(p.s2);
     uint32_t h_off[MG];
@@ -498,6 +499,8 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       first = start_of(r);
       members = count_of(r);
       ld_n = (members + 8 * MG - 1) / (8 * MG);
+      k_hi = KS - k_lo < left ? KS : k_lo + left;
+      left -= k_hi - k_lo;
     };
     auto enter_group = [&]() {
 #pragma unroll
@@ -520,14 +523,17 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     bool nr[D], vr[D];
     int gr[D];  // groups of 8 that hold a token
     auto load = [&](int d) {
-      const bool in = ld_u < hi;
-      if (in && ld_k == KS) {
-        ++ld_a;
-        ld_k = 0;
-        enter_expert();
+      if (ld_k == k_hi && (ld_g + 1 < ld_n || left > 0)) {
+        if (++ld_g == ld_n) {
+          ++ld_a;
+          ld_g = k_lo = 0;
+          enter_expert();
+        }
+        ld_k = k_lo;
         enter_group();
         fresh = true;
       }
+      const bool in = ld_k < k_hi;
       // past the run's last step the ranges are empty: zeros, and no traffic
       const __amdgpu_buffer_rsrc_t rw = make_rsrc(wbase, in ? w_bytes : 0u);
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(sbase, in ? s_bytes : 0u);
@@ -551,20 +557,7 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       vr[d] = in;
       gr[d] = (members - 8 * MG * ld_g + 7) >> 3;
       fresh = false;
-      if (in) {
-        if (ld_n == 1) {
-          ++ld_k;
-          ++ld_u;
-        } else {
-          if (++ld_g == ld_n) {
-            ld_g = 0;
-            ++ld_k;
-            ++ld_u;
-          }
-          enter_group();
-          fresh = true;
-        }
-      }
+      if (in) ++ld_k;
     };
     f32x4 acc[MG][2];
     int to[MG];
