@@ -18,7 +18,7 @@ namespace {
 // NW waves take a row, CH runs of 8 values a lane: run i of wave w is the
 // 512 columns from (i NW + w) 512 on, so that 16 lanes hold one 128-column
 // group and a wave's run one word of power-of-two scales.
-template <bool BF16, int KIND, int CH, int NW>
+template <bool BF16, int KIND, int CH, int NW, bool NT>
 __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormParams p) {
   constexpr int ROWS = NW <= 4 ? 4 / NW : 1;  // of a workgroup
   __shared__ float part[ROWS][NW];
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
   for (int i = 0; i < CH; ++i) {
     const int c = ((i * NW + w) * 64 + lane) * 8;
     h[i] = Raw8<BF16>{};
-    if (live && c < K) h[i] = load8<BF16>(p.x, at + c);
+    if (live && c < K) h[i] = load8<BF16, NT>(p.x, at + c);
   }
   if (p.residual) {
     Raw8<BF16> r[CH];
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
     for (int i = 0; i < CH; ++i) {
       const int c = ((i * NW + w) * 64 + lane) * 8;
       r[i] = Raw8<BF16>{};
-      if (live && c < K) r[i] = load8<BF16>(p.residual, at + c);
+      if (live && c < K) r[i] = load8<BF16, NT>(p.residual, at + c);
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
     values(h[i], a);
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(a[e], a[e], sum);
-    if (p.h && live && c < K) store8<BF16>(p.h, at + c, h[i]);
+    if (p.h && live && c < K) store8<BF16, NT>(p.h, at + c, h[i]);
   }
   sum = wave_sum(sum);
   if constexpr (NW > 1) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
     if (in) weights8(p.weight, p.weight_bf16, c, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = in ? (v[e] * r) * g[e] : 0.f;
-    if (p.y && in) store8<BF16>(p.y, at + c, rounded<BF16>(v));
+    if (p.y && in) store8<BF16, NT>(p.y, at + c, rounded<BF16>(v));
     if constexpr (KIND != kNoQuant) {
       const float amax = max16(max8(v));
       const int kb = run * 4 + (lane >> 4);
@@ -105,13 +105,17 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
       } else {
         const float s = scale_from_amax(amax);
         float y[8];
-        quotients<8>(v, y, s, 1.f / s);
+        quotients<8>(v, y, s);
         out.x = e4m3x4(y[0], y[1], y[2], y[3]);
         out.y = e4m3x4(y[4], y[5], y[6], y[7]);
         if ((lane & 15) == 0 && in) static_cast<float*>(p.sf)[(int64_t)kb * p.M + row] = s;
       }
       (void)kb;
-      if (in) *reinterpret_cast<uint2*>(p.q + at + c) = out;
+      if (in) {
+        typedef unsigned int raw2 __attribute__((ext_vector_type(2)));
+        if constexpr (NT) __builtin_nontemporal_store(raw2{out.x, out.y}, reinterpret_cast<raw2*>(p.q + at + c));
+        else *reinterpret_cast<uint2*>(p.q + at + c) = out;
+      }
     }
   }
 }
@@ -245,42 +249,42 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
 }
 
 template <bool BF16, int KIND, int CH, int NW>
-void norm_one(const NormParams& p, hipStream_t stream) {
+void norm_one(const NormParams& p, bool nt, hipStream_t stream) {
   constexpr int ROWS = NW <= 4 ? 4 / NW : 1;
-  hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW>), dim3((unsigned)((p.M + ROWS - 1) / ROWS)),
-                     dim3(NW <= 4 ? 256 : 64 * NW), 0, stream, p);
+  const dim3 grid((unsigned)((p.M + ROWS - 1) / ROWS)), wg(NW <= 4 ? 256 : 64 * NW);
+  if (nt) hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, true>), grid, wg, 0, stream, p);
+  else hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, false>), grid, wg, 0, stream, p);
 }
 
-// runs of 512 columns that a lane can hold of a row: 16 of bf16 (64 registers), 8 of fp32
-template <bool BF16, int NW>
-constexpr int most_runs() {
-  return kNormMaxK / 512 / NW < (BF16 ? 16 : 8) ? kNormMaxK / 512 / NW : (BF16 ? 16 : 8);
-}
+// runs of 512 columns that a lane holds of a row
+constexpr int kMostRuns = 4;
 template <bool BF16, int KIND, int NW>
-void norm_runs(const NormParams& p, int ch, hipStream_t stream) {
-  constexpr int MOST = most_runs<BF16, NW>();
-  if (ch <= 1) return norm_one<BF16, KIND, 1, NW>(p, stream);
-  if (ch <= 2) return norm_one<BF16, KIND, 2, NW>(p, stream);
-  if constexpr (MOST >= 4)
-    if (ch <= 4) return norm_one<BF16, KIND, 4, NW>(p, stream);
-  if constexpr (MOST >= 8)
-    if (ch <= 8) return norm_one<BF16, KIND, 8, NW>(p, stream);
-  if constexpr (MOST >= 16) norm_one<BF16, KIND, 16, NW>(p, stream);
+void norm_runs(const NormParams& p, int ch, bool nt, hipStream_t stream) {
+  constexpr int MOST = kNormMaxK / 512 / NW < kMostRuns ? kNormMaxK / 512 / NW : kMostRuns;
+  if (ch <= 1) return norm_one<BF16, KIND, 1, NW>(p, nt, stream);
+  if (ch <= 2) return norm_one<BF16, KIND, 2, NW>(p, nt, stream);
+  if constexpr (MOST >= 4) norm_one<BF16, KIND, 4, NW>(p, nt, stream);
 }
 
 template <bool BF16, int KIND>
 hipError_t norm_shape(const NormParams& p, int cus, hipStream_t stream) {
-  // the fewest waves a row that hold it, more while that leaves the chip's waves idle
+  // The fewest waves a row with four runs a lane, more while that leaves the chip's waves idle.  (A row of 14 runs by one wave
+  // of 16, two of 8 and four of 4: 16384 x 7168 with codes 202, 167 and 162 us: with fewer registers more rows are in flight.)
   const int runs = (p.K + 511) / 512;
   int nw = 1;
-  while (nw < 16 && (nw * (BF16 ? 16 : 8) < runs || (nw < runs && p.M * nw < 16 * cus))) nw *= 2;
+  while (nw < 16 && (nw * kMostRuns < runs || (nw < runs && p.M * nw < 16 * cus))) nw *= 2;
   const int ch = (runs + nw - 1) / nw;
+  // Rows that the 256 MB Infinity Cache cannot hold are streamed past it, in and out (16384 x 7168 bf16 173 -> 162 us; 1021 x
+  // 2048 fp32, which it holds from one call to the next: 7.6 -> 8.6, so not there; 8192 x 4096 bf16 with its backward pass: no
+  // difference)
+  const int64_t row = (int64_t)p.K * (BF16 ? 2 : 4);
+  const bool nt = p.M * (row * (1 + (p.residual != nullptr) + (p.h != nullptr) + (p.y != nullptr)) + (p.q ? p.K : 0)) >= (int64_t)512 << 20;
   switch (nw) {
-    case 1: norm_runs<BF16, KIND, 1>(p, ch, stream); break;
-    case 2: norm_runs<BF16, KIND, 2>(p, ch, stream); break;
-    case 4: norm_runs<BF16, KIND, 4>(p, ch, stream); break;
-    case 8: norm_runs<BF16, KIND, 8>(p, ch, stream); break;
-    default: norm_runs<BF16, KIND, 16>(p, ch, stream); break;
+    case 1: norm_runs<BF16, KIND, 1>(p, ch, nt, stream); break;
+    case 2: norm_runs<BF16, KIND, 2>(p, ch, nt, stream); break;
+    case 4: norm_runs<BF16, KIND, 4>(p, ch, nt, stream); break;
+    case 8: norm_runs<BF16, KIND, 8>(p, ch, nt, stream); break;
+    default: norm_runs<BF16, KIND, 16>(p, ch, nt, stream); break;
   }
   return hipGetLastError();
 }

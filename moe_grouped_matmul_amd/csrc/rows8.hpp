@@ -13,19 +13,24 @@ template <bool BF16>
 struct Raw8 {
   raw4 v[BF16 ? 1 : 2];
 };
-template <bool BF16>
+// (NT: past the caches)
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ Raw8<BF16> load8(const void* base, int64_t at) {
   Raw8<BF16> r;
   const raw4* p = reinterpret_cast<const raw4*>(static_cast<const uint8_t*>(base) + at * (BF16 ? 2 : 4));
-  r.v[0] = p[0];
-  if constexpr (!BF16) r.v[1] = p[1];
+  r.v[0] = NT ? __builtin_nontemporal_load(p) : p[0];
+  if constexpr (!BF16) r.v[1] = NT ? __builtin_nontemporal_load(p + 1) : p[1];
   return r;
 }
-template <bool BF16>
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ void store8(void* base, int64_t at, const Raw8<BF16>& r) {
   raw4* p = reinterpret_cast<raw4*>(static_cast<uint8_t*>(base) + at * (BF16 ? 2 : 4));
-  p[0] = r.v[0];
-  if constexpr (!BF16) p[1] = r.v[1];
+  if constexpr (NT) __builtin_nontemporal_store(r.v[0], p);
+  else p[0] = r.v[0];
+  if constexpr (!BF16) {
+    if constexpr (NT) __builtin_nontemporal_store(r.v[1], p + 1);
+    else p[1] = r.v[1];
+  }
 }
 template <bool BF16>
 __device__ __forceinline__ void values(const Raw8<BF16>& r, float* f) {
