@@ -181,7 +181,7 @@ int dg_epilogue_bwd(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* 
   if (M == 0 && !dbias) return ok();
   int cus = 0;
   if ((rc = check_device(&cus))) return rc;
-  const int64_t rows = M == 0 ? 16 : epilogue_bwd_rows(M, N, effective_cus(cus));
+  const int64_t rows = M == 0 ? 8 : epilogue_bwd_rows(M, N, effective_cus(cus));
   if (dbias && (rc = check_partials(workspace, workspace_bytes, partials_bytes(ceil_div(M, rows), N)))) return rc;
   const EpilogueBwdParams p{dy, pre, dz, q, sf, dbias, dbias ? partials_of(workspace) : nullptr, M, rows, (int)N};
   return launched(launch_epilogue_bwd(p, act, hs(stream)));

@@ -19,7 +19,7 @@
 namespace dg {
 namespace {
 
-constexpr int kBatch = 4;  // rows in flight of a wave
+constexpr int kBatch = 2;  // rows in flight of a wave
 
 // one rounded product, not fused with the sum it goes into: the bias' gradient is the same whatever else is asked for
 __device__ __forceinline__ float product(float a, float b) {
@@ -98,21 +98,22 @@ void bwd_act(const EpilogueBwdParams& p, dim3 grid, hipStream_t stream) {
 
 }  // namespace
 
-// Rows of a workgroup: a multiple of 16 (four waves, four rows in flight each), as many workgroups as four to a CU, at
-// most 1024 of them down the rows
+// Rows of a workgroup: a multiple of 8 (four waves, two rows in flight each), as many workgroups as eight to a CU, at most 1024
+// of them down the rows (4096 x 4096 with gelu, codes and bias: four rows in flight and four workgroups 31 us, two and four 29,
+// two and eight 27)
 static int64_t most_down(int64_t N, int cus) {
   const int64_t cols = (N + 511) / 512;
-  const int64_t down = (4 * (int64_t)cus + cols - 1) / cols;
+  const int64_t down = (8 * (int64_t)cus + cols - 1) / cols;
   return down < 1024 ? down : 1024;
 }
 int64_t epilogue_bwd_rows(int64_t M, int64_t N, int cus) {
   const int64_t down = most_down(N, cus);
   const int64_t rows = (M + down - 1) / down;
-  return (rows + 15) / 16 * 16;
+  return (rows + 7) / 8 * 8;
 }
 int64_t epilogue_bwd_partials(int64_t M, int64_t N, int cus) {
   const int64_t down = most_down(N, cus);
-  return (M + 15) / 16 < down ? (M + 15) / 16 : down;
+  return (M + 7) / 8 < down ? (M + 7) / 8 : down;
 }
 
 hipError_t launch_epilogue_bwd(const EpilogueBwdParams& p, int act, hipStream_t stream) {

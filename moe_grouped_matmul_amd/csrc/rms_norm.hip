@@ -225,19 +225,25 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwdParams p) {
   }
 }
 
-// 16 columns x 16 slices of rows a workgroup
+// 64 columns x 16 slices of rows a workgroup
+constexpr int kSumCols = 64;
 constexpr int kSumSlices = 16;
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ partials, float* __restrict__ out,
-                                                         int64_t rows, int N) {
-  __shared__ float s[kSumSlices][17];
-  const int col = threadIdx.x & 15, sl = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + col;
+__global__ void __launch_bounds__(64 * 16) column_sum_kernel(const float* __restrict__ partials, float* __restrict__ out,
+                                                                          int64_t rows, int N) {
+  __shared__ float s[kSumSlices][kSumCols];
+  const int col = threadIdx.x % kSumCols, sl = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + col;
   const int64_t per = (rows + kSumSlices - 1) / kSumSlices;
   const int64_t hi = (sl + 1) * per < rows ? (sl + 1) * per : rows;
   float a = 0.f;
   if (c < N) {
-#pragma unroll 8
-    for (int64_t r = sl * per; r < hi; ++r) a += partials[r * N + c];
+    for (int64_t r = sl * per; r < hi; r += 8) {  // eight rows in flight
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = r + i < hi ? partials[(r + i) * N + c] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a += v[i];
+    }
   }
   s[sl][col] = a;
   __syncthreads();
@@ -348,7 +354,7 @@ hipError_t launch_rms_norm_bwd(const NormBwdParams& p, bool bf16, int cus, hipSt
 }
 
 hipError_t launch_column_sum(const float* partials, float* out, int64_t rows, int N, hipStream_t stream) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + 15) / 16)), dim3(256), 0, stream, partials, out, rows, N);
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumSlices), 0, stream, partials, out, rows, N);
   return hipGetLastError();
 }
 
