@@ -63,9 +63,9 @@ __global__ void __launch_bounds__(256) epilogue_bwd_kernel(EpilogueBwdParams p) 
       for (int e = 0; e < 8; ++e) acc[e] += v[e];
       if (p.dz && in) store8<true>(p.dz, r * p.N + c, rounded<true>(v));
       if constexpr (QUANT) {  // N is a multiple of 128: a group's lanes are all inside or all outside
-        const float s_ = scale_from_amax(max16(max8(v)));
+        const float s_ = scale_of(max16(max8(v)));
         float y[8];
-        quotients<8>(v, y, s_);
+        quotients_of<8>(v, y, s_);
         if (in) {
           *reinterpret_cast<uint2*>(p.q + r * p.N + c) = uint2{e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7])};
           if ((lane & 15) == 0) p.sf[(int64_t)(c >> 7) * p.M + r] = s_;

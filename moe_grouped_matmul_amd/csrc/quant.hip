@@ -67,9 +67,10 @@ __global__ void __launch_bounds__(256) quant_1x128_kernel(const float* __restric
     }
   } else {
     const float s = scale_from_amax(amax);
+    const float r = 1.0f / s;  // IEEE division, correctly rounded
     const float xv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     float y[8];
-    quotients<8>(xv, y, s);
+    quotients<8>(xv, y, s, r);
     out.x = e4m3x4(y[0], y[1], y[2], y[3]);
     out.y = e4m3x4(y[4], y[5], y[6], y[7]);
     if (sub == 0) static_cast<float*>(sfa)[(g * KB + kb) * M + m] = s;
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(256) quant_128x128_kernel(const float* __restr
   __syncthreads();
   amax = fmaxf(fmaxf(s_wave_max[0], s_wave_max[1]), fmaxf(s_wave_max[2], s_wave_max[3]));
   const float s = scale_from_amax(amax);
+  const float rs = 1.0f / s;  // IEEE division, correctly rounded
   const int c = ue8m0_code(amax);
   const float inv = __builtin_ldexpf(1.0f, 127 - c);
   uint8_t* qbase = q + (g * N) * K + ((int64_t)kb << 7) + col;
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(256) quant_128x128_kernel(const float* __restr
       } else {
         const float xv[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
         float y[8];
-        quotients<8>(xv, y, s);
+        quotients<8>(xv, y, s, rs);
         out.x = e4m3x4(y[0], y[1], y[2], y[3]);
         out.y = e4m3x4(y[4], y[5], y[6], y[7]);
       }

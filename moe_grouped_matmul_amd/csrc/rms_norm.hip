@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
         if ((lane & 15) == 0 && run * 512 < K)
           (static_cast<uint8_t*>(p.sf) + ((int64_t)run * p.M + row) * 4)[lane >> 4] = in ? (uint8_t)code : 0;
       } else {
-        const float s = scale_from_amax(amax);
+        const float s = scale_of(amax);
         float y[8];
-        quotients<8>(v, y, s);
+        quotients_of<8>(v, y, s);
         out.x = e4m3x4(y[0], y[1], y[2], y[3]);
         out.y = e4m3x4(y[4], y[5], y[6], y[7]);
         if ((lane & 15) == 0 && in) static_cast<float*>(p.sf)[(int64_t)kb * p.M + row] = s;
