@@ -3,7 +3,8 @@
 Serving (`MoELayer`): the experts' weights in microscaled 4-bit floats.
   router -> dg_moe_gate -> dg_moe_layout_{contiguous,masked} -> dg_quant_mxfp4 (tokens gathered into expert rows)
   -> grouped product (gate and up projection) -> SiLU(gate) * up -> dg_quant_mxfp4 -> grouped product (down) -> dg_moe_combine
-`prefill` uses the contiguous form, `decode` the masked one (a fixed launch shape, for graph capture).
+`prefill` uses the contiguous form, `decode` the masked one (a fixed launch shape, for graph capture), `few` the experts of up to
+64 tokens in two kernels (dg_moe_experts_mxfp4), with activations that stay bf16.
 
 Training (`train_step`): one expert projection in block-scaled FP8 between the router and the combine, with the gradients
 of the router's logits and of the expert rows.
@@ -95,6 +96,14 @@ class MoELayer:
         dg.dg_moe_combine(out["rows"].reshape(-1, self.H), row_of, w, y)
         return dict(out, y=y, idx=idx, w=w, row_of=row_of, row_token=row_token)
 
+    def few(self, x):
+        """The layer for at most 64 tokens: x [T,H] bf16 -> y [T,H] bf16."""
+        idx, w = self.route(x)
+        y = torch.empty_like(x)
+        dg.dg_moe_experts_mxfp4(x, idx, w, *self.gate_up, *self.down, y,
+                                workspace=_workspace(dg.DG_OP_MOE_EXPERTS, x.shape[0] * self.k, self.H, self.I))
+        return dict(y=y, idx=idx, w=w)
+
 
 def train_step(x, logits, w8, sw8, dy, k, loss_coef):
     """One FP8 expert projection between router and combine: x [T,H] fp32, logits [T,E], w8/sw8 the experts' weights
@@ -132,6 +141,8 @@ def main():
     x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
     a, b = layer.prefill(x)["y"].float(), layer.decode(x, 128)["y"].float()
     print("prefill against decode: %.2e of the norm" % ((a - b).norm() / a.norm()).item())
+    c = layer.few(x[:48])["y"].float()
+    print("few tokens against prefill: %.2e of the norm (its activations are not quantised)" % ((a[:48] - c).norm() / c.norm()).item())
     w = torch.randn(E, 256, H, device="cuda") / math.sqrt(H)
     w8 = torch.empty(E, 256, H, dtype=torch.uint8, device="cuda")
     sw8 = torch.empty(E, 2, H // 128, dtype=torch.float32, device="cuda")
