@@ -239,8 +239,9 @@ int dg_epilogue_bwd(const uint16_t* dy, const uint16_t* pre, int act, uint16_t* 
  *        fp32) or dg_quant_1x128_ue8m0 (DG_SCALE_UE8M0: sf [ceil(K/512)][M] int32)
  *   rstd [M] fp32 or NULL (written): r
  * At least one of y and q is given.  K is a multiple of 8 (with q: of 128) up to
- * 16384, eps positive; sums are fp32, so a row whose sum of squares passes
- * 3.4e38 has r = 0.  Non-finite rows give NaN in y and unspecified codes.
+ * 16384, M below 2^23, eps positive; sums are fp32, so a row whose sum of squares
+ * passes 3.4e38 has r = 0.  A row with a NaN gives NaN in y, one with an infinity
+ * zeros, and NaN at the infinity; codes of such rows are unspecified.
  * Deterministic.
  *
  * dg_rms_norm_bwd: with n = h r,
@@ -521,8 +522,8 @@ int dg_moe_combine_bwd(const void* dy, int dtype, const uint16_t* rows, const in
  * Activations stay bf16: the weights are widened exactly, products are summed in
  * fp32, the inner activations are rounded to bf16 once and y once; a token's
  * experts are added in the order of their numbers (an e2m1 element past bf16's range, scale
- * codes 253 and above, is infinite).  The weights of the chosen experts are read once for up to 32
- * of their tokens.  A choice named twice counts twice.
+ * codes 253 and above, is infinite).  A choice named twice counts twice.  A NaN or infinity
+ * of a token, a weight or an expert stays with the tokens that chose it.
  * T in [0, 64], k in [1, 16], G in [1, 1024], H and I multiples of 128 up to
  * 32768.  workspace: required, dg_get_workspace_size(DG_OP_MOE_EXPERTS, T k, H,
  * I, 1) bytes, which also serve fewer tokens and choices; as for

@@ -820,7 +820,7 @@ int dg_fp8_gemm_nt_epilogue(const uint8_t* A, const float* sfa, const uint8_t* B
   if ((rc = check_activation(act))) return rc;
   if (M == 0) return ok();
   if ((rc = check_operands(A, sfa, B, sfb, D))) return rc;
-  if (pre == D) return fail(DG_ERR_INVALID_ARG, "pre and D must be different arrays");
+  if (pre && (pre == D || pre == residual)) return fail(DG_ERR_INVALID_ARG, "pre must be an array of its own");
   if (!aligned(bias, 16) || !aligned(residual, 16) || !aligned(pre, 16))
     return fail(DG_ERR_ALIGN, "bias, residual and pre must be 16-byte aligned");
   if ((rc = check_workspace(workspace, workspace_bytes))) return rc;

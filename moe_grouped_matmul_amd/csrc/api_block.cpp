@@ -14,7 +14,7 @@ namespace {
 using namespace dg;
 
 constexpr int64_t kIntMax = ((int64_t)1 << 31) - 1;
-constexpr int64_t kMaxWorkgroups = ((int64_t)1 << 24) - 1;  // of 256 threads in a launch: thread counts are 32 bits
+constexpr int64_t kMaxNormRows = ((int64_t)1 << 23) - 1;  // workgroups of up to 512 threads in a launch: thread counts are 32 bits
 
 hipStream_t hs(void* stream) { return static_cast<hipStream_t>(stream); }
 
@@ -28,7 +28,7 @@ int check_norm(int dtype, int weight_dtype, int64_t M, int64_t K) {
   if (K <= 0 || K % 8 || K > kNormMaxK)
     return fail(DG_ERR_SHAPE, "K must be a positive multiple of 8 up to %d (got %lld)", kNormMaxK, (long long)K);
   if (M < 0) return fail(DG_ERR_SHAPE, "M must be >= 0");
-  if (M > kMaxWorkgroups) return fail(DG_ERR_SHAPE, "M too large");
+  if (M > kMaxNormRows) return fail(DG_ERR_SHAPE, "M must be below 2^23 (got %lld)", (long long)M);
   return DG_OK;
 }
 

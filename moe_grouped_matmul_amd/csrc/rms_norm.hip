@@ -254,16 +254,21 @@ __global__ void __launch_bounds__(64 * 16) column_sum_kernel(const float* __rest
   }
 }
 
+// runs of 512 columns that a lane holds of a row
+constexpr int kMostRuns = 4;
+
 template <bool BF16, int KIND, int CH, int NW>
 void norm_one(const NormParams& p, bool nt, hipStream_t stream) {
   constexpr int ROWS = NW <= 4 ? 4 / NW : 1;
   const dim3 grid((unsigned)((p.M + ROWS - 1) / ROWS)), wg(NW <= 4 ? 256 : 64 * NW);
-  if (nt) hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, true>), grid, wg, 0, stream, p);
-  else hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, false>), grid, wg, 0, stream, p);
+  if constexpr (NW == 1 || CH == kMostRuns)  // (shapes of many rows: the others are for few)
+    if (nt) {
+      hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, true>), grid, wg, 0, stream, p);
+      return;
+    }
+  hipLaunchKernelGGL((rms_norm_kernel<BF16, KIND, CH, NW, false>), grid, wg, 0, stream, p);
 }
 
-// runs of 512 columns that a lane holds of a row
-constexpr int kMostRuns = 4;
 template <bool BF16, int KIND, int NW>
 void norm_runs(const NormParams& p, int ch, bool nt, hipStream_t stream) {
   constexpr int MOST = kNormMaxK / 512 / NW < kMostRuns ? kNormMaxK / 512 / NW : kMostRuns;

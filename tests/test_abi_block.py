@@ -36,7 +36,7 @@ def test_norm(lib):
     for kw, want, text in [
         (dict(dtype=2), V, "dtypes"), (dict(wt=-1), V, "dtypes"), (dict(kind=2), V, "scale_kind"),
         (dict(eps=0.0), V, "eps"), (dict(eps=-1.0), V, "eps"), (dict(eps=float("nan")), V, "eps"), (dict(eps=float("inf")), V, "eps"),
-        (dict(K=0), S, "K"), (dict(K=12), S, "K"), (dict(K=16392), S, "K"), (dict(M=-1), S, "M"), (dict(M=1 << 24), S, "M"),
+        (dict(K=0), S, "K"), (dict(K=12), S, "K"), (dict(K=16392), S, "K"), (dict(M=-1), S, "M"), (dict(M=1 << 23), S, "M"),
         (dict(K=136), S, "128"), (dict(x=None), V, "null"), (dict(weight=None), V, "null"), (dict(h=None), V, "null"),
         (dict(q=None, sf=None), V, "null"), (dict(sf=None), V, "null"), (dict(q=None, y=P), V, "null"), (dict(y=P), V, "different"),
         (dict(x=P + 8), A, "16"), (dict(residual=P + 4), A, "16"), (dict(weight=P + 2), A, "16"), (dict(h=P + 8), A, "16"),
@@ -67,7 +67,7 @@ def _epi(lib, A=P, sfa=P, B=P, sfb=P, bias=P, act=2, residual=P, pre=2 * P, D=P,
 def test_epilogue(lib):
     for kw, want, text in [
         (dict(K=100), S, "K"), (dict(N=24), S, "N"), (dict(M=-1), S, "M"), (dict(act=5), V, "activation"), (dict(act=-1), V, "activation"),
-        (dict(A=None), V, "null"), (dict(D=None), V, "null"), (dict(sfb=None), V, "null"), (dict(pre=P), V, "different"),
+        (dict(A=None), V, "null"), (dict(D=None), V, "null"), (dict(sfb=None), V, "null"), (dict(pre=P), V, "own"), (dict(pre=3 * P, residual=3 * P), V, "own"),
         (dict(A=P + 8), A, "16"), (dict(sfa=P + 2), A, "4"), (dict(bias=P + 4), A, "16"), (dict(residual=P + 8), A, "16"),
         (dict(pre=P + 8), A, "16"), (dict(ws=P + 4, n=64), W, "16"), (dict(ws=P, n=3), W, "multiple of 4"),
         (dict(N=1 << 24, K=1 << 10), S, "4 GiB"),
