@@ -17,6 +17,13 @@
 // upper and lower half with different chunks; 8 tokens are its columns, twice
 // too.  The products of unlike halves are of no use, those of like halves are
 // two sums over K that meet at the end: one token costs what eight do.
+//
+// Rates (both kernels, weights alone): one token, 8 of 32 experts, 7168 x 2048
+// e4m3 (352 MB) 62 us, 6.1 and 5.0 TB/s; 48 tokens x 8 of 256, 32 of them here,
+// e2m1 (560 MB) 79-99 us; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB) 68 us,
+// where the activations, read from the L2 caches by every workgroup that needs
+// them, are as many bytes as the weights; one token, 4 of 16 experts, 1024 x
+// 512 (6 MB) 11.4 us, two launches and the order of the choices.
 
 #include "activation.hpp"
 #include "block_internal.hpp"

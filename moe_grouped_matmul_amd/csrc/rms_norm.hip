@@ -7,6 +7,14 @@
 // The norm is of h as it is stored (rounded to its type): what the backward
 // pass reads is then what the forward pass normalised.  Sums and statistics
 // are fp32, v is quantised before any rounding.
+//
+// HBM-bound: a row stays in the registers of its waves between the sum of its
+// squares and the outputs, so x and the residual are read once, and nothing is
+// written that is not asked for.  16384 x 7168 bf16 with residual and codes
+// (826 MB) 146-154 us, 5.4-5.7 TB/s; 8192 x 4096 bf16 without (134 MB) 52 us;
+// its gradient (201 MB, half of it kept by the Infinity Cache) 47 us and 4.8
+// for the weight's.  One row of 7168 is a launch and a chain of loads, sum and
+// quotients: 3.6 us.
 
 #include "block_internal.hpp"
 #include "e4m3.hpp"
@@ -122,7 +130,8 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
 
 // A workgroup of 8 waves takes 8 / NW rows at a time; the gradient of the
 // weight is summed in registers over all its rows, then over its slots, and
-// written as one row of partials that launch_column_sum joins.
+// written as one row of partials that launch_column_sum joins.  Two workgroups
+// a CU, so the partials are 512 rows at most (8 MB of a row of 4096).
 template <bool BF16, int CH, int NW>
 __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwdParams p) {
   constexpr int SLOTS = 8 / NW;
