@@ -100,23 +100,24 @@ __device__ __forceinline__ float scale_of(float amax) {
 
 // q[0..N) = bytes of fl32(x[e] / s), |x[e]| <= 448 s up to rounding.  The
 // hardware's reciprocal (1 ulp) leaves the products within the guard; the nearest
-// to a midpoint and the least of all N tell whether one of them may not be safe
-// (a reciprocal in the normal range bounds the largest), and then those that are
-// not are divided.  A product of zero is the byte of a zero.
+// to a midpoint and the least of all N that is not zero tell whether one of them
+// may not be safe (a reciprocal in the normal range bounds the largest), and then
+// those that are not are divided.  A product of zero is the byte of a zero.
+// (Zeros are common: a bf16 sum of two like values, the slope of a relu.)
 template <int N>
 __device__ __forceinline__ void quotients_of(const float* x, float* y, float s) {
   const float r = __builtin_amdgcn_rcpf(s);
-  uint32_t near = 0xffffffffu;
-  float least = 1.f;
+  uint32_t near = 0xffffffffu, least = 0xffffffffu;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
     y[e] = x[e] * r;
     const uint32_t d = (__float_as_uint(y[e]) + (kGuard - 0x80000u)) & 0xfffffu;  // up to 2 kGuard about a midpoint
     near = d < near ? d : near;
-    least = fminf(least, fabsf(y[e]));
+    const uint32_t m = (__float_as_uint(y[e]) << 1) - 1u;  // by magnitude, zero above all
+    least = m < least ? m : least;
   }
   const bool normal = __float_as_uint(r) - 0x00800000u < 0x7e000000u;
-  if (!(normal && near > 2u * kGuard && least >= __uint_as_float(0x3c800000u + kGuard))) {
+  if (!(normal && near > 2u * kGuard && least >= ((0x3c800000u + kGuard) << 1) - 1u)) {
 #pragma unroll
     for (int e = 0; e < N; ++e)
       if (!normal || !(product_safe(y[e]) || y[e] == 0.f)) y[e] = x[e] / s;

@@ -11,8 +11,8 @@
 // MN-major scales, and sums the bias' gradient in registers over them.  The
 // workgroups' sums meet in launch_column_sum, in order.  4096 x 4096 with the
 // erf gelu, codes and bias (118 MB) 26.7 us, 4.4 TB/s, and 4.9 for the bias;
-// beside the loads the vector units are busy 0.86 of the busy CUs' cycles there
-// (the slope of the gelu and the quotients).
+// beside the loads the vector units are busy 0.84 of the cycles there (the slope
+// of the gelu and the quotients).
 
 #include "activation.hpp"
 #include "block_internal.hpp"
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(256) epilogue_bwd_kernel(EpilogueBwdParams p) 
       for (int e = 0; e < 8; ++e) acc[e] += v[e];
       if (p.dz && in) store8<true>(p.dz, r * p.N + c, rounded<true>(v));
       if constexpr (QUANT) {  // N is a multiple of 128: a group's lanes are all inside or all outside
-        const float s_ = scale_of(max16(max8(v)));
+        const float s_ = scale_of(group_amax(v));
         float y[8];
         quotients_of<8>(v, y, s_);
         if (in) {

@@ -11,7 +11,8 @@
 // HBM-bound: a row stays in the registers of its waves between the sum of its
 // squares and the outputs, so x and the residual are read once, and nothing is
 // written that is not asked for.  16384 x 7168 bf16 with residual and codes
-// (826 MB) 146-154 us, 5.4-5.7 TB/s; 8192 x 4096 bf16 without (134 MB) 52 us;
+// (826 MB) 145-150 us, 5.5-5.7 TB/s, with
+// the vector units busy 0.77 of the cycles beside; 8192 x 4096 bf16 without (134 MB) 52 us;
 // its gradient (201 MB, half of it kept by the Infinity Cache) 47 us and 4.8
 // for the weight's.  One row of 7168 is a launch and a chain of loads, sum and
 // quotients: 3.6 us.
@@ -94,12 +95,15 @@ __global__ void __launch_bounds__(NW <= 4 ? 256 : 64 * NW) rms_norm_kernel(NormP
     const bool in = c < K;
     float v[8], g[8];
     values(h[i], v);
+    // (past K whole groups are outside, and nothing of them is kept)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = 0.f;
     if (in) weights8(p.weight, p.weight_bf16, c, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = in ? (v[e] * r) * g[e] : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = (v[e] * r) * g[e];
     if (p.y && in) store8<BF16, NT>(p.y, at + c, rounded<BF16>(v));
     if constexpr (KIND != kNoQuant) {
-      const float amax = max16(max8(v));
+      const float amax = group_amax(v);
       const int kb = run * 4 + (lane >> 4);
       uint2 out;
       if constexpr (KIND == kScaleUe8m0) {

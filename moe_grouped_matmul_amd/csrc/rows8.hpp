@@ -65,27 +65,44 @@ __device__ __forceinline__ Raw8<BF16> rounded(const float* f) {
   return r;
 }
 
-__device__ __forceinline__ float max8(const float* v) {
-  return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
-               fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
-}
-
 __device__ __forceinline__ float wave_sum(float s) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
   return s;
 }
 
-// largest of 16 neighbouring lanes, in all of them (rotations within the 16)
-__device__ __forceinline__ float max16(float v) {
-#define DG_ROT(n) \
-  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), 0x120 + (n), 0xf, 0xf, false)))
-  DG_ROT(8);
-  DG_ROT(4);
-  DG_ROT(2);
-  DG_ROT(1);
+// Largest magnitude of the 128 values of 16 neighbouring lanes, in all of them: NaN is passed over, and is the result where there
+// is nothing else (as in the quantisers).  A lane's maximum is taken with zero, so that its bits are ordered as it is and a
+// rotation within the 16 is one instruction; a group of zeros and NaN is looked at again.
+__device__ __forceinline__ float group_amax(const float* v) {
+  const float a = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fabsf(v[2]));
+  const float b = fmaxf(fmaxf(fabsf(v[3]), fabsf(v[4])), fabsf(v[5]));
+  const float c = fmaxf(fmaxf(fabsf(v[6]), fabsf(v[7])), 0.f);
+  uint32_t u = __float_as_uint(fmaxf(fmaxf(a, b), c));
+#define DG_ROT(n) (uint32_t) __builtin_amdgcn_update_dpp(0, (int)u, 0x120 + (n), 0xf, 0xf, false)
+#define DG_MAX(n)                   \
+  do {                              \
+    const uint32_t o_ = DG_ROT(n);  \
+    u = o_ > u ? o_ : u;            \
+  } while (0)
+  DG_MAX(8);
+  DG_MAX(4);
+  DG_MAX(2);
+  DG_MAX(1);
+#undef DG_MAX
+  if (u == 0) {  // all 16 lanes
+    bool none = true;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) none &= v[e] != v[e];
+    u = none ? 1u : 0u;
+    u &= DG_ROT(8);
+    u &= DG_ROT(4);
+    u &= DG_ROT(2);
+    u &= DG_ROT(1);
+    if (u) u = 0x7fc00000u;
+  }
 #undef DG_ROT
-  return v;
+  return __uint_as_float(u);
 }
 
 }  // namespace dg
