@@ -12,7 +12,26 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
 
-// Phi(z) of the normal distribution and e^(-z^2 / 2).  The complementary error
+// z Phi(z) = max(z, 0) - a Phi(-a), a = |z|.  log2 Phi(-a) is smooth: a polynomial
+// of degree 8, fitted here to least a Phi(-a) off over [0, 6] (1.4e-8, 5.4e-8 with
+// the fp32 roundings) and falling fast past that, takes eight FMAs and one 2^x,
+// where the formula below takes a reciprocal too and is off by more.  At the end of
+// a 256 x 256 tile it costs 5 us (6.6 with that formula; silu 0.7): less its
+// arithmetic than its 16 KB of straight code, which no cache holds then.
+__device__ __forceinline__ float gelu(float z) {
+  const float a = fminf(fabsf(z), 16.f);  // 2^-3660 there
+  float p = __builtin_fmaf(-2.27583314e-06f, a, 3.29678624e-05f);
+  p = __builtin_fmaf(p, a, -0.000157279617f);
+  p = __builtin_fmaf(p, a, -0.000202473879f);
+  p = __builtin_fmaf(p, a, 0.00714277336f);
+  p = __builtin_fmaf(p, a, -0.0525464304f);
+  p = __builtin_fmaf(p, a, -0.459193051f);
+  p = __builtin_fmaf(p, a, -1.15110695f);
+  p = __builtin_fmaf(p, a, -0.99999994f);
+  return __builtin_fmaf(-a, __builtin_amdgcn_exp2f(p), z < 0.f ? 0.f : z);  // NaN stays
+}
+
+// Phi(z) of the normal distribution and e^(-z^2 / 2), which its slope needs both.  The complementary error
 // function is formula 7.1.26 of Abramowitz and Stegun, Handbook of Mathematical
 // Functions (after Hastings), off by at most 1.5e-7: half of that here, where a
 // bf16 result near 1 is rounded by up to 2e-3.
@@ -34,10 +53,7 @@ template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // NaN stays
   if constexpr (ACT == kActSilu) return z * sigmoid(z);
-  if constexpr (ACT == kActGelu) {
-    float e;
-    return z * normal_cdf(z, &e);
-  }
+  if constexpr (ACT == kActGelu) return gelu(z);
   if constexpr (ACT == kActGeluTanh) return z * sigmoid(kGeluTanh * __builtin_fmaf(0.044715f * z * z, z, z));
   return z;
 }

@@ -44,7 +44,10 @@
 //     split of a tile to finish (agent-scope counter) has every wave read
 //     back its own fragments of all splits, sums them in split order 0, 1, 2,
 //     ... and writes bf16, then resets the counter to zero.  The result is
-//     therefore independent of the order in which splits finish.
+//     therefore independent of the order in which splits finish;
+//   * the epilogue form (D = act(A . B^T + bias) + residual) is the last
+//     split's: 64 x 4096 x 7168 11.7 us with a bias, 11.8 with silu, 12.5 with
+//     gelu, residual and the kept product.
 
 #include "dg_internal.hpp"
 #include "epilogue.hpp"

@@ -11,11 +11,10 @@
 // HBM-bound: a row stays in the registers of its waves between the sum of its
 // squares and the outputs, so x and the residual are read once, and nothing is
 // written that is not asked for.  16384 x 7168 bf16 with residual and codes
-// (826 MB) 145-150 us, 5.5-5.7 TB/s, with
-// the vector units busy 0.77 of the cycles beside; 8192 x 4096 bf16 without (134 MB) 52 us;
-// its gradient (201 MB, half of it kept by the Infinity Cache) 47 us and 4.8
-// for the weight's.  One row of 7168 is a launch and a chain of loads, sum and
-// quotients: 3.6 us.
+// (826 MB) 145-150 us, 5.5-5.7 TB/s, the vector units busy 0.77 of the cycles
+// beside; 8192 x 4096 bf16 with residual (268 MB) 52 us, its gradient (as many)
+// 47 us and 4.8 for the weight's.  One row of 7168 is a launch and a chain of
+// loads, sum and quotients: 3.6 us.
 
 #include "block_internal.hpp"
 #include "e4m3.hpp"
