@@ -79,11 +79,22 @@ __device__ __forceinline__ float exponent_of(uint32_t word, int q) { return __ui
 
 // 16 bytes of each lane to where the products want them: loaded so that four neighbouring lanes have 64 consecutive bytes (row
 // lane / 8, chunk lane % 8, which the address unit takes as one access and not as four), used by the lane of row lane % 8 and
-// chunk lane / 16 + 4 (lane / 8 % 2)
-__device__ __forceinline__ u32x4 spread(int from, u32x4 v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v[i]);
-  return v;
+// chunk lane / 16 + 4 (lane / 8 % 2).  They go through 1 KB of the wave's own LDS, a row's chunks turned about by its number, so
+// that neither side meets another lane's banks: a wave's LDS accesses happen in order, and no wait stands between the two (16
+// cycles of the LDS; four rotations of a register between lanes took 23).  Slots in turn leave the next ones free to be written.
+constexpr int kSpreadSlots = 2;
+struct Spread {
+  u32x4* put;
+  const u32x4* get;
+};
+__device__ __forceinline__ Spread spread_of(u32x4* slots) {
+  const int lane = threadIdx.x & 63;
+  const int r8 = lane & 7, chunk = (lane >> 4) + 4 * ((lane >> 3) & 1);
+  return Spread{slots + (lane & ~7) + ((lane & 7) ^ (lane >> 3)), slots + 8 * r8 + (chunk ^ r8)};
+}
+__device__ __forceinline__ u32x4 spread(const Spread& s, int turn, u32x4 v) {
+  s.put[64 * (turn % kSpreadSlots)] = v;
+  return s.get[64 * (turn % kSpreadSlots)];
 }
 
 // the sum of both like halves of a product, in both
@@ -203,9 +214,11 @@ constexpr int up_depth(int mg, int maxmg) {
   return maxmg == 2 ? (mg == 1 ? 3 : 1) : (mg == 1 ? 2 : 1);
 }
 
-struct UpShared {
+template <int MAXMG>
+struct __attribute__((aligned(16))) UpShared {
   Members members;
-  __attribute__((aligned(16))) f32x4 part[2][3][16][16];  // [turn][wave - 1][accumulator][lane]
+  f32x4 part[2][3][4 * MAXMG][16];  // [turn][wave - 1][accumulator][lane]
+  u32x4 spread[kUpThreads / 64][64 * kSpreadSlots];
 };
 
 // A pass of 8 MG tokens, from m0 on, of unit u (all uniform)
@@ -234,7 +247,7 @@ __device__ __forceinline__ int up_groups(const UpItem& it) {
 
 // the passes of this workgroup from `it` on, as long as they are of MG groups; returns whether one is left, which is in `it`
 template <int FMT, int MG, int MAXMG, bool NT>
-__device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared& sh, UpItem& it, int units, int stride, int& turn) {
+__device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG>& sh, UpItem& it, int units, int stride, int& turn) {
   constexpr int D = up_depth<FMT>(MG, MAXMG);
   constexpr int P = kParts<FMT>;
   const Members& s = sh.members;
@@ -255,7 +268,7 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared& sh, 
   const int padded = (per + D - 1) / D * D;
   // loads: row (or token) lane / 8, chunk lane % 8; weight rows 2 (lane / 8) + a: neighbours, whose scale words are loaded together
   const int l8 = lane >> 3, ch = lane & 7;
-  const int from = 4 * (8 * r8 + q + 4 * half);
+  const Spread sp = spread_of(sh.spread[wave]);
   uint32_t w_off[2];
 #pragma unroll
   for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(2 * l8 + a) * row_bytes + 16u * ch;
@@ -351,14 +364,14 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared& sh, 
 #pragma unroll
         for (int g = 0; g < MG; ++g)
 #pragma unroll
-          for (int t = 0; t < P; ++t) y[g][t] = spread(from, xr[d][g][t]);
+          for (int t = 0; t < P; ++t) y[g][t] = spread(sp, g * P + t, xr[d][g][t]);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const float beta = FMT == kFp8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cur.beta[b]), i)) : 1.f;
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             const float ex = FMT == kFp4 ? exponent_of(sc[d][b][a], q) : 1.f;
-            const u32x4 chunk = spread(from, w[d][b][a]);
+            const u32x4 chunk = spread(sp, a, w[d][b][a]);
             bf16x8 v[P];
 #pragma unroll
             for (int t = 0; t < P; ++t) v[t] = widened<FMT>(chunk, t, ex);
@@ -421,7 +434,7 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared& sh, 
 
 template <int FMT, int MAXMG, bool NT>
 __global__ void __launch_bounds__(kUpThreads) experts_up_kernel(ExpertsParams p) {
-  __shared__ UpShared sh;
+  __shared__ UpShared<MAXMG> sh;
   read_members(p, sh.members);
   // as many workgroups as give each the same number of units, or one less
   const int tiles = p.I >> 4;
@@ -460,7 +473,7 @@ constexpr int down_depth(int mg) {
 
 // the wave's part: its run of the steps, into its sums
 template <int FMT, int MG, bool FEW, bool NT>
-__device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTable& s, f32x4* sums, int c0, int slot, int slots) {
+__device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTable& s, f32x4* sums, u32x4* slots_of_wave, int c0, int slot, int slots) {
   constexpr int D = down_depth<FMT, FEW>(MG);
   constexpr int P = kParts<FMT>;
   const int lane = threadIdx.x & 63;
@@ -478,7 +491,7 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     const uint32_t w_bytes = H * row_bytes;
     // loads: row (or token) lane / 8, chunk lane % 8; weight rows c0 + 2 (lane / 8) + a
     const int l8 = lane >> 3, ch = lane & 7;
-    const int from = 4 * (8 * r8 + q + 4 * half);
+    const Spread sp = spread_of(slots_of_wave);
     uint32_t w_off[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(c0 + 2 * l8 + a) * row_bytes + 16u * ch;
@@ -608,7 +621,7 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
           const float ex = FMT == kFp4 ? exponent_of(sc[d][a], q) : 1.f;
-          const u32x4 chunk = spread(from, w[d][a]);
+          const u32x4 chunk = spread(sp, a, w[d][a]);
 #pragma unroll
           for (int t = 0; t < P; ++t) v[a][t] = widened<FMT>(chunk, t, ex);
         }
@@ -617,7 +630,7 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
           if (g > 0 && g >= gr[d]) break;  // uniform
           u32x4 x[P];
 #pragma unroll
-          for (int t = 0; t < P; ++t) x[t] = spread(from, hr[d][g][t]);
+          for (int t = 0; t < P; ++t) x[t] = spread(sp, t, hr[d][g][t]);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
             f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[g][a];
@@ -645,6 +658,7 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
   constexpr int THREADS = 64 * W;
   __shared__ ExpertsTable s;
   __shared__ __attribute__((aligned(16))) f32x4 sums[W][(FEW ? 8 : kExpertsMaxTokens) * (kDownCols / 4)];  // [token][four columns]
+  __shared__ __attribute__((aligned(16))) u32x4 spread_s[W][64 * kSpreadSlots];
   __shared__ int last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -663,15 +677,15 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
   __syncthreads();
   const int slot = split * W + wave, slots = W * p.splits;
   if constexpr (FEW) {
-    down_run<FMT, 1, FEW, NT>(p, s, sums[wave], c0, slot, slots);
+    down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   } else {
     // tokens of an expert on average: an expert of more takes its steps group by group
     const int chosen = __builtin_amdgcn_readfirstlane(s.n);
     const uint32_t end = chosen > 0 ? __builtin_amdgcn_readfirstlane(s.run[chosen - 1]) : 0u;
     const int entries = chosen > 0 ? start_of(end) + count_of(end) : 0;
-    if (entries <= 6 * chosen) down_run<FMT, 1, FEW, NT>(p, s, sums[wave], c0, slot, slots);
-    else if (entries <= 12 * chosen) down_run<FMT, 2, FEW, NT>(p, s, sums[wave], c0, slot, slots);
-    else down_run<FMT, 4, FEW, NT>(p, s, sums[wave], c0, slot, slots);
+    if (entries <= 6 * chosen) down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
+    else if (entries <= 12 * chosen) down_run<FMT, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
+    else down_run<FMT, 4, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   }
   __syncthreads();
   // the waves' sums in order: a thread takes four columns of a token
