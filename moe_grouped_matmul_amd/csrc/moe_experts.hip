@@ -86,11 +86,15 @@ constexpr int kSpreadSlots = 2;
 struct Spread {
   u32x4* put;
   const u32x4* get;
+  const u32x4* get16;  // of two slots together: row lane % 16, chunk lane / 16, and from those of the upper half the chunks past 4
+  int upper;
 };
 __device__ __forceinline__ Spread spread_of(u32x4* slots) {
   const int lane = threadIdx.x & 63;
   const int r8 = lane & 7, chunk = (lane >> 4) + 4 * ((lane >> 3) & 1);
-  return Spread{slots + (lane & ~7) + ((lane & 7) ^ (lane >> 3)), slots + 8 * r8 + (chunk ^ r8)};
+  const int row = 64 * ((lane >> 3) & 1) + 8 * r8, low = (lane >> 4) ^ r8;
+  return Spread{slots + (lane & ~7) + ((lane & 7) ^ (lane >> 3)), slots + 8 * r8 + (chunk ^ r8), slots + row + low,
+                (low ^ 4) - low};
 }
 __device__ __forceinline__ u32x4 spread(const Spread& s, int turn, u32x4 v) {
   s.put[64 * (turn % kSpreadSlots)] = v;
@@ -106,6 +110,14 @@ __device__ __forceinline__ f32x4 halves(f32x4 v) {
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// two registers of 8 rows each as both halves of the chunks of 16 rows
+__device__ __forceinline__ void spread16(const Spread& s, u32x4 rows0, u32x4 rows8, u32x4 (&out)[2]) {
+  s.put[0] = rows0;
+  s.put[64] = rows8;
+  out[0] = s.get16[0];
+  out[1] = s.get16[s.upper];
 }
 
 // ---- who chose what.  Every workgroup of the first kernel sorts the choices by expert; its first leaves the result for the second.
@@ -238,11 +250,11 @@ __device__ __forceinline__ UpItem up_item(const Members& s, int u, int m0, int t
   r.i0 = (u - a * tiles) * 16;
   return r;
 }
-// groups of 8 that share the pass: 1, 2 or 4
+// groups of 8 that share the pass: 1, 2 or 4.  One and more than one add in different orders, and which tokens a last pass has is
+// not the same in every run: so an expert of more than 8 tokens takes none of one group.
 template <int MAXMG>
 __device__ __forceinline__ int up_groups(const UpItem& it) {
-  const int left = it.m - it.m0;
-  return left > 8 * 2 && MAXMG > 2 ? 4 : left > 8 ? 2 : 1;
+  return it.m - it.m0 > 8 * 2 && MAXMG > 2 ? 4 : it.m > 8 ? 2 : 1;
 }
 
 // the passes of this workgroup from `it` on, as long as they are of MG groups; returns whether one is left, which is in `it`
@@ -271,8 +283,8 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
   const Spread sp = spread_of(sh.spread[wave]);
   uint32_t w_off[2];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(2 * l8 + a) * row_bytes + 16u * ch;
-  const uint32_t s_off = (half * 2 * I + 2 * r8) * 4u;
+  for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(MG == 1 ? 2 * l8 + a : 8 * a + l8) * row_bytes + 16u * ch;
+  const uint32_t s_off = (MG == 1 ? half * 2 * I + 2 * r8 : (uint32_t)(lane & 15)) * 4u;
 
   // a pass' own: where its weights and tokens are, and the block scales of the wave's steps, one to a lane (e4m3)
   struct Own {
@@ -324,7 +336,12 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(static_cast<const uint8_t*>(p.s1) + (int64_t)o.expert * s_bytes, in ? s_bytes : 0u);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        sc[d][b] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
+        if constexpr (MG == 1) {
+          sc[d][b] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
+        } else {
+          sc[d][b][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
+          sc[d][b][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off, ((k * 4u + 2u) * I + b * I + (uint32_t)o.i0) * 4u, 0);
+        }
     }
 #pragma unroll
     for (int g = 0; g < MG; ++g)
@@ -344,13 +361,12 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
     else left = false;
     const bool on = left && up_groups<MAXMG>(next) == MG;
     const Own then = own_of(next, on);
-    f32x4 c[2][2][MG];
+    constexpr int Q = MG == 1 ? 2 : MG / 2;  // accumulators of 16 rows: of the rows 2 i and 2 i + 1, or of 16 tokens each
+    f32x4 c[2][Q];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int g = 0; g < MG; ++g) c[b][a][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int a = 0; a < Q; ++a) c[b][a] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < padded; k0 += D) {
       const bool ahead = k0 + D >= padded;  // the loads of this turn are the next pass'
       Own o = cur;
@@ -360,69 +376,100 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
         __builtin_amdgcn_sched_barrier(0);
         // a lane's: a wave has at most 64 steps, and past them lanes hold zero, or the step's products are zero
         const int i = k0 + d < 63 ? k0 + d : 63;
-        u32x4 y[MG][P];
+        float beta[2] = {1.f, 1.f};
+        if constexpr (FMT == kFp8)
 #pragma unroll
-        for (int g = 0; g < MG; ++g)
+          for (int b = 0; b < 2; ++b) beta[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cur.beta[b]), i));
+        auto add = [&](int b, int a, f32x4 z) {
+          if constexpr (FMT == kFp8) {
 #pragma unroll
-          for (int t = 0; t < P; ++t) y[g][t] = spread(sp, g * P + t, xr[d][g][t]);
+            for (int e = 0; e < 4; ++e) c[b][a][e] = __builtin_fmaf(z[e], beta[b], c[b][a][e]);
+          } else {
+            c[b][a] = z;
+          }
+        };
+        if constexpr (MG == 1) {
+          u32x4 y[P];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const float beta = FMT == kFp8 ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cur.beta[b]), i)) : 1.f;
+          for (int t = 0; t < P; ++t) y[t] = spread(sp, t, xr[d][0][t]);
 #pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            const float ex = FMT == kFp4 ? exponent_of(sc[d][b][a], q) : 1.f;
-            const u32x4 chunk = spread(sp, a, w[d][b][a]);
-            bf16x8 v[P];
+          for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int t = 0; t < P; ++t) v[t] = widened<FMT>(chunk, t, ex);
+            for (int a = 0; a < 2; ++a) {
+              const float ex = FMT == kFp4 ? exponent_of(sc[d][b][a], q) : 1.f;
+              const u32x4 chunk = spread(sp, a, w[d][b][a]);
+              f32x4 z = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a];
 #pragma unroll
-            for (int g = 0; g < MG; ++g) {
-              f32x4 z = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a][g];
+              for (int t = 0; t < P; ++t) z = mfma(widened<FMT>(chunk, t, ex), y[t], z);
+              add(b, a, z);
+            }
+        } else {
+          u32x4 y[MG / 2][P][2];
 #pragma unroll
-              for (int t = 0; t < P; ++t) z = mfma(v[t], y[g][t], z);
-              if constexpr (FMT == kFp8) {
+          for (int g = 0; g < MG; g += 2)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) c[b][a][g][e] = __builtin_fmaf(z[e], beta, c[b][a][g][e]);
-              } else {
-                c[b][a][g] = z;
+            for (int t = 0; t < P; ++t) spread16(sp, xr[d][g][t], xr[d][g + 1][t], y[g / 2][t]);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            u32x4 chunk[2];
+            spread16(sp, w[d][b][0], w[d][b][1], chunk);
+            f32x4 z[MG / 2];
+#pragma unroll
+            for (int a = 0; a < MG / 2; ++a) z[a] = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a];
+#pragma unroll
+            for (int s2 = 0; s2 < 2; ++s2) {
+              const float ex = FMT == kFp4 ? exponent_of(sc[d][b][s2], q) : 1.f;
+#pragma unroll
+              for (int t = 0; t < P; ++t) {
+                const bf16x8 v = widened<FMT>(chunk[s2], t, ex);
+#pragma unroll
+                for (int a = 0; a < MG / 2; ++a) z[a] = mfma(v, y[a][t][s2], z[a]);
               }
             }
+#pragma unroll
+            for (int a = 0; a < MG / 2; ++a) add(b, a, z[a]);
           }
         }
         load(d, o, ahead ? d : k0 + D + d);
       }
     }
-    // the waves' sums, in order; lanes (token r8, q < 2) of the lower half have weight rows 8 q + 2 e + a
-    const int at = r8 | (q << 3);
-    const bool mine = !half && q < 2;
+    // the waves' sums, in order: `part` has four places of 16 lanes for every 16 accumulators of a column
+    const int at = MG == 1 ? r8 | (q << 3) : lane & 15;
+    const bool mine = MG > 1 || (!half && q < 2);  // one row of tokens: lanes (token r8, q < 2) of the lower half have weight rows 8 q + 2 e + a
+    auto place = [&](int b, int a) { return MG == 1 ? b * 2 + a : (a * 2 + b) * 4 + q; };
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
-#pragma unroll
-        for (int g = 0; g < MG; ++g) {
-          c[b][a][g] = halves(c[b][a][g]);
-          if (wave > 0 && mine) sh.part[turn][wave - 1][(g * 2 + b) * 2 + a][at] = c[b][a][g];
-        }
+      for (int a = 0; a < Q; ++a) {
+        if constexpr (MG == 1) c[b][a] = halves(c[b][a]);
+        if (wave > 0 && mine) sh.part[turn][wave - 1][place(b, a)][at] = c[b][a];
+      }
     __syncthreads();  // (the other half of `part` is what the next pass writes)
     if (wave == 0 && mine) {
+      f32x4 v[Q];
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        const int r = it.m0 + 8 * g + r8;
-        float v[8];
+      for (int a = 0; a < Q; ++a) {
+        f32x4 z[2] = {c[0][a], c[1][a]};
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          f32x4 z[2] = {c[0][a][g], c[1][a][g]};
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int u = 0; u < 3; ++u) z[b] += sh.part[turn][u][place(b, a)][at];
 #pragma unroll
-            for (int u = 0; u < 3; ++u) z[b] += sh.part[turn][u][(g * 2 + b) * 2 + a][at];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[2 * e + a] = activate<kActSilu>(z[0][e]) * z[1][e];
-        }
+        for (int e = 0; e < 4; ++e) v[a][e] = activate<kActSilu>(z[0][e]) * z[1][e];
+      }
+      if constexpr (MG == 1) {
+        const int r = it.m0 + r8;
         if (r < it.m)
           *reinterpret_cast<uint4*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 8 * q) =
-              uint4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+              uint4{pack_bf16x2(v[0][0], v[1][0]), pack_bf16x2(v[0][1], v[1][1]), pack_bf16x2(v[0][2], v[1][2]), pack_bf16x2(v[0][3], v[1][3])};
+      } else {
+#pragma unroll
+        for (int a = 0; a < Q; ++a) {
+          const int r = it.m0 + 16 * a + (lane & 15);
+          if (r < it.m)
+            *reinterpret_cast<uint2*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 4 * q) =
+                uint2{pack_bf16x2(v[a][0], v[a][1]), pack_bf16x2(v[a][2], v[a][3])};
+        }
       }
     }
     turn ^= 1;
@@ -494,10 +541,12 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     const Spread sp = spread_of(slots_of_wave);
     uint32_t w_off[2];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(c0 + 2 * l8 + a) * row_bytes + 16u * ch;
+    for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(c0 + (MG == 1 ? 2 * l8 + a : 8 * a + l8)) * row_bytes + 16u * ch;
     // scales: e4m3 [ceil(H / 128)][KB] fp32, e2m1 words [KB][H]
     const uint32_t s_bytes = FMT == kFp8 ? ((H + 127) >> 7) * (uint32_t)KB * 4u : (uint32_t)KB * H * 4u;
-    const uint32_t s_off = FMT == kFp8 ? (uint32_t)(c0 >> 7) * (uint32_t)KB * 4u : (half * H + (uint32_t)(c0 + 2 * r8)) * 4u;
+    const uint32_t s_off = FMT == kFp8 ? (uint32_t)(c0 >> 7) * (uint32_t)KB * 4u
+                           : MG == 1    ? (half * H + (uint32_t)(c0 + 2 * r8)) * 4u
+                                        : (uint32_t)(c0 + (lane & 15)) * 4u;
     const uint32_t s_step = FMT == kFp8 ? 4u : 8u * H;
     const uint32_t h_bytes = (uint32_t)p.T * (uint32_t)p.k * I * 2u;
 
@@ -508,9 +557,10 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     int ld_k = k_lo, ld_g = 0, ld_n = 1, first = 0, members = 0;
     const uint8_t* wbase = p.w2;
     const uint8_t* sbase = static_cast<const uint8_t*>(p.s2);
+    constexpr int N = MG == 1 ? 1 : MG / 2;  // tokens of a lane's columns: one of 8, or one of every 16
     uint32_t h_off[MG];
-    float fac[MG];
-    int token[MG];
+    float fac[N];
+    int token[N];
     auto enter_expert = [&]() {
       const uint32_t r = __builtin_amdgcn_readfirstlane(s.run[ld_a]);
       const int e = expert_of(r);
@@ -527,8 +577,12 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       for (int g = 0; g < MG; ++g) {
         const int r = 8 * (MG * ld_g + g);
         h_off[g] = r + l8 < members ? (s.entry[first + r + l8] & 0xffffu) * I * 2u + 16u * P * ch : kOOB;
-        fac[g] = r + r8 < members ? s.weight[first + r + r8] : 0.f;
-        token[g] = r + r8 < members ? (int)(s.entry[first + r + r8] >> 16) : -1;
+      }
+#pragma unroll
+      for (int g = 0; g < N; ++g) {
+        const int r = 8 * MG * ld_g + (MG == 1 ? r8 : 16 * g + (lane & 15));
+        fac[g] = r < members ? s.weight[first + r] : 0.f;
+        token[g] = r < members ? (int)(s.entry[first + r] >> 16) : -1;
       }
     };
     enter_expert();
@@ -538,8 +592,8 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     u32x4 w[D][2];
     u32x2 sc[D];
     u32x4 hr[D][MG][P];
-    float fr[D][MG];
-    int tr[D][MG];
+    float fr[D][N];
+    int tr[D][N];
     bool nr[D], vr[D];
     int gr[D];  // groups of 8 that hold a token
     auto load = [&](int d) {
@@ -564,12 +618,18 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
 #pragma unroll
       for (int a = 0; a < 2; ++a) w[d][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], k * 128u, NT ? kStream : 0);
       if constexpr (FMT == kFp8) sc[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
-      else sc[d] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, k * s_step, 0);
+      else if constexpr (MG == 1) sc[d] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, k * s_step, 0);
+      else {
+        sc[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
+        sc[d][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off, k * s_step + 4u * H, 0);
+      }
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
+      for (int g = 0; g < MG; ++g)
 #pragma unroll
         for (int t = 0; t < P; ++t)
           hr[d][g][t] = __builtin_amdgcn_raw_buffer_load_b128(rh, cut || h_off[g] == kOOB ? kOOB : h_off[g] + 16u * t, k * 2u * kStepDepth<FMT>, 0);
+#pragma unroll
+      for (int g = 0; g < N; ++g) {
         fr[d][g] = fac[g];
         tr[d][g] = token[g];
       }
@@ -579,27 +639,35 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       fresh = false;
       if (in) ++ld_k;
     };
-    f32x4 acc[MG][2];
-    int to[MG];
-    float by[MG];
-    // the accumulators into the sums: lanes (token r8, q < 2) of the lower half have columns 8 q + 2 e + a
-    auto flush = [&]() {
+    constexpr int Q = MG == 1 ? 2 : N;  // accumulators: of the rows 2 i and 2 i + 1, or of 16 tokens each
+    f32x4 acc[Q];
+    int to[N];
+    float by[N];
+    auto clear = [&]() {
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        const f32x4 x = halves(acc[g][0]), y = halves(acc[g][1]);
-        if (to[g] >= 0 && !half && q < 2) {
-          f32x4* at = &sums[to[g] * (kDownCols / 4) + 2 * q];
-          at[0] += f32x4{x[0], y[0], x[1], y[1]} * by[g];
-          at[1] += f32x4{x[2], y[2], x[3], y[3]} * by[g];
+      for (int a = 0; a < Q; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+    };
+    // the accumulators into the sums: of 8 tokens lanes (token r8, q < 2) of the lower half have columns 8 q + 2 e + a
+    auto flush = [&]() {
+      if constexpr (MG == 1) {
+        const f32x4 x = halves(acc[0]), y = halves(acc[1]);
+        if (to[0] >= 0 && !half && q < 2) {
+          f32x4* at = &sums[to[0] * (kDownCols / 4) + 2 * q];
+          at[0] += f32x4{x[0], y[0], x[1], y[1]} * by[0];
+          at[1] += f32x4{x[2], y[2], x[3], y[3]} * by[0];
         }
+      } else {
+#pragma unroll
+        for (int a = 0; a < Q; ++a)
+          if (to[a] >= 0) sums[to[a] * (kDownCols / 4) + q] += acc[a] * by[a];
       }
     };
 #pragma unroll
-    for (int g = 0; g < MG; ++g) {
+    for (int g = 0; g < N; ++g) {
       to[g] = -1;
       by[g] = 0.f;
-      acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    clear();
 #pragma unroll
     for (int d = 0; d < D; ++d) load(d);
     bool any = false, more = true;
@@ -611,37 +679,55 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
           if (any) flush();
           any = true;
 #pragma unroll
-          for (int g = 0; g < MG; ++g) {
+          for (int g = 0; g < N; ++g) {
             to[g] = tr[d][g];
             by[g] = fr[d][g];
-            acc[g][0] = acc[g][1] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
+          clear();
         }
-        bf16x8 v[2][P];
+        auto add = [&](int a, f32x4 o) {
+          if constexpr (FMT == kFp8) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const float ex = FMT == kFp4 ? exponent_of(sc[d][a], q) : 1.f;
-          const u32x4 chunk = spread(sp, a, w[d][a]);
-#pragma unroll
-          for (int t = 0; t < P; ++t) v[a][t] = widened<FMT>(chunk, t, ex);
-        }
-#pragma unroll
-        for (int g = 0; g < MG; ++g) {
-          if (g > 0 && g >= gr[d]) break;  // uniform
+            for (int e = 0; e < 4; ++e) acc[a][e] = __builtin_fmaf(o[e], __uint_as_float(sc[d][0]), acc[a][e]);
+          } else {
+            acc[a] = o;
+          }
+        };
+        if constexpr (MG == 1) {
           u32x4 x[P];
 #pragma unroll
-          for (int t = 0; t < P; ++t) x[t] = spread(sp, t, hr[d][g][t]);
+          for (int t = 0; t < P; ++t) x[t] = spread(sp, t, hr[d][0][t]);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
-            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[g][a];
+            const float ex = FMT == kFp4 ? exponent_of(sc[d][a], q) : 1.f;
+            const u32x4 chunk = spread(sp, a, w[d][a]);
+            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a];
 #pragma unroll
-            for (int t = 0; t < P; ++t) o = mfma(v[a][t], x[t], o);
-            if constexpr (FMT == kFp8) {
+            for (int t = 0; t < P; ++t) o = mfma(widened<FMT>(chunk, t, ex), x[t], o);
+            add(a, o);
+          }
+        } else {
+          u32x4 chunk[2];
+          spread16(sp, w[d][0], w[d][1], chunk);
+          bf16x8 v[2][P];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[g][a][e] = __builtin_fmaf(o[e], __uint_as_float(sc[d][0]), acc[g][a][e]);
-            } else {
-              acc[g][a] = o;
+          for (int s2 = 0; s2 < 2; ++s2) {
+            const float ex = FMT == kFp4 ? exponent_of(sc[d][s2], q) : 1.f;
+#pragma unroll
+            for (int t = 0; t < P; ++t) v[s2][t] = widened<FMT>(chunk[s2], t, ex);
+          }
+#pragma unroll
+          for (int a = 0; a < Q; ++a) {
+            if (a > 0 && 2 * a >= gr[d]) break;  // uniform
+            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a];
+#pragma unroll
+            for (int t = 0; t < P; ++t) {
+              u32x4 x[2];
+              spread16(sp, hr[d][2 * a][t], hr[d][2 * a + 1][t], x);
+#pragma unroll
+              for (int s2 = 0; s2 < 2; ++s2) o = mfma(v[s2][t], x[s2], o);
             }
+            add(a, o);
           }
         }
         load(d);
