@@ -16,14 +16,17 @@
 // 8 % 2), and the matrix cores' 16 x 16 product takes the 8 rows twice, in its
 // upper and lower half with different chunks; 8 tokens are its columns, twice
 // too.  The products of unlike halves are of no use, those of like halves are
-// two sums over K that meet at the end: one token costs what eight do.
+// two sums over K that meet at the end: one token costs what eight do.  Where an
+// expert has more, two such loads are turned into whole products of 16 rows and
+// 16 tokens, one half of the chunks after the other.
 //
 // Rates (both kernels, weights alone): one token, 8 of 32 experts, 7168 x 2048
 // e4m3 (352 MB) 62 us, 6.1 and 5.0 TB/s; 48 tokens x 8 of 256, 32 of them here,
-// e2m1 (560 MB) 79-99 us; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB) 68 us,
-// where the activations, read from the L2 caches by every workgroup that needs
-// them, are as many bytes as the weights; one token, 4 of 16 experts, 1024 x
-// 512 (6 MB) 11.4 us, two launches and the order of the choices.
+// e2m1 (560 MB) 79-101 us; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB) 54-63
+// us, where the address units are busy 0.7 of the cycles: the activations, read
+// from the L2 caches by every workgroup that needs them, take more of their time
+// than the weights; one token, 4 of 16 experts, 1024 x 512 (6 MB) 11.4 us, two
+// launches and the order of the choices.
 
 #include "activation.hpp"
 #include "block_internal.hpp"
@@ -137,7 +140,15 @@ __device__ __forceinline__ int count_of(uint32_t r) { return (int)((r >> 10) & 6
 __device__ __forceinline__ int start_of(uint32_t r) { return (int)(r >> 16); }
 static_assert(kExpertsMaxGroups <= 1024 && kExpertsMaxTokens <= 64 && kExpertsMaxChoices <= 65536, "the words of the table");
 
+// the tokens of all chosen experts
+__device__ __forceinline__ int entries_of(const ExpertsTable& s) {
+  const int n = __builtin_amdgcn_readfirstlane(s.n);
+  const uint32_t end = n > 0 ? __builtin_amdgcn_readfirstlane(s.run[n - 1]) : 0u;
+  return n > 0 ? start_of(end) + count_of(end) : 0;
+}
+
 constexpr int kUpThreads = 256;
+constexpr int kPairTokens = 6;  // tokens of an expert on average from which neighbouring units are taken together
 
 __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s) {
   constexpr int EACH = kExpertsMaxChoices / kUpThreads;
@@ -215,13 +226,19 @@ __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s)
 }
 
 // ---- gate and up projection.  A unit is 16 columns of h of one chosen expert (16 rows of the gate and of the up weights); a
-// workgroup takes every so-manyth unit, its four waves a quarter of H each, and the next unit's first steps are in flight while
-// the current one ends.  An expert's tokens share a pass over the weights, up to 8 MAXMG of them.
+// workgroup takes a run of units (or every so-manyth), its four waves a quarter of H each, and the next pass' first steps are in
+// flight while the current one ends.  An expert's tokens share a pass over the weights, up to 8 MAXMG of them.  Where there are
+// more than 8, two neighbouring units of a run are one pass: the tokens' activations, which the address unit takes as long for as
+// for the weights, are loaded for both (8 experts, 64 tokens, 4096 x 2048: 34.8
+// -> 33.4 us of this kernel).  Fewer are taken unit by unit, neighbouring workgroups on neighbouring units (48 tokens of 1.5 an
+// expert 61.5 us, 68 in runs).
 
-// steps in flight: (weights and activations of) a step take 16 + 8 registers for every 8 tokens of e4m3, 20 + 16 of e2m1, and the
-// accumulators 16 for every 8 tokens
+// steps in flight: (weights and activations of) a step take 16 + 8 registers for every 8 tokens of e4m3, 20 + 16 of e2m1, twice
+// those of the weights for two units.  More are no faster: a wave has few steps of a row, padded to whole turns (16 to 32 tokens
+// of 4096 x 2048, three in place of two: 36.0 -> 36.8 us)
 template <int FMT>
-constexpr int up_depth(int mg, int maxmg) {
+constexpr int up_depth(int mg, int c, int maxmg) {
+  if (c == 2) return FMT == kFp8 ? 2 : mg == 2 ? 2 : 1;
   if (FMT == kFp8) return maxmg == 2 ? 2 : mg == 1 ? 4 : mg == 2 ? 3 : 2;
   return maxmg == 2 ? (mg == 1 ? 3 : 1) : (mg == 1 ? 2 : 1);
 }
@@ -256,11 +273,19 @@ template <int MAXMG>
 __device__ __forceinline__ int up_groups(const UpItem& it) {
   return it.m - it.m0 > 8 * 2 && MAXMG > 2 ? 4 : it.m > 8 ? 2 : 1;
 }
+// units of the pass: two that share their block scales
+struct UpRun {
+  int end, step;  // the workgroup's units are every `step`th before `end`
+};
+template <int MAXMG>
+__device__ __forceinline__ int up_units(const UpItem& it, const UpRun& run) {
+  return MAXMG > 2 && run.step == 1 && it.m > 8 && it.u % 2 == 0 && it.u + 1 < run.end ? 2 : 1;
+}
 
-// the passes of this workgroup from `it` on, as long as they are of MG groups; returns whether one is left, which is in `it`
-template <int FMT, int MG, int MAXMG, bool NT>
-__device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG>& sh, UpItem& it, int units, int stride, int& turn) {
-  constexpr int D = up_depth<FMT>(MG, MAXMG);
+// the passes of this workgroup from `it` on, as long as they are of MG groups and C units; returns whether one is left, which is in `it`
+template <int FMT, int MG, int C, int MAXMG, bool NT>
+__device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG>& sh, UpItem& it, const UpRun& run, int& turn) {
+  constexpr int D = up_depth<FMT>(MG, C, MAXMG);
   constexpr int P = kParts<FMT>;
   const Members& s = sh.members;
   const int lane = threadIdx.x & 63;
@@ -281,9 +306,9 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
   // loads: row (or token) lane / 8, chunk lane % 8; weight rows 2 (lane / 8) + a: neighbours, whose scale words are loaded together
   const int l8 = lane >> 3, ch = lane & 7;
   const Spread sp = spread_of(sh.spread[wave]);
-  uint32_t w_off[2];
+  uint32_t w_off[2 * C];
 #pragma unroll
-  for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(MG == 1 ? 2 * l8 + a : 8 * a + l8) * row_bytes + 16u * ch;
+  for (int a = 0; a < 2 * C; ++a) w_off[a] = (uint32_t)(MG == 1 ? 2 * l8 + a : 8 * a + l8) * row_bytes + 16u * ch;
   const uint32_t s_off = (MG == 1 ? half * 2 * I + 2 * r8 : (uint32_t)(lane & 15)) * 4u;
 
   // a pass' own: where its weights and tokens are, and the block scales of the wave's steps, one to a lane (e4m3)
@@ -315,8 +340,8 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
     return o;
   };
 
-  u32x4 w[D][2][2];
-  u32x2 sc[D][2];
+  u32x4 w[D][2][2 * C];
+  u32x2 sc[D][2][C];
   u32x4 xr[D][MG][P];
   // step i of a pass into stage d; empty ranges past its last step: zeros, and no traffic; so are the upper chunks of a last
   // half step of e2m1
@@ -330,17 +355,21 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int a = 0; a < 2 * C; ++a)
         w[d][b][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], (b * I + (uint32_t)o.i0) * row_bytes + k * 128u, NT ? kStream : 0);
     if constexpr (FMT == kFp4) {  // the words of step k are 2 k and 2 k + 1 of a row
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(static_cast<const uint8_t*>(p.s1) + (int64_t)o.expert * s_bytes, in ? s_bytes : 0u);
 #pragma unroll
       for (int b = 0; b < 2; ++b)
         if constexpr (MG == 1) {
-          sc[d][b] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
+          sc[d][b][0] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
         } else {
-          sc[d][b][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, (k * 4u * I + b * I + (uint32_t)o.i0) * 4u, 0);
-          sc[d][b][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off, ((k * 4u + 2u) * I + b * I + (uint32_t)o.i0) * 4u, 0);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const uint32_t at = (k * 4u * I + b * I + (uint32_t)o.i0) * 4u;
+            sc[d][b][c][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off + 64u * c, at, 0);
+            sc[d][b][c][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off + 64u * c, at + 8u * I, 0);
+          }
         }
     }
 #pragma unroll
@@ -357,16 +386,18 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
     UpItem next = it;
     bool left = true;
     if (it.m0 + 8 * MG < it.m) next.m0 += 8 * MG;
-    else if (it.u + stride < units) next = up_item(s, it.u + stride, 0, tiles);
+    else if (it.u + C * run.step < run.end) next = up_item(s, it.u + C * run.step, 0, tiles);
     else left = false;
-    const bool on = left && up_groups<MAXMG>(next) == MG;
+    const bool on = left && up_groups<MAXMG>(next) == MG && up_units<MAXMG>(next, run) == C;
     const Own then = own_of(next, on);
     constexpr int Q = MG == 1 ? 2 : MG / 2;  // accumulators of 16 rows: of the rows 2 i and 2 i + 1, or of 16 tokens each
-    f32x4 c[2][Q];
+    f32x4 c[C][2][Q];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int n2 = 0; n2 < C; ++n2)
 #pragma unroll
-      for (int a = 0; a < Q; ++a) c[b][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int a = 0; a < Q; ++a) c[n2][b][a] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int k0 = 0; k0 < padded; k0 += D) {
       const bool ahead = k0 + D >= padded;  // the loads of this turn are the next pass'
       Own o = cur;
@@ -380,12 +411,12 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
         if constexpr (FMT == kFp8)
 #pragma unroll
           for (int b = 0; b < 2; ++b) beta[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(cur.beta[b]), i));
-        auto add = [&](int b, int a, f32x4 z) {
+        auto add = [&](int n2, int b, int a, f32x4 z) {
           if constexpr (FMT == kFp8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[b][a][e] = __builtin_fmaf(z[e], beta[b], c[b][a][e]);
+            for (int e = 0; e < 4; ++e) c[n2][b][a][e] = __builtin_fmaf(z[e], beta[b], c[n2][b][a][e]);
           } else {
-            c[b][a] = z;
+            c[n2][b][a] = z;
           }
         };
         if constexpr (MG == 1) {
@@ -396,12 +427,12 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
           for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-              const float ex = FMT == kFp4 ? exponent_of(sc[d][b][a], q) : 1.f;
+              const float ex = FMT == kFp4 ? exponent_of(sc[d][b][0][a], q) : 1.f;
               const u32x4 chunk = spread(sp, a, w[d][b][a]);
-              f32x4 z = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a];
+              f32x4 z = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[0][b][a];
 #pragma unroll
               for (int t = 0; t < P; ++t) z = mfma(widened<FMT>(chunk, t, ex), y[t], z);
-              add(b, a, z);
+              add(0, b, a, z);
             }
         } else {
           u32x4 y[MG / 2][P][2];
@@ -410,25 +441,27 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
 #pragma unroll
             for (int t = 0; t < P; ++t) spread16(sp, xr[d][g][t], xr[d][g + 1][t], y[g / 2][t]);
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            u32x4 chunk[2];
-            spread16(sp, w[d][b][0], w[d][b][1], chunk);
-            f32x4 z[MG / 2];
+          for (int n2 = 0; n2 < C; ++n2)
 #pragma unroll
-            for (int a = 0; a < MG / 2; ++a) z[a] = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[b][a];
+            for (int b = 0; b < 2; ++b) {
+              u32x4 chunk[2];
+              spread16(sp, w[d][b][2 * n2], w[d][b][2 * n2 + 1], chunk);
+              f32x4 z[Q];
 #pragma unroll
-            for (int s2 = 0; s2 < 2; ++s2) {
-              const float ex = FMT == kFp4 ? exponent_of(sc[d][b][s2], q) : 1.f;
+              for (int a = 0; a < Q; ++a) z[a] = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : c[n2][b][a];
 #pragma unroll
-              for (int t = 0; t < P; ++t) {
-                const bf16x8 v = widened<FMT>(chunk[s2], t, ex);
+              for (int s2 = 0; s2 < 2; ++s2) {
+                const float ex = FMT == kFp4 ? exponent_of(sc[d][b][n2][s2], q) : 1.f;
 #pragma unroll
-                for (int a = 0; a < MG / 2; ++a) z[a] = mfma(v, y[a][t][s2], z[a]);
+                for (int t = 0; t < P; ++t) {
+                  const bf16x8 v = widened<FMT>(chunk[s2], t, ex);
+#pragma unroll
+                  for (int a = 0; a < Q; ++a) z[a] = mfma(v, y[a][t][s2], z[a]);
+                }
               }
-            }
 #pragma unroll
-            for (int a = 0; a < MG / 2; ++a) add(b, a, z[a]);
-          }
+              for (int a = 0; a < Q; ++a) add(n2, b, a, z[a]);
+            }
         }
         load(d, o, ahead ? d : k0 + D + d);
       }
@@ -438,41 +471,44 @@ __device__ __forceinline__ bool up_passes(const ExpertsParams& p, UpShared<MAXMG
     const bool mine = MG > 1 || (!half && q < 2);  // one row of tokens: lanes (token r8, q < 2) of the lower half have weight rows 8 q + 2 e + a
     auto place = [&](int b, int a) { return MG == 1 ? b * 2 + a : (a * 2 + b) * 4 + q; };
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int n2 = 0; n2 < C; ++n2) {
 #pragma unroll
-      for (int a = 0; a < Q; ++a) {
-        if constexpr (MG == 1) c[b][a] = halves(c[b][a]);
-        if (wave > 0 && mine) sh.part[turn][wave - 1][place(b, a)][at] = c[b][a];
-      }
-    __syncthreads();  // (the other half of `part` is what the next pass writes)
-    if (wave == 0 && mine) {
-      f32x4 v[Q];
-#pragma unroll
-      for (int a = 0; a < Q; ++a) {
-        f32x4 z[2] = {c[0][a], c[1][a]};
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int u = 0; u < 3; ++u) z[b] += sh.part[turn][u][place(b, a)][at];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[a][e] = activate<kActSilu>(z[0][e]) * z[1][e];
-      }
-      if constexpr (MG == 1) {
-        const int r = it.m0 + r8;
-        if (r < it.m)
-          *reinterpret_cast<uint4*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 8 * q) =
-              uint4{pack_bf16x2(v[0][0], v[1][0]), pack_bf16x2(v[0][1], v[1][1]), pack_bf16x2(v[0][2], v[1][2]), pack_bf16x2(v[0][3], v[1][3])};
-      } else {
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int a = 0; a < Q; ++a) {
-          const int r = it.m0 + 16 * a + (lane & 15);
+          if constexpr (MG == 1) c[n2][b][a] = halves(c[n2][b][a]);
+          if (wave > 0 && mine) sh.part[turn][wave - 1][place(b, a)][at] = c[n2][b][a];
+        }
+      __syncthreads();  // (the other half of `part` is what the next pass writes)
+      if (wave == 0 && mine) {
+        f32x4 v[Q];
+#pragma unroll
+        for (int a = 0; a < Q; ++a) {
+          f32x4 z[2] = {c[n2][0][a], c[n2][1][a]};
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int u = 0; u < 3; ++u) z[b] += sh.part[turn][u][place(b, a)][at];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[a][e] = activate<kActSilu>(z[0][e]) * z[1][e];
+        }
+        if constexpr (MG == 1) {
+          const int r = it.m0 + r8;
           if (r < it.m)
-            *reinterpret_cast<uint2*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 4 * q) =
-                uint2{pack_bf16x2(v[a][0], v[a][1]), pack_bf16x2(v[a][2], v[a][3])};
+            *reinterpret_cast<uint4*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 8 * q) =
+                uint4{pack_bf16x2(v[0][0], v[1][0]), pack_bf16x2(v[0][1], v[1][1]), pack_bf16x2(v[0][2], v[1][2]), pack_bf16x2(v[0][3], v[1][3])};
+        } else {
+#pragma unroll
+          for (int a = 0; a < Q; ++a) {
+            const int r = it.m0 + 16 * a + (lane & 15);
+            if (r < it.m)
+              *reinterpret_cast<uint2*>(p.h + (int64_t)(s.table.entry[it.start + r] & 0xffffu) * p.I + it.i0 + 16 * n2 + 4 * q) =
+                  uint2{pack_bf16x2(v[a][0], v[a][1]), pack_bf16x2(v[a][2], v[a][3])};
+          }
         }
       }
+      turn ^= 1;
     }
-    turn ^= 1;
     it = next;
     if (!on) return left;
     cur = then;
@@ -483,20 +519,33 @@ template <int FMT, int MAXMG, bool NT>
 __global__ void __launch_bounds__(kUpThreads) experts_up_kernel(ExpertsParams p) {
   __shared__ UpShared<MAXMG> sh;
   read_members(p, sh.members);
-  // as many workgroups as give each the same number of units, or one less
   const int tiles = p.I >> 4;
   const int units = __builtin_amdgcn_readfirstlane(sh.members.table.n) * tiles;
+  int first = (int)blockIdx.x;
+  UpRun run{units, 0};
   if (units == 0) return;
-  const int rounds = (units + (int)gridDim.x - 1) / (int)gridDim.x;
-  const int stride = (units + rounds - 1) / rounds;
-  if ((int)blockIdx.x >= stride) return;
-  UpItem it = up_item(sh.members, (int)blockIdx.x, 0, tiles);
+  if (MAXMG > 2 && entries_of(sh.members.table) > kPairTokens * sh.members.table.n) {  // a run of neighbouring units, one more for some workgroups than for others
+    const int n = units < (int)gridDim.x ? units : (int)gridDim.x;
+    if (first >= n) return;
+    run.end = (int)((int64_t)(first + 1) * units / n);
+    first = (int)((int64_t)first * units / n);
+    run.step = 1;
+  } else {  // as many workgroups as give each the same number of units, or one less
+    const int rounds = (units + (int)gridDim.x - 1) / (int)gridDim.x;
+    run.step = (units + rounds - 1) / rounds;
+    if (first >= run.step) return;
+  }
+  UpItem it = up_item(sh.members, first, 0, tiles);
   int turn = 0;
   for (bool left = true; left;) {
-    const int g = up_groups<MAXMG>(it);
-    if (g == 1) left = up_passes<FMT, 1, MAXMG, NT>(p, sh, it, units, stride, turn);
-    else if (g == 2) left = up_passes<FMT, 2, MAXMG, NT>(p, sh, it, units, stride, turn);
-    else if constexpr (MAXMG > 2) left = up_passes<FMT, 4, MAXMG, NT>(p, sh, it, units, stride, turn);
+    const int g = up_groups<MAXMG>(it), c = up_units<MAXMG>(it, run);
+    if (g == 1) left = up_passes<FMT, 1, 1, MAXMG, NT>(p, sh, it, run, turn);
+    else if (g == 2 && c == 1) left = up_passes<FMT, 2, 1, MAXMG, NT>(p, sh, it, run, turn);
+    else if constexpr (MAXMG > 2) {
+      if (g == 2) left = up_passes<FMT, 2, 2, MAXMG, NT>(p, sh, it, run, turn);
+      else if (c == 1) left = up_passes<FMT, 4, 1, MAXMG, NT>(p, sh, it, run, turn);
+      else left = up_passes<FMT, 4, 2, MAXMG, NT>(p, sh, it, run, turn);
+    }
   }
 }
 
@@ -766,9 +815,7 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
     down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   } else {
     // tokens of an expert on average: an expert of more takes its steps group by group
-    const int chosen = __builtin_amdgcn_readfirstlane(s.n);
-    const uint32_t end = chosen > 0 ? __builtin_amdgcn_readfirstlane(s.run[chosen - 1]) : 0u;
-    const int entries = chosen > 0 ? start_of(end) + count_of(end) : 0;
+    const int chosen = __builtin_amdgcn_readfirstlane(s.n), entries = entries_of(s);
     if (entries <= 6 * chosen) down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
     else if (entries <= 12 * chosen) down_run<FMT, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
     else down_run<FMT, 4, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
