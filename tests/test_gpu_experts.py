@@ -50,7 +50,11 @@ def _run(L, x, idx, w, first=0, ws=None, y=None, stream=None):
     ws = _ws(idx.numel(), L["H"], L["I"]) if ws is None else ws
     call = dg.dg_moe_experts_fp8 if L["fmt"] == "fp8" else dg.dg_moe_experts_mxfp4
     q1, s1, q2, s2 = L["args"]
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())  # y and ws are filled there
     call(x, idx, w, q1, s1, q2, s2, y, first_expert=first, workspace=ws, stream=stream)
+    if stream is not None:
+        torch.cuda.current_stream().wait_stream(stream)
     assert not ws[:4096].any()  # counters back at zero
     return y
 

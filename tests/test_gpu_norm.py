@@ -73,6 +73,8 @@ def _norm(x, w, residual=None, kind=None, y=True, eps=1e-6, stream=None):
     if kind:
         o["q"] = torch.full((M, K), 0x55, dtype=torch.uint8, device=DEV)
         o["sf"] = torch.full((K // 128, M), 7.0, device=DEV) if kind == "f32" else torch.full(((K + 511) // 512, M), -1, dtype=torch.int32, device=DEV)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())  # the outputs are filled there
     dg.dg_rms_norm(x, w, residual=residual, eps=eps, stream=stream, **o)
     return o
 
