@@ -44,7 +44,9 @@ int check_partials(const void* ws, size_t ws_bytes, size_t need) {
 constexpr size_t kTableBytes = (sizeof(ExpertsTable) + 255) / 256 * 256;
 
 size_t experts_bytes(int64_t choices, int64_t T, int64_t H, int64_t I, int splits) {
-  return kBlockWsCounterBytes + kTableBytes + experts_h_bytes(choices, I) + (splits > 1 ? (size_t)splits * (size_t)H * (size_t)T * 4 : 0);
+  // (more than 8 tokens may be summed by twice as many workgroups to twice as many columns)
+  const int most = T > 8 ? 2 * splits : splits;
+  return kBlockWsCounterBytes + kTableBytes + experts_h_bytes(choices, I) + (most > 1 ? (size_t)most * (size_t)H * (size_t)T * 4 : 0);
 }
 
 bool experts_dim(int64_t d) { return d > 0 && d % 128 == 0 && d <= kExpertsMaxDim; }

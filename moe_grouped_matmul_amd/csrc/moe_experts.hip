@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(kUpThreads) experts_up_kernel(ExpertsParams p)
   }
 }
 
-// ---- down projection and weighted sum.  A workgroup takes 16 columns of y for all tokens; its waves, and those of all
-// p.splits workgroups of the columns, take equal runs of the steps of all chosen experts, one expert after the other, with the
+// ---- down projection and weighted sum.  A workgroup takes 16 columns of y for all tokens (where experts have many tokens 32, and
+// twice as many workgroups share them: h is loaded half as often); its waves, and those of all workgroups of the columns, take equal runs of the steps of all chosen experts, one expert after the other, with the
 // next steps' loads in flight across experts.  The tokens of an expert share its steps, 8 MG at a time (one group).  When the
 // group changes, the accumulators times the tokens' weights are added to the wave's sums of the tokens in LDS, so that a
 // token's experts are added in the order of their numbers.
@@ -562,15 +562,16 @@ constexpr int kDownWaves = FEW ? 8 : 4;
 
 // Steps in flight.  128 registers leave room for two workgroups of eight waves a CU, 256 for two of four.
 template <int FMT, bool FEW>
-constexpr int down_depth(int mg) {
+constexpr int down_depth(int mg, int c) {
+  if (c == 2) return FMT == kFp8 ? (mg == 2 ? 3 : 2) : mg == 2 ? 2 : 1;
   if (FMT == kFp8) return FEW ? 4 : mg == 1 ? 5 : mg == 2 ? 3 : 2;
   return FEW ? 2 : mg == 1 ? 3 : mg == 2 ? 2 : 1;
 }
 
-// the wave's part: its run of the steps, into its sums
-template <int FMT, int MG, bool FEW, bool NT>
+// the wave's part: its run of the steps, into its sums of 16 C columns
+template <int FMT, int MG, int C, bool FEW, bool NT>
 __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTable& s, f32x4* sums, u32x4* slots_of_wave, int c0, int slot, int slots) {
-  constexpr int D = down_depth<FMT, FEW>(MG);
+  constexpr int D = down_depth<FMT, FEW>(MG, C);
   constexpr int P = kParts<FMT>;
   const int lane = threadIdx.x & 63;
   const int r8 = lane & 7, half = (lane >> 3) & 1, q = lane >> 4;
@@ -588,9 +589,9 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     // loads: row (or token) lane / 8, chunk lane % 8; weight rows c0 + 2 (lane / 8) + a
     const int l8 = lane >> 3, ch = lane & 7;
     const Spread sp = spread_of(slots_of_wave);
-    uint32_t w_off[2];
+    uint32_t w_off[2 * C];
 #pragma unroll
-    for (int a = 0; a < 2; ++a) w_off[a] = (uint32_t)(c0 + (MG == 1 ? 2 * l8 + a : 8 * a + l8)) * row_bytes + 16u * ch;
+    for (int a = 0; a < 2 * C; ++a) w_off[a] = (uint32_t)(c0 + (MG == 1 ? 2 * l8 + a : 8 * a + l8)) * row_bytes + 16u * ch;
     // scales: e4m3 [ceil(H / 128)][KB] fp32, e2m1 words [KB][H]
     const uint32_t s_bytes = FMT == kFp8 ? ((H + 127) >> 7) * (uint32_t)KB * 4u : (uint32_t)KB * H * 4u;
     const uint32_t s_off = FMT == kFp8 ? (uint32_t)(c0 >> 7) * (uint32_t)KB * 4u
@@ -638,8 +639,8 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     enter_group();
     bool fresh = true;  // the next load begins a group of tokens
 
-    u32x4 w[D][2];
-    u32x2 sc[D];
+    u32x4 w[D][2 * C];
+    u32x2 sc[D][C];
     u32x4 hr[D][MG][P];
     float fr[D][N];
     int tr[D][N];
@@ -665,12 +666,15 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       const bool over = FMT == kFp4 && (k + 1) * 256u > I;  // a last half step has no upper chunks
       const bool cut = over && ch >= 4;
 #pragma unroll
-      for (int a = 0; a < 2; ++a) w[d][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], k * 128u, NT ? kStream : 0);
-      if constexpr (FMT == kFp8) sc[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
-      else if constexpr (MG == 1) sc[d] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, k * s_step, 0);
+      for (int a = 0; a < 2 * C; ++a) w[d][a] = __builtin_amdgcn_raw_buffer_load_b128(rw, cut ? kOOB : w_off[a], k * 128u, NT ? kStream : 0);
+      if constexpr (FMT == kFp8) sc[d][0][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
+      else if constexpr (MG == 1) sc[d][0] = __builtin_amdgcn_raw_buffer_load_b64(rs, over && half ? kOOB : s_off, k * s_step, 0);
       else {
-        sc[d][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off, k * s_step, 0);
-        sc[d][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off, k * s_step + 4u * H, 0);
+#pragma unroll
+        for (int n2 = 0; n2 < C; ++n2) {
+          sc[d][n2][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, s_off + 64u * n2, k * s_step, 0);
+          sc[d][n2][1] = __builtin_amdgcn_raw_buffer_load_b32(rs, over ? kOOB : s_off + 64u * n2, k * s_step + 4u * H, 0);
+        }
       }
 #pragma unroll
       for (int g = 0; g < MG; ++g)
@@ -689,17 +693,19 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       if (in) ++ld_k;
     };
     constexpr int Q = MG == 1 ? 2 : N;  // accumulators: of the rows 2 i and 2 i + 1, or of 16 tokens each
-    f32x4 acc[Q];
+    f32x4 acc[C][Q];
     int to[N];
     float by[N];
     auto clear = [&]() {
 #pragma unroll
-      for (int a = 0; a < Q; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int n2 = 0; n2 < C; ++n2)
+#pragma unroll
+        for (int a = 0; a < Q; ++a) acc[n2][a] = f32x4{0.f, 0.f, 0.f, 0.f};
     };
     // the accumulators into the sums: of 8 tokens lanes (token r8, q < 2) of the lower half have columns 8 q + 2 e + a
     auto flush = [&]() {
       if constexpr (MG == 1) {
-        const f32x4 x = halves(acc[0]), y = halves(acc[1]);
+        const f32x4 x = halves(acc[0][0]), y = halves(acc[0][1]);
         if (to[0] >= 0 && !half && q < 2) {
           f32x4* at = &sums[to[0] * (kDownCols / 4) + 2 * q];
           at[0] += f32x4{x[0], y[0], x[1], y[1]} * by[0];
@@ -708,7 +714,9 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
       } else {
 #pragma unroll
         for (int a = 0; a < Q; ++a)
-          if (to[a] >= 0) sums[to[a] * (kDownCols / 4) + q] += acc[a] * by[a];
+          if (to[a] >= 0)
+#pragma unroll
+            for (int n2 = 0; n2 < C; ++n2) sums[to[a] * (C * kDownCols / 4) + 4 * n2 + q] += acc[n2][a] * by[a];
       }
     };
 #pragma unroll
@@ -734,12 +742,12 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
           }
           clear();
         }
-        auto add = [&](int a, f32x4 o) {
+        auto add = [&](int n2, int a, f32x4 o) {
           if constexpr (FMT == kFp8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[a][e] = __builtin_fmaf(o[e], __uint_as_float(sc[d][0]), acc[a][e]);
+            for (int e = 0; e < 4; ++e) acc[n2][a][e] = __builtin_fmaf(o[e], __uint_as_float(sc[d][0][0]), acc[n2][a][e]);
           } else {
-            acc[a] = o;
+            acc[n2][a] = o;
           }
         };
         if constexpr (MG == 1) {
@@ -748,35 +756,43 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
           for (int t = 0; t < P; ++t) x[t] = spread(sp, t, hr[d][0][t]);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
-            const float ex = FMT == kFp4 ? exponent_of(sc[d][a], q) : 1.f;
+            const float ex = FMT == kFp4 ? exponent_of(sc[d][0][a], q) : 1.f;
             const u32x4 chunk = spread(sp, a, w[d][a]);
-            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a];
+            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[0][a];
 #pragma unroll
             for (int t = 0; t < P; ++t) o = mfma(widened<FMT>(chunk, t, ex), x[t], o);
-            add(a, o);
+            add(0, a, o);
           }
         } else {
-          u32x4 chunk[2];
-          spread16(sp, w[d][0], w[d][1], chunk);
-          bf16x8 v[2][P];
+          bf16x8 v[C][2][P];
 #pragma unroll
-          for (int s2 = 0; s2 < 2; ++s2) {
-            const float ex = FMT == kFp4 ? exponent_of(sc[d][s2], q) : 1.f;
+          for (int n2 = 0; n2 < C; ++n2) {
+            u32x4 chunk[2];
+            spread16(sp, w[d][2 * n2], w[d][2 * n2 + 1], chunk);
 #pragma unroll
-            for (int t = 0; t < P; ++t) v[s2][t] = widened<FMT>(chunk[s2], t, ex);
+            for (int s2 = 0; s2 < 2; ++s2) {
+              const float ex = FMT == kFp4 ? exponent_of(sc[d][n2][s2], q) : 1.f;
+#pragma unroll
+              for (int t = 0; t < P; ++t) v[n2][s2][t] = widened<FMT>(chunk[s2], t, ex);
+            }
           }
 #pragma unroll
           for (int a = 0; a < Q; ++a) {
             if (a > 0 && 2 * a >= gr[d]) break;  // uniform
-            f32x4 o = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[a];
+            f32x4 o[C];
+#pragma unroll
+            for (int n2 = 0; n2 < C; ++n2) o[n2] = FMT == kFp8 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[n2][a];
 #pragma unroll
             for (int t = 0; t < P; ++t) {
               u32x4 x[2];
               spread16(sp, hr[d][2 * a][t], hr[d][2 * a + 1][t], x);
 #pragma unroll
-              for (int s2 = 0; s2 < 2; ++s2) o = mfma(v[s2][t], x[s2], o);
+              for (int s2 = 0; s2 < 2; ++s2)
+#pragma unroll
+                for (int n2 = 0; n2 < C; ++n2) o[n2] = mfma(v[n2][s2][t], x[s2], o[n2]);
             }
-            add(a, o);
+#pragma unroll
+            for (int n2 = 0; n2 < C; ++n2) add(n2, a, o[n2]);
           }
         }
         load(d);
@@ -792,13 +808,11 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
   constexpr int W = kDownWaves<FEW>;
   constexpr int THREADS = 64 * W;
   __shared__ ExpertsTable s;
-  __shared__ __attribute__((aligned(16))) f32x4 sums[W][(FEW ? 8 : kExpertsMaxTokens) * (kDownCols / 4)];  // [token][four columns]
+  __shared__ __attribute__((aligned(16))) f32x4 sums[W][(FEW ? 8 : 2 * kExpertsMaxTokens) * (kDownCols / 4)];  // [token][four columns]
   __shared__ __attribute__((aligned(16))) u32x4 spread_s[W][64 * kSpreadSlots];
   __shared__ int last;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = (int)blockIdx.x / p.splits, split = (int)blockIdx.x - tile * p.splits;
-  const int c0 = tile * kDownCols;
   {
     const int n = p.T * p.k;
     for (int i = threadIdx.x; i < n; i += THREADS) {
@@ -808,54 +822,75 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
     }
     if (threadIdx.x == 0) s.n = p.table->n;
   }
-  for (int i = lane; i < p.T * (kDownCols / 4); i += 64) sums[wave][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = lane; i < (FEW ? 1 : 2) * p.T * (kDownCols / 4); i += 64) sums[wave][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   __syncthreads();
-  const int slot = split * W + wave, slots = W * p.splits;
-  if constexpr (FEW) {
-    down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
-  } else {
-    // tokens of an expert on average: an expert of more takes its steps group by group
-    const int chosen = __builtin_amdgcn_readfirstlane(s.n), entries = entries_of(s);
-    if (entries <= 6 * chosen) down_run<FMT, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
-    else if (entries <= 12 * chosen) down_run<FMT, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
-    else down_run<FMT, 4, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
+  // tokens of an expert on average: an expert of more takes its steps group by group
+  const int chosen = __builtin_amdgcn_readfirstlane(s.n), entries = entries_of(s);
+  const bool wide = !FEW && entries > kPairTokens * chosen;
+  const int cols = wide ? 2 * kDownCols : kDownCols, splits = wide ? 2 * p.splits : p.splits;
+  const int tile = (int)blockIdx.x / splits, split = (int)blockIdx.x - tile * splits;
+  const int c0 = tile * cols;
+  const int slot = split * W + wave, slots = W * splits;
+  if (!wide) down_run<FMT, 1, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
+  if constexpr (!FEW) {
+    if (wide && entries <= 12 * chosen) down_run<FMT, 2, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
+    else if (wide) down_run<FMT, 4, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   }
   __syncthreads();
-  // the waves' sums in order: a thread takes four columns of a token
-  const int u = threadIdx.x;
-  const bool live = u < p.T * (kDownCols / 4);
-  f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (live)
+  // the waves' sums in order: a thread takes four columns of a token, of 32 columns two times four
+  constexpr int E = FEW ? 1 : 2;
+  const int fours = p.T * cols / 4;
+  f32x4 y[E];
 #pragma unroll
-    for (int o = 0; o < W; ++o) y += sums[o][u];
-  if (p.splits > 1) {
+  for (int e = 0; e < E; ++e) {
+    const int u = threadIdx.x + THREADS * e;
+    y[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (u < fours)
+#pragma unroll
+      for (int o = 0; o < W; ++o) y[e] += sums[o][u];
+  }
+  if (splits > 1) {
     // The workgroups' sums meet in the workspace: sc1 stores and loads are coherent across the XCDs' L2 caches; every wave's
     // stores are acknowledged (vmcnt 0) before the barrier that precedes the relaxed counter increment, and the last
     // workgroup loads only after its own increment has returned.  It adds them in order and leaves the counter at zero.
-    const uint32_t one = (uint32_t)p.T * 4u * kDownCols;
-    const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.partials, (uint32_t)p.splits * (uint32_t)p.H * (uint32_t)p.T * 4u);
-    const uint32_t off = live ? (uint32_t)tile * (uint32_t)p.splits * one + (uint32_t)u * 16u : kOOB;
-    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y), rp, off, (uint32_t)split * one, kCoherent);
+    const uint32_t one = (uint32_t)fours * 16u;
+    const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.partials, (uint32_t)splits * (uint32_t)p.H * (uint32_t)p.T * 4u);
+    uint32_t off[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int u = threadIdx.x + THREADS * e;
+      off[e] = u < fours ? (uint32_t)tile * (uint32_t)splits * one + (uint32_t)u * 16u : kOOB;
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[e]), rp, off[e], (uint32_t)split * one, kCoherent);
+    }
     wait_vmcnt<0>();
     __syncthreads();
     if (threadIdx.x == 0)
-      last = __hip_atomic_fetch_add(&p.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned int)(p.splits - 1);
+      last = __hip_atomic_fetch_add(&p.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned int)(splits - 1);
     __syncthreads();
     if (!last) return;
     if (threadIdx.x == 0) __hip_atomic_store(&p.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    y = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int i0 = 0; i0 < p.splits; i0 += 4) {  // four in flight; past the last, an empty place
-      f32x4 t[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        t[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, i0 + i < p.splits ? off : kOOB, (uint32_t)(i0 + i < p.splits ? i0 + i : 0) * one, kCoherent));
+    for (int e = 0; e < E; ++e) y[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i0 = 0; i0 < splits; i0 += 4) {  // four in flight; past the last, an empty place
+      f32x4 t[E][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y += t[i];
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          t[e][i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, i0 + i < splits ? off[e] : kOOB, (uint32_t)(i0 + i < splits ? i0 + i : 0) * one, kCoherent));
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[e] += t[e][i];
     }
   }
-  if (live)
-    *reinterpret_cast<uint2*>(p.y + (int64_t)(u / (kDownCols / 4)) * p.H + c0 + 4 * (u % (kDownCols / 4))) =
-        uint2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int u = threadIdx.x + THREADS * e;
+    if (u < fours)
+      *reinterpret_cast<uint2*>(p.y + (int64_t)(u / (cols / 4)) * p.H + c0 + 4 * (u % (cols / 4))) =
+          uint2{pack_bf16x2(y[e][0], y[e][1]), pack_bf16x2(y[e][2], y[e][3])};
+  }
 }
 
 template <int FMT, bool NT>
