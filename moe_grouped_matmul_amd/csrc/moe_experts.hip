@@ -22,11 +22,12 @@
 //
 // Rates (both kernels, weights alone): one token, 8 of 32 experts, 7168 x 2048
 // e4m3 (352 MB) 62 us, 6.1 and 5.0 TB/s; 48 tokens x 8 of 256, 32 of them here,
-// e2m1 (560 MB) 79-101 us; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB) 54-63
-// us, where the address units are busy 0.7 of the cycles: the activations, read
-// from the L2 caches by every workgroup that needs them, take more of their time
-// than the weights; one token, 4 of 16 experts, 1024 x 512 (6 MB) 11.4 us, two
-// launches and the order of the choices.
+// e2m1 (430 MB of the 17 to 19 that were chosen) 77-103 us, where a step's four
+// loads of activations and two of scales keep the data path behind the address
+// units busy 0.9 of the cycles; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB)
+// 54-63 us, busy 0.8: the activations, read from the L2 caches by every workgroup
+// that needs them, take as long as the weights; one token, 4 of 16 experts, 1024
+// x 512 (6 MB) 11.4 us, two launches and the order of the choices.
 
 #include "activation.hpp"
 #include "block_internal.hpp"
@@ -859,25 +860,36 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int u = threadIdx.x + THREADS * e;
-      off[e] = u < fours ? (uint32_t)tile * (uint32_t)splits * one + (uint32_t)u * 16u : kOOB;
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[e]), rp, off[e], (uint32_t)split * one, kCoherent);
+      off[e] = u < fours ? ((uint32_t)tile * (uint32_t)splits + (uint32_t)split) * one + (uint32_t)u * 16u : kOOB;
+      asm volatile("" : "+v"(off[e]));
     }
+    // All addresses first, and the stores back to back: a register of a 16-byte store that the next instruction overwrites can
+    // reach memory overwritten (the compiler keeps one instruction between them only where the scalar offset is a constant, and
+    // the split's place in that register had single words of 2 in 56 calls wrong).
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int e = 0; e < E; ++e) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, y[e]), rp, off[e], 0, kCoherent);
     wait_vmcnt<0>();
+    __builtin_amdgcn_sched_barrier(0);
     __syncthreads();
     if (threadIdx.x == 0)
       last = __hip_atomic_fetch_add(&p.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (unsigned int)(splits - 1);
     __syncthreads();
     if (!last) return;
     if (threadIdx.x == 0) __hip_atomic_store(&p.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    uint32_t from[E];  // of the first split
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < E; ++e) {
+      from[e] = off[e] == kOOB ? kOOB : off[e] - (uint32_t)split * one;
+      y[e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     for (int i0 = 0; i0 < splits; i0 += 4) {  // four in flight; past the last, an empty place
       f32x4 t[E][4];
 #pragma unroll
       for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          t[e][i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, i0 + i < splits ? off[e] : kOOB, (uint32_t)(i0 + i < splits ? i0 + i : 0) * one, kCoherent));
+          t[e][i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, i0 + i < splits ? from[e] : kOOB, (uint32_t)(i0 + i < splits ? i0 + i : 0) * one, kCoherent));
 #pragma unroll
       for (int e = 0; e < E; ++e)
 #pragma unroll

@@ -63,3 +63,15 @@ def test_nan_among_many_tokens(fmt):
     keep[:] = True
     keep[9] = False
     assert torch.equal(got[keep], y[keep]) and not got[9].isfinite().any()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp4"])
+def test_many_calls_with_splits(fmt):
+    # two workgroups and more share every 32 columns of y: each call's partial sums reach the last of them whole
+    H, inner, G = 4096, 512, 8
+    L = _layer(fmt, G, H, inner)
+    for seed in range(4):
+        x, idx, w = _tokens(64, 2, G, H, seed=seed, drop=0)
+        y = _run(L, x, idx, w)
+        for _ in range(60):
+            assert torch.equal(_run(L, x, idx, w), y)
