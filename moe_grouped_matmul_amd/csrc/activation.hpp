@@ -12,23 +12,22 @@ __device__ __forceinline__ float sigmoid(float z) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
 
-// z Phi(z) = max(z, 0) - a Phi(-a), a = |z|.  log2 Phi(-a) is smooth: a polynomial
-// of degree 8, fitted here to least a Phi(-a) off over [0, 6] (1.4e-8, 5.4e-8 with
-// the fp32 roundings) and falling fast past that, takes eight FMAs and one 2^x,
-// where the formula below takes a reciprocal too and is off by more.  At the end of
-// a 256 x 256 tile it costs 5 us (6.6 with that formula; silu 0.7): less its
-// arithmetic than its 16 KB of straight code, which no cache holds then.
+// z Phi(z) = max(z, 0) - a Phi(-a), a = |z|.  Phi(-a) = e^(-a^2 / 2) T(1 / (1 + c a)): what is left of the tail beside
+// its exponential is smooth in that argument, and a polynomial of degree 6 without a constant was fitted here to it over [0, 13.4]
+// with weights that bound both what is off relative to 1 (1.3e-7 with the fp32 roundings) and relative to the result, which
+// falls below 2^-126 in that range (5.5e-5 of it, where bf16 rounds by up to 3.9e-3; 1e-6 above -2).  (A polynomial of
+// log2 Phi(-a) alone needs degree 11 for 1.9e-3 of the result; one of degree 8 that bounds what is off of 1 alone, 43% wrong at
+// -7, took 1.2 us less at the end of 4096 x 4096 x 7168: 121.5 and 122.7 us.)
 __device__ __forceinline__ float gelu(float z) {
-  const float a = fminf(fabsf(z), 16.f);  // 2^-3660 there
-  float p = __builtin_fmaf(-2.27583314e-06f, a, 3.29678624e-05f);
-  p = __builtin_fmaf(p, a, -0.000157279617f);
-  p = __builtin_fmaf(p, a, -0.000202473879f);
-  p = __builtin_fmaf(p, a, 0.00714277336f);
-  p = __builtin_fmaf(p, a, -0.0525464304f);
-  p = __builtin_fmaf(p, a, -0.459193051f);
-  p = __builtin_fmaf(p, a, -1.15110695f);
-  p = __builtin_fmaf(p, a, -0.99999994f);
-  return __builtin_fmaf(-a, __builtin_amdgcn_exp2f(p), z < 0.f ? 0.f : z);  // NaN stays
+  const float a = fminf(fabsf(z), 16.f);  // e^(-a^2 / 2) is zero in fp32 there, and infinities stay out of the products
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.295893878f, a, 1.f));
+  const float e = __builtin_amdgcn_exp2f(-0.5f * 1.44269504f * a * a);
+  float p = __builtin_fmaf(-0.0838792995f, t, 0.248623431f);
+  p = __builtin_fmaf(p, t, -0.0515091605f);
+  p = __builtin_fmaf(p, t, 0.159625828f);
+  p = __builtin_fmaf(p, t, 0.108404532f);
+  p = __builtin_fmaf(p, t, 0.118734419f);
+  return __builtin_fmaf(-(a * t * p), e, z < 0.f ? 0.f : z);  // NaN stays
 }
 
 // Phi(z) of the normal distribution and e^(-z^2 / 2), which its slope needs both.  The complementary error
