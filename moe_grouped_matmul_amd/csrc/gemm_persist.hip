@@ -825,13 +825,15 @@ __global__ void __launch_bounds__(512) fp8_gemm_persistent_kernel(GemmParams p) 
     const __amdgpu_buffer_rsrc_t rw =
         make_rsrc(reinterpret_cast<uint8_t*>(p.ws) + kWsCounterBytes, (uint32_t)p.sk_tiles * (uint32_t)P * tile_bytes);
     const uint32_t w_off = (uint32_t)(cp_t.tail * P) * tile_bytes + (uint32_t)wave * frag_bytes + (uint32_t)lane * 16u;
+    // (the piece's place in the vector offset: a 16-byte store with a register as its scalar offset, whose data register the
+    // next instruction overwrites, can write the new value, and the compiler keeps the two apart only where that offset is constant)
+    const uint32_t own_off = w_off + (uint32_t)cp_t.piece * tile_bytes;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, u[i][j]), rw,
-                                               w_off + (uint32_t)(i * TN + j) * 1024u,
-                                               (uint32_t)cp_t.piece * tile_bytes, kCoherent);
+                                               own_off + (uint32_t)(i * TN + j) * 1024u, 0, kCoherent);
     wait_vmcnt<0>();
     __syncthreads();
     unsigned int* counters = reinterpret_cast<unsigned int*>(p.ws);
