@@ -565,7 +565,8 @@ size_t dg_get_workspace_size(int op, int64_t rows, int64_t N, int64_t K, int64_t
  *                     with at most 2048 rows use bm-row tiles (64 or 128) of
  *                     4 wn columns (wn 16 or 32), a K split of s (bounded by
  *                     the K blocks and the workspace) and ring depth p (one
- *                     of the compiled depths; other values are ignored);
+ *                     of the compiled depths; other values are ignored,
+ *                     and the epilogue form keeps the tile's default);
  *                     "mxfp4=<bm>x<bn>[x<s>]" makes the microscaled 4-bit
  *                     products use tiles of that shape (64x64, 128x256 or
  *                     256x256) where their form has it, 64x64 tiles with a

@@ -406,8 +406,9 @@ double persistent_cost_us(const DensePlan& pl, int64_t K) {
 // 16, and only as large as the workspace holds.  (Re-measured against a sweep
 // of tile shape, split and ring depth on the decode shapes of the dense sweep,
 // each configuration with a freshly zeroed workspace: no configuration beat
-// this rule by more than the run-to-run spread.)
-void plan_skinny(DensePlan& pl, int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes) {
+// this rule by more than the run-to-run spread.)  deep_rings: the form has
+// the deeper rings that DG_FORCE_CONFIG may ask for.
+void plan_skinny(DensePlan& pl, int64_t M, int64_t N, int64_t K, int cus, size_t ws_bytes, bool deep_rings) {
   const int KB = (int)(K / 128);
   pl.skinny = true;
   // 64 < M <= 128: one 128-row tile (weights read once) when the columns
@@ -466,7 +467,7 @@ void plan_skinny(DensePlan& pl, int64_t M, int64_t N, int64_t K, int cus, size_t
     splits = f.sk_splits < KB ? f.sk_splits : KB;
     if ((int64_t)pl.m_tiles * pl.n_tiles > dg::kWsMaxCounters) splits = 1;
     while (splits > 1 && dg::skinny_workspace_bytes(pl.cfg, pl.m_tiles, pl.n_tiles, pl.wn, splits) > ws_bytes) --splits;
-    depth = f.sk_depth;
+    depth = deep_rings ? f.sk_depth : dg::skinny_depth(pl.cfg, pl.wn);
   }
   pl.depth = depth;
   // whole ring cycles per split where that does not cost a split
@@ -505,7 +506,7 @@ DensePlan plan_dense(DenseKind kind, int64_t M, int64_t N, int64_t K, int cus, s
   const bool mid = M > 128 && f.kernel == kForceNone &&
                    ((f.sk_bm && M <= 2048) || (M <= 512 && 2 * ceil_div(N, 128) <= cus && K <= 8192));
   if (kind != kBf16 && (M <= 128 || mid)) {
-    plan_skinny(pl, M, N, K, cus, ws_bytes);
+    plan_skinny(pl, M, N, K, cus, ws_bytes, kind != kEpi);
     return pl;
   }
   const bool wide =
@@ -523,7 +524,7 @@ DensePlan plan_dense(DenseKind kind, int64_t M, int64_t N, int64_t K, int cus, s
     int bm = 0, wn = 0, s = 0;
     if (1.15 * best_skinny(M, N, K, cus, ws_bytes, &bm, &wn, &s) < persistent_cost_us(pl, K)) {
       pl = DensePlan();
-      plan_skinny(pl, M, N, K, cus, ws_bytes);
+      plan_skinny(pl, M, N, K, cus, ws_bytes, kind != kEpi);
     }
   }
   return pl;

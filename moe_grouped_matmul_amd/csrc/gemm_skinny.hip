@@ -522,7 +522,8 @@ size_t skinny_workspace_bytes(int bm, int m_tiles, int n_tiles, int wn, int spli
 }
 
 hipError_t launch_gemm_skinny(int bm, int wn, int depth, bool ue, int act, const GemmParams& p, hipStream_t stream) {
-  const bool deep = act < 0 && depth != skinny_depth(bm, wn);  // the epilogue form has the default depths only
+  const bool deep = depth != skinny_depth(bm, wn);
+  if (deep && act >= 0) return hipErrorInvalidValue;  // the epilogue form has the default depths only, and is planned so
   if (bm == 64 && wn == 16)
     return deep ? launch_skinny_cfg<64, 16, 8>(ue, act, p, stream) : launch_skinny_cfg<64, 16, 4>(ue, act, p, stream);
   if (bm == 64)
