@@ -87,6 +87,8 @@ __device__ __forceinline__ float exponent_of(uint32_t word, int q) { return __ui
 // that neither side meets another lane's banks: a wave's LDS accesses happen in order, and no wait stands between the two (16
 // cycles of the LDS; four rotations of a register between lanes took 23).  Slots in turn leave the next ones free to be written.
 constexpr int kSpreadSlots = 2;
+// what other lanes of the wave put into the LDS before this is seen after it: an order for the compiler, no instruction
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
 struct Spread {
   u32x4* put;
   const u32x4* get;
@@ -102,6 +104,7 @@ __device__ __forceinline__ Spread spread_of(u32x4* slots) {
 }
 __device__ __forceinline__ u32x4 spread(const Spread& s, int turn, u32x4 v) {
   s.put[64 * (turn % kSpreadSlots)] = v;
+  wave_fence();  // (and the slot's last reads are before the fence of the turn between)
   return s.get[64 * (turn % kSpreadSlots)];
 }
 
@@ -118,8 +121,10 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, u32x4 b, f32x4 c) {
 
 // two registers of 8 rows each as both halves of the chunks of 16 rows
 __device__ __forceinline__ void spread16(const Spread& s, u32x4 rows0, u32x4 rows8, u32x4 (&out)[2]) {
+  wave_fence();  // the last reads of both slots
   s.put[0] = rows0;
   s.put[64] = rows8;
+  wave_fence();
   out[0] = s.get16[0];
   out[1] = s.get16[s.upper];
 }
