@@ -237,11 +237,12 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(NormBwdParams p) {
   }
 }
 
-// 64 columns x 16 slices of rows a workgroup
+// 64 columns x 16 slices of rows a workgroup; rows are `stride` apart
 constexpr int kSumCols = 64;
 constexpr int kSumSlices = 16;
+constexpr int kSumMostCols = 1 << 27;  // of a launch: 16 threads a column, and thread counts are 32 bits
 __global__ void __launch_bounds__(64 * 16) column_sum_kernel(const float* __restrict__ partials, float* __restrict__ out,
-                                                                          int64_t rows, int N) {
+                                                                          int64_t rows, int N, int64_t stride) {
   __shared__ float s[kSumSlices][kSumCols];
   const int col = threadIdx.x % kSumCols, sl = threadIdx.x / kSumCols;
   const int c = blockIdx.x * kSumCols + col;
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(64 * 16) column_sum_kernel(const float* __rest
     for (int64_t r = sl * per; r < hi; r += 8) {  // eight rows in flight
       float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r + i < hi ? partials[(r + i) * N + c] : 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = r + i < hi ? partials[(r + i) * stride + c] : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) a += v[i];
     }
@@ -371,8 +372,14 @@ hipError_t launch_rms_norm_bwd(const NormBwdParams& p, bool bf16, int cus, hipSt
 }
 
 hipError_t launch_column_sum(const float* partials, float* out, int64_t rows, int N, hipStream_t stream) {
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((N + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumSlices), 0, stream, partials, out, rows, N);
-  return hipGetLastError();
+  for (int64_t c = 0; c < N; c += kSumMostCols) {
+    const int n = (int)(N - c < kSumMostCols ? N - c : kSumMostCols);
+    hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((n + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumSlices), 0, stream, partials + c,
+                       out + c, rows, n, (int64_t)N);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace dg
