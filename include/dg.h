@@ -198,7 +198,9 @@ int dg_fp8_gemm_nt_acc(const uint8_t* A, const float* sfa, const uint8_t* B, con
 /*
  * Dense GEMM with bias, activation and residual: z = A . B^T + bias,
  * D = act(z) + residual, all in fp32 and rounded once to bf16 (the activations
- * are within 1e-4 of their values before that, where these are above 2^-118).
+ * are within 1e-4 of their values before that, where these are above 2^-118; an
+ * infinite z gives NaN where the formula has inf * 0: silu and gelu_tanh of
+ * -inf, and the slopes of silu and gelu).
  *   A, sfa, B, sfb, workspace as for dg_fp8_gemm_nt (same size query)
  *   bias     [N] fp32 or NULL      act  one of DG_ACT_*
  *   residual [M,N] bf16 or NULL; may equal D (in place)

@@ -54,10 +54,11 @@
 // Epilogue form: bias, activation and residual are applied to the fp32
 // accumulators, which are rounded once; the kept product (pre) is stored from
 // the same registers.  The residual is loaded a 64-column half at a time (all
-// of a tile's at once spilled).  4096 x 4096 x 7168 98.3 us plain: bias 98-101,
-// silu 99, gelu 103, gelu and pre 105, residual too 112; 4095 x 7168 x 2048,
-// two rounds of tiles, 57-67 plain, with bias and residual 70-74: the 59 MB of
-// the residual arrive when the tiles end, and nothing overlaps them there.
+// of a tile's at once spilled).  4096 x 4096 x 7168 100-105 us plain: bias
+// 101-105, silu 102-105, gelu_tanh 103-106, relu 105-110, gelu 110-113, gelu and
+// pre 114-116, residual too 120-122; 4095 x 7168 x 2048, two rounds of tiles,
+// 57-67 plain, with bias and residual 76-80: the 59 MB of the residual arrive
+// when the tiles end, and nothing overlaps them there.
 //
 // K-grouped form (MoE weight gradient, fp32 D[g] = C[g] + A[:, seg g] .
 // B[:, seg g]^T): every workgroup reads the group lengths on the device and

@@ -7,9 +7,14 @@
 // sums; the block scales are applied to each 128-deep product.  h is rounded to
 // bf16 once, as the matrix cores take it; y once at the end.
 //
-// Bound by the weights of the experts that were chosen, which are read once,
-// straight into registers: no two waves share a weight, so staging them in LDS
-// would only add a hop.  An instruction loads whole cache lines, 8 rows of 128
+// Bound by the weights of the experts that were chosen, which are read straight
+// into registers: no two waves share a weight, so staging them in LDS would only
+// add a hop.  They are read once for as many tokens of an expert as share a pass:
+// gate and up 16 (calls of up to 16 tokens) or 32; down 8, 16 or 32, one size
+// for the whole call by the tokens an expert has on average.  So an expert of
+// many tokens among cold ones is read more than once (64 tokens x 2 of 32, 4096
+// x 2048 e4m3: 133 us even, 143 with one expert of 32 tokens, 154 with one of 64;
+// e2m1 96, 103, 115).  An instruction loads whole cache lines, 8 rows of 128
 // bytes, streamed past the caches (8 rows x 128 bytes 6.3 TB/s of 224 MB,
 // 16 rows x 64 bytes, where a line is taken in two halves, 5.1).  So a lane has
 // 16 bytes (a chunk) of one of 8 rows, row lane % 8, chunk lane / 16 + 4 (lane /
@@ -25,8 +30,10 @@
 // e2m1 (430 MB of the 17 to 19 that were chosen) 77-103 us, where a step's four
 // loads of activations and two of scales keep the data path behind the address
 // units busy 0.9 of the cycles; 64 tokens x 2 of 8, 4096 x 2048 e4m3 (202 MB)
-// 54-63 us, busy 0.8: the activations, read from the L2 caches by every workgroup
-// that needs them, take as long as the weights; one token, 4 of 16 experts, 1024
+// 53-67 us, busy 0.8: the activations, read from the L2 caches by every workgroup
+// that needs them, take as long as the weights, e2m1 (107 MB) 42-45; 1, 8 and 16
+// tokens x 8 of 64, 7168 x 2048 e2m1 (187, 983 and 1217 MB) 50, 199 and 247 us,
+// 3.8-4.9 TB/s, e4m3 of 8 and 16 tokens 6.7 and 6.3; one token, 4 of 16 experts, 1024
 // x 512 (6 MB) 11.4 us, two launches and the order of the choices.
 
 #include "activation.hpp"
@@ -154,7 +161,10 @@ __device__ __forceinline__ int entries_of(const ExpertsTable& s) {
 }
 
 constexpr int kUpThreads = 256;
-constexpr int kPairTokens = 6;  // tokens of an expert on average from which neighbouring units are taken together
+// Tokens of an expert on average past which neighbouring units are taken together, in both kernels.  64 tokens, 4096 x 2048, every
+// expert as many, apart and together: e4m3 of 32 experts with 4 tokens 132.6 and 137.4 us, 6: 135.8 and 138.7, 8: 141.2 and 140.1,
+// 10: 183 and 142; e2m1 91 and 86, 103 and 92, 118 and 101, 148 and 102
+constexpr int kPairTokens = 6;
 
 __device__ __forceinline__ void read_members(const ExpertsParams& p, Members& s) {
   constexpr int EACH = kExpertsMaxChoices / kUpThreads;
@@ -839,6 +849,8 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
   const int slot = split * W + wave, slots = W * splits;
   if (!wide) down_run<FMT, 1, 1, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   if constexpr (!FEW) {
+    // (16 tokens a pass against 32, e4m3: 8 of an expert 140.1 and 143.6 us, 12: 81.4 and 81.5, 24: 59.3 and 51.0; e2m1 100.7 and
+    // 107, 61.1 and 62.1, 49.8 and 45.0)
     if (wide && entries <= 12 * chosen) down_run<FMT, 2, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
     else if (wide) down_run<FMT, 4, 2, FEW, NT>(p, s, sums[wave], spread_s[wave], c0, slot, slots);
   }
@@ -913,6 +925,7 @@ __global__ void __launch_bounds__(64 * kDownWaves<FEW>, FEW ? 4 : 2) experts_dow
 template <int FMT, bool NT>
 hipError_t launch_format(const ExpertsParams& p, int cus, hipStream_t stream) {
   const int64_t most = (int64_t)(p.G < p.T * p.k ? p.G : p.T * p.k) * (p.I / 16);  // units, where every choice names another expert
+  // workgroups a CU: what the registers let be there at once, but for e2m1 of up to 16 tokens, whose 191 hold two of the three
   const int64_t room = (int64_t)(p.T <= 16 ? 3 : 2) * cus;
   const dim3 up((unsigned)(most < room ? most : room));
   if (p.T <= 16) hipLaunchKernelGGL((experts_up_kernel<FMT, 2, NT>), up, dim3(kUpThreads), 0, stream, p);
