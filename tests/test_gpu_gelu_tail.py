@@ -44,3 +44,19 @@ def test_the_sigmoids_are_right_relative_to_their_values(kind, low):
     want = v / (1.0 + np.exp(-(v if kind == "silu" else 2 * math.sqrt(2 / math.pi) * (v + 0.044715 * v**3))))
     bad = ~(np.abs(D.double().cpu().numpy() - want) <= (2.0**-8 + 1e-4) * np.abs(want))
     assert not bad.any(), (int(bad.sum()), z[np.argwhere(bad)[:, 1]].min(), z[np.argwhere(bad)[:, 1]].max())
+
+
+def test_infinities():
+    # the limit where the formula has one without inf * 0, else NaN
+    inf = float("inf")
+    z = torch.tensor([-inf, inf] * 8, device=DEV)
+    A, B = (torch.zeros(n, 128, dtype=torch.uint8, device=DEV) for n in (1, 16))
+    D, dz = (torch.empty(1, 16, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    one, pre = torch.ones(1, 1, device=DEV), z.to(torch.bfloat16)[None].contiguous()
+    for kind, low, slopes in (("none", -inf, (1, 1)), ("relu", 0, (0, 1)), ("silu", None, None), ("gelu", 0, None), ("gelu_tanh", None, (0, 1))):
+        dg.dg_fp8_gemm_nt_epilogue(A, one, B, one, D, bias=z, act=kind)
+        got = D.float()[0].tolist()
+        assert all(v == inf for v in got[1::2]) and all(v != v if low is None else v == low for v in got[::2]), kind
+        dg.dg_epilogue_bwd(torch.ones_like(pre), dz, pre=pre, act=kind)
+        got = dz.float()[0].tolist()
+        assert all(v != v for v in got) if slopes is None else (got == list(slopes) * 8), kind
