@@ -461,10 +461,12 @@ __global__ void __launch_bounds__(512) fp8_gemm_wide_kernel(GemmParams p) {
 #define WD_PUT(i_, h_, w_, rsrc_) /* eight packed words of the lane's run, through this wave's 2 KB of LDS */   \
   do {                                                                                                     \
     const int ra_ = st_row0 + wm * 64 + (i_) * 16 + sr_;                                                   \
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); /* the last reads of the 2 KB */       \
     *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q) ^ (q16 & 7)) << 4)) =                           \
         uint4{w_[0], w_[1], w_[2], w_[3]};                                                                 \
     *reinterpret_cast<uint4*>(stg_ + q16 * 128 + (((2 * q + 1) ^ (q16 & 7)) << 4)) =                       \
         uint4{w_[4], w_[5], w_[6], w_[7]};                                                                 \
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); /* other lanes' words, below */        \
     const uint4 va_ = *reinterpret_cast<const uint4*>(stg_ + sr_ * 128 + ((sc_ ^ sr_) << 4));              \
     const uint4 vb_ = *reinterpret_cast<const uint4*>(stg_ + (8 + sr_) * 128 + ((sc_ ^ sr_) << 4));        \
     const int c_ = st_col0 + wn * 128 + (h_) * 64 + sc_ * 8;                                               \
