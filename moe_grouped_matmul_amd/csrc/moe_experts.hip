@@ -720,6 +720,7 @@ __device__ __forceinline__ void down_run(const ExpertsParams& p, const ExpertsTa
     };
     // the accumulators into the sums: of 8 tokens lanes (token r8, q < 2) of the lower half have columns 8 q + 2 e + a
     auto flush = [&]() {
+      wave_fence();  // a token's sums may be another lane's from the expert before
       if constexpr (MG == 1) {
         const f32x4 x = halves(acc[0][0]), y = halves(acc[0][1]);
         if (to[0] >= 0 && !half && q < 2) {
